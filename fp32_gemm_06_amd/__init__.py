@@ -21,6 +21,7 @@ _lib = None
 
 KIND_SGEMM = 0
 KIND_SGEMV = 1
+KIND_S8GEMM = 2
 ERR_CONFIG = -100
 ERR_SCRATCH = -101
 
@@ -46,6 +47,17 @@ _SPLITK_ARGTYPES = _EX_ARGTYPES[:-1] + [ctypes.c_int, ctypes.c_void_p, ctypes.c_
 _SPLITK_NOALLOC_ARGTYPES = _EX_ARGTYPES[:-1] + [ctypes.c_int, ctypes.c_void_p]
 _STREAMK_ARGTYPES = _EX_ARGTYPES[:-1] + [ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]
 
+TYPE_F32 = 0
+TYPE_F16 = 1
+TYPE_BF16 = 2
+_S8GEMM_ARGTYPES = [ctypes.c_int] * 3 + [ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p] * 2 + [
+    ctypes.c_float, ctypes.c_int, ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p, ctypes.c_int,
+    ctypes.c_void_p]
+_S8_QUANTIZE_ARGTYPES = [ctypes.c_int] * 4 + [ctypes.c_void_p, ctypes.c_int] * 2 + [
+    ctypes.c_void_p] * 2
+_S8_RMSNORM_ARGTYPES = [ctypes.c_int] * 3 + [ctypes.c_void_p, ctypes.c_int] * 3 + [
+    ctypes.c_void_p, ctypes.c_float, ctypes.c_void_p, ctypes.c_int] + [ctypes.c_void_p] * 2
+
 # Every symbol include/fp32gemm.h declares.
 EXPORTS = ("sgemm", "sgemv", "sgemm_ex", "sgemm_strided_batched", "sgemm_fused", "sgemm_splitk",
            "sgemm_splitk_noalloc", "sgemm_splitk_workspace_size", "fp32gemm_splitk_splits",
@@ -53,7 +65,8 @@ EXPORTS = ("sgemm", "sgemv", "sgemm_ex", "sgemm_strided_batched", "sgemm_fused",
            "fp32gemm_streamk_plan", "fp32gemm_streamk_with_config", "fp32gemm_strerror",
            "fp32gemm_num_configs", "fp32gemm_config_name", "fp32gemm_select_config",
            "fp32gemm_config_max_rows", "fp32gemm_round_split", "fp32gemm_sgemm_with_config",
-           "fp32gemm_sgemv_with_config")
+           "fp32gemm_sgemv_with_config", "s8gemm", "s8_quantize", "s8_rmsnorm",
+           "fp32gemm_s8gemm_with_config")
 
 
 class Fp32GemmError(RuntimeError):
@@ -118,6 +131,14 @@ def lib():
         L.fp32gemm_sgemm_with_config.restype = ctypes.c_int
         L.fp32gemm_sgemv_with_config.argtypes = [ctypes.c_int] + _GEMM_ARGTYPES
         L.fp32gemm_sgemv_with_config.restype = ctypes.c_int
+        L.s8gemm.argtypes = _S8GEMM_ARGTYPES
+        L.s8gemm.restype = ctypes.c_int
+        L.s8_quantize.argtypes = _S8_QUANTIZE_ARGTYPES
+        L.s8_quantize.restype = ctypes.c_int
+        L.s8_rmsnorm.argtypes = _S8_RMSNORM_ARGTYPES
+        L.s8_rmsnorm.restype = ctypes.c_int
+        L.fp32gemm_s8gemm_with_config.argtypes = [ctypes.c_int] + _S8GEMM_ARGTYPES
+        L.fp32gemm_s8gemm_with_config.restype = ctypes.c_int
         _lib = L
     return _lib
 
@@ -245,6 +266,34 @@ def fp32gemm_sgemv_with_config(cfg, M, N, K, alpha, A, lda, B, ldb, beta, C, ldc
                                stream=None) -> int:
     return lib().fp32gemm_sgemv_with_config(cfg, M, N, K, alpha, _addr(A), lda, _addr(B), ldb,
                                             beta, _addr(C), ldc, _stream(stream))
+
+
+def s8gemm(M, N, K, A, lda, scaleA, B, ldb, scaleB, beta, type, C, ldc, bias=None, act=ACT_NONE,
+           stream=None) -> int:
+    """C <- act(scaleA scaleB (A B^T) + beta C + bias) on 8-bit codes, A M x K
+    and B N x K; C of ``type`` (TYPE_F32, TYPE_F16, TYPE_BF16)."""
+    return lib().s8gemm(M, N, K, _addr(A), lda, _addr(scaleA), _addr(B), ldb, _addr(scaleB), beta,
+                        type, _addr(C), ldc, _addr(bias), act, _stream(stream))
+
+
+def s8_quantize(trans, M, K, type, X, ldx, Q, ldq, scales, stream=None) -> int:
+    """8-bit codes and scales of the M rows of op(X) (op = identity or transpose)."""
+    return lib().s8_quantize(trans, M, K, type, _addr(X), ldx, _addr(Q), ldq, _addr(scales),
+                             _stream(stream))
+
+
+def s8_rmsnorm(M, K, type, X, ldx, R, ldr, H, ldh, W, eps, Q, ldq, scales, stream=None) -> int:
+    """H <- X + R, and the 8-bit codes and scales of rmsnorm(H) * W; R and H
+    may be None."""
+    return lib().s8_rmsnorm(M, K, type, _addr(X), ldx, _addr(R), ldr, _addr(H), ldh, _addr(W), eps,
+                            _addr(Q), ldq, _addr(scales), _stream(stream))
+
+
+def fp32gemm_s8gemm_with_config(cfg, M, N, K, A, lda, scaleA, B, ldb, scaleB, beta, type, C, ldc,
+                                bias=None, act=ACT_NONE, stream=None) -> int:
+    return lib().fp32gemm_s8gemm_with_config(cfg, M, N, K, _addr(A), lda, _addr(scaleA), _addr(B),
+                                             ldb, _addr(scaleB), beta, type, _addr(C), ldc,
+                                             _addr(bias), act, _stream(stream))
 
 
 def fp32gemm_strerror(code: int) -> str:

@@ -6,7 +6,7 @@
 #include <mutex>
 
 #include "../../include/fp32gemm.h"
-#include "common.h"
+#include "s8_common.h"
 
 using namespace fp32gemm;
 
@@ -249,6 +249,44 @@ int streamk_call(int tile, int groups, int base, int transA, int transB, int M, 
   if (workspace_bytes < streamk_workspace_bytes(plan)) return -(15 + off);
   return (int)launch_streamk(transA, transB, a, plan, workspace, s);
 }
+
+// ---- 8-bit linear layer ------------------------------------------------------
+// Longest K of s8gemm: 131071 products of two codes, at most 2^14 each, stay
+// inside 32 bits.
+constexpr int kMaxS8K = 131071;
+
+int type_size(int type) { return type == kTypeF32 ? 4 : 2; }
+bool known_type(int type) { return type == kTypeF32 || type == kTypeF16 || type == kTypeBf16; }
+bool misaligned(const void *p, int size) { return (uintptr_t)p % (uintptr_t)size != 0; }
+
+int s8gemm_call(int cfg, int base, int M, int N, int K, const signed char *A, int lda,
+                const float *scaleA, const signed char *B, int ldb, const float *scaleB, float beta,
+                int type, void *C, int ldc, const float *bias, int act, hipStream_t s) {
+  const int off = base - 1;  // `base`: the 1-based position of M
+  if (M < 0) return -(1 + off);
+  if (N < 0) return -(2 + off);
+  if (K < 0 || K > kMaxS8K) return -(3 + off);
+  if (lda < imax(1, K) || lda > kMaxLd) return -(5 + off);
+  if (ldb < imax(1, K) || ldb > kMaxLd) return -(8 + off);
+  if (!known_type(type)) return -(11 + off);
+  if (ldc < imax(1, N) || ldc > kMaxLd) return -(13 + off);
+  if (act != FP32GEMM_ACT_NONE && act != FP32GEMM_ACT_RELU) return -(15 + off);
+  const bool work = M > 0 && N > 0, reads = work && K > 0;
+  if (reads && A == nullptr) return -(4 + off);
+  if (reads && (scaleA == nullptr || misaligned(scaleA, 4))) return -(6 + off);
+  if (reads && B == nullptr) return -(7 + off);
+  if (reads && (scaleB == nullptr || misaligned(scaleB, 4))) return -(9 + off);
+  if (work && (C == nullptr || misaligned(C, type_size(type)))) return -(12 + off);
+  if (work && misaligned(bias, 4)) return -(14 + off);
+  if (!work) return 0;
+  const S8Args a = {M, N, K, A, B, scaleA, scaleB, beta, type, C, lda, ldb, ldc, bias,
+                    act == FP32GEMM_ACT_RELU ? kActRelu : kActNone};
+  if (K == 0) {
+    const bool noop = beta == 1.0f && bias == nullptr && act == FP32GEMM_ACT_NONE;
+    return noop ? 0 : (int)launch_s8_epilogue_only(a, s);
+  }
+  return (int)launch_s8(cfg, a, s);
+}
 }  // namespace
 
 #pragma GCC visibility push(default)
@@ -405,6 +443,65 @@ int fp32gemm_streamk_with_config(int tile, int groups, int transA, int transB, i
                       true);
 }
 
+int s8_quantize(int trans, int M, int K, int type, const void *X, int ldx, signed char *Q, int ldq,
+                float *scales, fp32gemm_stream_t stream) {
+  if (trans != FP32GEMM_OP_N && trans != FP32GEMM_OP_T) return -1;
+  if (M < 0) return -2;
+  if (K < 0) return -3;
+  if (!known_type(type)) return -4;
+  if (ldx < imax(1, trans ? M : K) || ldx > kMaxLd) return -6;
+  if (ldq < imax(1, K) || ldq > kMaxLd) return -8;
+  if (M > 0 && K > 0 && (X == nullptr || misaligned(X, type_size(type)))) return -5;
+  if (M > 0 && K > 0 && Q == nullptr) return -7;
+  if (M > 0 && (scales == nullptr || misaligned(scales, 4))) return -9;
+  if (M == 0) return 0;
+  const S8RowArgs a = {M, K, X, ldx, nullptr, 0, nullptr, 0, nullptr, 0.0f, Q, ldq, scales};
+  const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  return (int)(trans ? launch_s8_columns(a, type, s) : launch_s8_rows(a, type, s));
+}
+
+int s8_rmsnorm(int M, int K, int type, const void *X, int ldx, const void *R, int ldr, void *H,
+               int ldh, const void *W, float eps, signed char *Q, int ldq, float *scales,
+               fp32gemm_stream_t stream) {
+  if (M < 0) return -1;
+  if (K < 0) return -2;
+  if (!known_type(type)) return -3;
+  const int size = type_size(type);
+  if (ldx < imax(1, K) || ldx > kMaxLd) return -5;
+  if (R != nullptr && (ldr < imax(1, K) || ldr > kMaxLd)) return -7;
+  if (H != nullptr && (ldh < imax(1, K) || ldh > kMaxLd)) return -9;
+  if (!(eps >= 0.0f) || eps > 3.4028235e38f) return -11;
+  if (ldq < imax(1, K) || ldq > kMaxLd) return -13;
+  const bool work = M > 0 && K > 0;
+  if (work && (X == nullptr || misaligned(X, size))) return -4;
+  if (work && misaligned(R, size)) return -6;
+  if (work && misaligned(H, size)) return -8;
+  // in place is element by element: the sum over X or R, with the same rows
+  if (work && H != nullptr && ((H == X && ldh != ldx) || (H == R && ldh != ldr))) return -9;
+  if (work && (W == nullptr || misaligned(W, size))) return -10;
+  if (work && Q == nullptr) return -12;
+  if (M > 0 && (scales == nullptr || misaligned(scales, 4))) return -14;
+  if (M == 0) return 0;
+  const S8RowArgs a = {M, K, X, ldx, R, ldr, H, ldh, W, eps, Q, ldq, scales};
+  return (int)launch_s8_rows(a, type, reinterpret_cast<hipStream_t>(stream));
+}
+
+int s8gemm(int M, int N, int K, const signed char *A, int lda, const float *scaleA,
+           const signed char *B, int ldb, const float *scaleB, float beta, int type, void *C,
+           int ldc, const float *bias, int act, fp32gemm_stream_t stream) {
+  return s8gemm_call(-1, 1, M, N, K, A, lda, scaleA, B, ldb, scaleB, beta, type, C, ldc, bias, act,
+                     reinterpret_cast<hipStream_t>(stream));
+}
+
+int fp32gemm_s8gemm_with_config(int cfg, int M, int N, int K, const signed char *A, int lda,
+                                const float *scaleA, const signed char *B, int ldb,
+                                const float *scaleB, float beta, int type, void *C, int ldc,
+                                const float *bias, int act, fp32gemm_stream_t stream) {
+  if (cfg < -1 || cfg >= s8_num_configs()) return FP32GEMM_ERR_CONFIG;
+  return s8gemm_call(cfg, 2, M, N, K, A, lda, scaleA, B, ldb, scaleB, beta, type, C, ldc, bias, act,
+                     reinterpret_cast<hipStream_t>(stream));
+}
+
 const char *fp32gemm_strerror(int code) {
   static const char *const bad[] = {
       "invalid argument 1",  "invalid argument 2",  "invalid argument 3",
@@ -432,6 +529,7 @@ int fp32gemm_num_configs(int kind) {
     (void)gemv_configs(&n);
     return n;
   }
+  if (kind == 2) return s8_num_configs();
   return 0;
 }
 
@@ -442,12 +540,14 @@ const char *fp32gemm_config_name(int kind, int cfg) {
     const GemvConfig *c = gemv_configs(&n);
     return (cfg >= 0 && cfg < n) ? c[cfg].name : nullptr;
   }
+  if (kind == 2) return s8_config_name(cfg);
   return nullptr;
 }
 
 int fp32gemm_select_config(int kind, int M, int N, int K) {
   if (kind == 0) return select_gemm_config(M, N, K, 1);
   if (kind == 1) return select_gemv_config(M, N, K);
+  if (kind == 2) return select_s8_config(M, N, K);
   return FP32GEMM_ERR_CONFIG;
 }
 
@@ -458,6 +558,7 @@ int fp32gemm_config_max_rows(int kind, int cfg) {
     return (cfg >= 0 && cfg < n) ? c[cfg].max_rows : -1;
   }
   if (kind == 0) return (cfg >= 0 && cfg < num_gemm_config_ids()) ? 0x7fffffff : -1;
+  if (kind == 2) return (cfg >= 0 && cfg < s8_num_configs()) ? 0x7fffffff : -1;
   return -1;
 }
 

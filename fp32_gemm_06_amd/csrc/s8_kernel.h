@@ -1,0 +1,376 @@
+// C <- act(sA_i sB_j (A B^T)_ij + beta C_ij + bias_j) for 8-bit codes, on the
+// integer matrix cores: A is M x K, B is N x K (a linear layer's weight), both
+// with k contiguous.  The products of codes and their sums are exact in 32
+// bits (K is at most 131071), so every split of K gives the same C.
+//
+// A workgroup owns a BM x BN tile of C and walks K in stages of KS slices of
+// 128 bytes; two stages' LDS buffers, the next one in flight during this one.
+//
+// LDS.  A slice is a row of eight 16-byte chunks for each row of the operand,
+// chunk c of row p at position c ^ swizzle(p), which spreads the rows that one
+// ds_read_b128 reads at the same chunk over the banks.  The 128-bit path
+// writes it with buffer loads straight into LDS; the other path loads through
+// registers, at any alignment, into the same places.
+//
+// Matrix cores.  The weight's rows are the instruction's rows and A's rows its
+// columns, so a lane ends up with several n of one m: C is row-major, and
+// those are next to each other in it.  Which n they are is ours to choose by
+// where a row of B is put in LDS: row r of block j of a wave's columns is put
+// so that a lane's registers, over all its blocks, hold WN / 4 (16 x 16
+// blocks) or WN / 2 (32 x 32) consecutive columns, a whole 16-byte store or
+// several.
+//
+// K need not be a multiple of 16 on the 128-bit path: the last chunk of a row
+// of A is cleared past K in LDS, and what B's holds there meets zeros.
+#pragma once
+
+#include "s8_common.h"
+
+namespace fp32gemm {
+namespace {
+
+template <int BM_, int BN_, int WM_, int WN_, int MF_, int KS_>
+struct S8Tile {
+  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, MF = MF_, KS = KS_;
+  static constexpr int WAVES_N = BN / WN;
+  static constexpr int WT = (BM / WM) * WAVES_N;  // waves per K group
+  static constexpr int WAVES = WT * KS;
+  static constexpr int NT = WAVES * 64;
+  static constexpr int TM = WM / MF, TN = WN / MF;
+  static constexpr int NV = MF == 32 ? 16 : 4;     // accumulator registers of a block
+  static constexpr int STEPS = MF == 32 ? 4 : 2;   // instructions a block takes per slice
+  static constexpr int LQ = 64 / MF;               // lanes with the same row of a block
+  static constexpr int SLICE = (BM + BN) * 128;    // bytes
+  static constexpr int STAGE = SLICE * KS;
+  static constexpr int NIA = KS * BM / 8 / WAVES;  // 1 KB loads per wave per stage
+  static constexpr int NIB = KS * BN / 8 / WAVES;
+  static_assert(MF == 16 || MF == 32, "16x16x64 or 32x32x32 blocks");
+  static_assert(BM % WM == 0 && BN % WN == 0 && WM % MF == 0 && WN % MF == 0, "wave tiling");
+  static_assert(KS * BM / 8 % WAVES == 0 && KS * BN / 8 % WAVES == 0, "whole loads per wave");
+  static_assert(2 * STAGE <= 160 * 1024, "LDS of a CU");
+  static_assert((KS - 1) * BM * BN * 4 <= 2 * STAGE, "the K groups' sums fit in the buffers");
+};
+
+__device__ __forceinline__ int s8_swizzle(int row) { return (row & 7) ^ ((row >> 3) & 1); }
+
+// The column, within a wave's WN, of LDS row `pl` of them.
+template <class T> __device__ __forceinline__ int s8_column(int pl) {
+  const int j = pl / T::MF, r = pl % T::MF;
+  if constexpr (T::MF == 16) return (r >> 2) * (4 * T::TN) + j * 4 + (r & 3);
+  else return ((r >> 2) & 1) * (16 * T::TN) + j * 16 + (r >> 3) * 4 + (r & 3);
+}
+
+__device__ __forceinline__ void s8_dma16(__amdgpu_buffer_rsrc_t rs, char *dst, uint32_t off, int soff) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  typedef __attribute__((address_space(3))) void lds_void_t;
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void_t *)dst, 16, off, soff, 0, 0);
+#else
+  (void)rs; (void)dst; (void)off; (void)soff;
+#endif
+}
+
+// 16 codes from any address, the last 16 - valid of them zero and not read.
+__device__ __forceinline__ intx4 s8_load16(const int8_t *p, int valid) {
+  intx4 v = {0, 0, 0, 0};
+  if (valid >= 16) {
+    __builtin_memcpy(&v, p, 16);
+  } else if (valid > 0) {
+#pragma unroll
+    for (int e = 0; e < 15; ++e)
+      if (e < valid) v[e / 4] |= (int)(uint8_t)p[e] << (8 * (e % 4));
+  }
+  return v;
+}
+
+// What is left to do with the sums of one lane's row: scales, C, bias,
+// activation, rounding to C's type (once, from 32 bits).
+template <class F, int CW>
+__device__ __forceinline__ void s8_store_row(const S8Args &a, F *c, const float *sb, const float *bias,
+                                             int cols, float sa, const int (&acc)[CW], bool wide) {
+  constexpr int G = sizeof(F) == 2 && CW % 8 == 0 ? 8 : 4;  // 16 bytes, or 8
+#pragma unroll
+  for (int t = 0; t < CW; t += G) {
+    if (t >= cols) break;
+    F out[G];
+    const bool whole = wide && t + G <= cols;
+    F c0[G];
+    if (a.beta != 0.0f) {
+      if (whole) {
+        __builtin_memcpy(c0, __builtin_assume_aligned(c + t, G * sizeof(F)), sizeof(c0));
+      } else {
+#pragma unroll
+        for (int e = 0; e < G; ++e) c0[e] = t + e < cols ? c[t + e] : (F)0.0f;
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < G; ++e) {
+      const bool in = t + e < cols;
+      float v = (float)acc[t + e] * sa * (in ? sb[t + e] : 0.0f);
+      if (a.beta != 0.0f) v += a.beta * (float)c0[e];
+      if (bias != nullptr) v += in ? bias[t + e] : 0.0f;
+      out[e] = (F)apply_act(v, a.act);
+    }
+    if (whole) {
+      __builtin_memcpy(__builtin_assume_aligned(c + t, G * sizeof(F)), out, sizeof(out));
+    } else {
+#pragma unroll
+      for (int e = 0; e < G; ++e)
+        if (t + e < cols) c[t + e] = out[e];
+    }
+  }
+}
+
+// Whether the lanes' groups of columns can be moved 16 (8) bytes at a time.
+__device__ __forceinline__ bool s8_wide_c(const S8Args &a) {
+  const int size = a.type == kTypeF32 ? 4 : 2;
+  return ((uintptr_t)a.C & 15) == 0 && (a.ldc * size & 15) == 0;
+}
+
+template <class T, bool DMA>
+__global__ void __launch_bounds__(T::NT) s8_kernel(S8Args a, int tiles_m, int tiles_n, int group_m) {
+  constexpr int BM = T::BM, BN = T::BN, KS = T::KS;
+  __shared__ __attribute__((aligned(16))) char lds[2 * T::STAGE];
+  const int tid = threadIdx.x;
+  const int lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int kg = wave / T::WT, wt = wave % T::WT;
+  const int wm = wt / T::WAVES_N, wn = wt % T::WAVES_N;
+
+  // Workgroups go to the 8 XCDs in turn; logical ids give each XCD a run of
+  // neighbouring tiles, in strips of group_m tile rows.
+  const int G = gridDim.x;
+  const int xcd = (int)blockIdx.x & 7;
+  const int lid = xcd * (G >> 3) + min(xcd, G & 7) + ((int)blockIdx.x >> 3);
+  const int strip = lid / (group_m * tiles_n);
+  const int gsz = min(tiles_m - strip * group_m, group_m);
+  const int within = lid - strip * group_m * tiles_n;
+  const int m0 = (strip * group_m + within % gsz) * BM;
+  const int n0 = (within / gsz) * BN;
+  const int rows = a.M - m0, cols = a.N - n0;
+  const int8_t *Ag = a.A + (size_t)m0 * a.lda;
+  const int8_t *Bg = a.B + (size_t)n0 * a.ldb;
+
+  const int nst = (a.K + 128 * KS - 1) / (128 * KS);
+  const int klast = a.K - (nst - 1) * 128 * KS;  // valid k of the last stage
+
+  // Lane l of load `inst` moves the chunk at position l % 8 of LDS row
+  // 8 inst + l / 8, counted over a slice's rows and then the stage's slices.
+  const int pos = lane & 7;
+  uint32_t offa[T::NIA], offb[T::NIB];
+  int cola[T::NIA], colb[T::NIB];
+  int rowa[T::NIA], rowb[T::NIB];
+#pragma unroll
+  for (int q = 0; q < T::NIA; ++q) {
+    const int f = (wave * T::NIA + q) * 8 + (lane >> 3);
+    rowa[q] = f % BM;
+    cola[q] = f / BM * 128 + 16 * (pos ^ s8_swizzle(f % BM));
+  }
+#pragma unroll
+  for (int q = 0; q < T::NIB; ++q) {
+    const int f = (wave * T::NIB + q) * 8 + (lane >> 3);
+    const int p = f % BN;
+    rowb[q] = p / T::WN * T::WN + s8_column<T>(p % T::WN);
+    colb[q] = f / BN * 128 + 16 * (pos ^ s8_swizzle(p));
+  }
+  auto set_offsets = [&](int kvalid) {
+#pragma unroll
+    for (int q = 0; q < T::NIA; ++q)
+      offa[q] = rowa[q] < rows && cola[q] < kvalid ? (uint32_t)(rowa[q] * a.lda + cola[q]) : kOob;
+#pragma unroll
+    for (int q = 0; q < T::NIB; ++q)
+      offb[q] = rowb[q] < cols && colb[q] < kvalid ? (uint32_t)(rowb[q] * a.ldb + colb[q]) : kOob;
+  };
+  // where a load goes: 1 KB a load, over the slices' operand areas
+  auto dst_a = [&](int q) -> int {
+    const int f = (wave * T::NIA + q) * 8;
+    return f / BM * T::SLICE + f % BM * 128;
+  };
+  auto dst_b = [&](int q) -> int {
+    const int f = (wave * T::NIB + q) * 8;
+    return f / BN * T::SLICE + BM * 128 + f % BN * 128;
+  };
+
+  const __amdgpu_buffer_rsrc_t rs_a = make_rsrc(Ag);
+  const __amdgpu_buffer_rsrc_t rs_b = make_rsrc(Bg);
+  intx4 sta[DMA ? 1 : T::NIA], stb[DMA ? 1 : T::NIB];
+  (void)sta;
+  (void)stb;
+  auto fetch = [&](char *buf, int st) {
+    const int k0 = st * 128 * KS;
+    if constexpr (DMA) {
+#pragma unroll
+      for (int q = 0; q < T::NIA; ++q) s8_dma16(rs_a, buf + dst_a(q), offa[q], k0);
+#pragma unroll
+      for (int q = 0; q < T::NIB; ++q) s8_dma16(rs_b, buf + dst_b(q), offb[q], k0);
+    } else {
+      (void)buf;
+      const int kvalid = a.K - k0;
+#pragma unroll
+      for (int q = 0; q < T::NIA; ++q)
+        sta[q] = s8_load16(Ag + (size_t)rowa[q] * a.lda + k0 + cola[q],
+                           rowa[q] < rows ? kvalid - cola[q] : 0);
+#pragma unroll
+      for (int q = 0; q < T::NIB; ++q)
+        stb[q] = s8_load16(Bg + (size_t)rowb[q] * a.ldb + k0 + colb[q],
+                           rowb[q] < cols ? kvalid - colb[q] : 0);
+    }
+  };
+  auto commit = [&](char *buf) {
+    if constexpr (!DMA) {
+#pragma unroll
+      for (int q = 0; q < T::NIA; ++q) *reinterpret_cast<intx4 *>(buf + dst_a(q) + 16 * lane) = sta[q];
+#pragma unroll
+      for (int q = 0; q < T::NIB; ++q) *reinterpret_cast<intx4 *>(buf + dst_b(q) + 16 * lane) = stb[q];
+    } else {
+      (void)buf;
+    }
+  };
+  // After the last stage has landed: the chunk of A's rows that K ends in.
+  auto clear_tail = [&](char *buf) {
+    if constexpr (DMA) {
+      if ((a.K & 15) == 0) return;
+      for (int p = tid; p < BM; p += T::NT) {
+        intx4 *c = reinterpret_cast<intx4 *>(buf + klast / 128 * T::SLICE + p * 128 +
+                                             16 * ((klast % 128 / 16) ^ s8_swizzle(p)));
+        intx4 v = *c;
+#pragma unroll
+        for (int d = 0; d < 4; ++d) {
+          const int keep = (klast & 15) - 4 * d;  // bytes of this word inside K
+          v[d] = keep >= 4 ? v[d] : keep <= 0 ? 0 : v[d] & (int)((1u << (8 * keep)) - 1);
+        }
+        *c = v;
+      }
+      __syncthreads();
+    } else {
+      (void)buf;
+    }
+  };
+
+  typedef int acc_t __attribute__((ext_vector_type(T::NV)));
+  acc_t acc[T::TM][T::TN];
+#pragma unroll
+  for (int i = 0; i < T::TM; ++i)
+#pragma unroll
+    for (int j = 0; j < T::TN; ++j) acc[i][j] = acc_t{};
+
+  const int lr = lane % T::MF, lq = lane / T::MF;
+  const int pa = wm * T::WM + lr, pb = wn * T::WN + lr;  // LDS rows of block 0
+  auto compute = [&](const char *buf) {
+    const char *As = buf + kg * T::SLICE, *Bs = As + BM * 128;
+#pragma unroll
+    for (int s = 0; s < T::STEPS; ++s) {
+      intx4 fa[T::TM], fb[T::TN];
+      const int c = s * T::LQ + lq;
+#pragma unroll
+      for (int i = 0; i < T::TM; ++i)
+        fa[i] = *reinterpret_cast<const intx4 *>(As + (pa + i * T::MF) * 128 +
+                                                 16 * (c ^ s8_swizzle(pa + i * T::MF)));
+#pragma unroll
+      for (int j = 0; j < T::TN; ++j)
+        fb[j] = *reinterpret_cast<const intx4 *>(Bs + (pb + j * T::MF) * 128 +
+                                                 16 * (c ^ s8_swizzle(pb + j * T::MF)));
+#pragma unroll
+      for (int i = 0; i < T::TM; ++i)
+#pragma unroll
+        for (int j = 0; j < T::TN; ++j) {
+          if constexpr (T::MF == 32)
+            acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fb[j], fa[i], acc[i][j], 0, 0, 0);
+          else
+            acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fb[j], fa[i], acc[i][j], 0, 0, 0);
+        }
+    }
+  };
+
+  set_offsets(nst == 1 ? klast : 128 * KS);
+  fetch(lds, 0);
+  commit(lds);
+  if constexpr (DMA) __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0)
+  __syncthreads();
+  if (nst == 1) clear_tail(lds);
+  for (int st = 0; st < nst; ++st) {
+    char *cur = lds + (st & 1) * T::STAGE, *nxt = lds + ((st + 1) & 1) * T::STAGE;
+    const bool more = st + 1 < nst;
+    if (more) {
+      if (st + 2 == nst) set_offsets(klast);
+      fetch(nxt, st + 1);
+    }
+    compute(cur);
+    if (more) commit(nxt);
+    if constexpr (DMA) __builtin_amdgcn_s_waitcnt(0x0F70);
+    __syncthreads();
+    if (st + 2 == nst) clear_tail(nxt);
+  }
+
+  // K groups 1.. leave their sums in LDS (free since the last barrier), group
+  // 0 adds them.
+  if constexpr (KS > 1) {
+    constexpr int PER = T::TM * T::TN * T::NV * 64;
+    int *red = reinterpret_cast<int *>(lds);
+    if (kg > 0) {
+      int *mine = red + ((kg - 1) * T::WT + wt) * PER + lane;
+#pragma unroll
+      for (int i = 0; i < T::TM; ++i)
+#pragma unroll
+        for (int j = 0; j < T::TN; ++j)
+#pragma unroll
+          for (int v = 0; v < T::NV; ++v) mine[((i * T::TN + j) * T::NV + v) * 64] = acc[i][j][v];
+    }
+    __syncthreads();
+    if (kg > 0) return;
+#pragma unroll
+    for (int g = 1; g < KS; ++g) {
+      const int *theirs = red + ((g - 1) * T::WT + wt) * PER + lane;
+#pragma unroll
+      for (int i = 0; i < T::TM; ++i)
+#pragma unroll
+        for (int j = 0; j < T::TN; ++j)
+#pragma unroll
+          for (int v = 0; v < T::NV; ++v) acc[i][j][v] += theirs[((i * T::TN + j) * T::NV + v) * 64];
+    }
+  }
+
+  // Epilogue: this lane's columns of each of its rows.
+  constexpr int CW = T::TN * T::NV;
+  const int nl = wn * T::WN + lq * CW;
+  const float *sb = a.sB + n0 + nl;
+  const float *bias = a.bias != nullptr ? a.bias + n0 + nl : nullptr;
+  const bool wide = s8_wide_c(a);
+#pragma unroll
+  for (int i = 0; i < T::TM; ++i) {
+    const int m = wm * T::WM + i * T::MF + lr;
+    if (m >= rows) continue;
+    int sums[CW];
+#pragma unroll
+    for (int j = 0; j < T::TN; ++j)
+#pragma unroll
+      for (int v = 0; v < T::NV; ++v) sums[j * T::NV + v] = acc[i][j][v];
+    const float sa = a.sA[m0 + m];
+    const size_t at = (size_t)(m0 + m) * a.ldc + n0 + nl;
+    if (a.type == kTypeF32)
+      s8_store_row<float, CW>(a, static_cast<float *>(a.C) + at, sb, bias, cols - nl, sa, sums, wide);
+    else if (a.type == kTypeF16)
+      s8_store_row<_Float16, CW>(a, static_cast<_Float16 *>(a.C) + at, sb, bias, cols - nl, sa, sums, wide);
+    else
+      s8_store_row<__bf16, CW>(a, static_cast<__bf16 *>(a.C) + at, sb, bias, cols - nl, sa, sums, wide);
+  }
+}
+
+// 16-byte loads of whole chunks: rows that start at multiples of 16 bytes.
+// The chunk that K ends in is read whole: lda and ldb are then multiples of
+// 16 and at least K, so it lies inside its row.
+inline bool s8_dma_ok(const S8Args &a) {
+  return (uintptr_t)a.A % 16 == 0 && (uintptr_t)a.B % 16 == 0 && a.lda % 16 == 0 && a.ldb % 16 == 0;
+}
+
+template <class T> hipError_t s8_launch(const S8Args &a, hipStream_t s) {
+  const int tm = (a.M + T::BM - 1) / T::BM, tn = (a.N + T::BN - 1) / T::BN;
+  const int group_m = 4;
+  if (s8_dma_ok(a))
+    s8_kernel<T, true><<<tm * tn, T::NT, 0, s>>>(a, tm, tn, group_m);
+  else
+    s8_kernel<T, false><<<tm * tn, T::NT, 0, s>>>(a, tm, tn, group_m);
+  return hipGetLastError();
+}
+
+}  // namespace
+}  // namespace fp32gemm

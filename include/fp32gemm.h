@@ -20,7 +20,7 @@
  *    owned by the caller.  The library keeps no reference after the call's
  *    kernels finish.  C must not overlap A or B.
  *  - Arithmetic: fp32 throughout (fp32 MFMA or fp32 FMA); no conversion to a
- *    narrower format.  The order of the k-sum is unspecified, so results may
+ *    narrower format (the s8 routines below say what theirs is).  The order of the k-sum is unspecified, so results may
  *    differ from a sequential loop by rounding.  Repeated calls with the same
  *    arguments and configuration give bit-identical results (no atomics on
  *    floats).
@@ -271,6 +271,97 @@ size_t sgemm_splitk_workspace_size(int M, int N, int K, int splits);
  * tiled kernel's rate for the enlarged grid plus the reduction's traffic. */
 int fp32gemm_splitk_splits(int M, int N, int K);
 
+/*
+ * The 8-bit linear layer: y = x W^T with x and W in 8-bit integer codes, a
+ * scale for each token (row of x) and one for each channel (row of W, stored
+ * N x K).  s8_quantize and s8_rmsnorm make codes and scales from floats;
+ * s8gemm multiplies them exactly in integers and returns floats.  W's codes
+ * are a quarter of its fp32 bytes, which is what a decode step's time is.
+ * A code c with scale s stands for the value c * s.
+ *
+ * The float operands (X, R, H, W of the norm, C) are fp32, fp16 or bf16, one
+ * type in a call; scales and bias are fp32.  Codes are signed char; those the
+ * library makes lie in -127 .. 127, s8gemm takes -128 too.  Any alignment of
+ * codes is accepted and any leading dimension up to 2^20; float operands are
+ * aligned to their type (an argument error otherwise).  Rows of codes that
+ * start at multiples of 16 bytes (base address and leading dimension) take
+ * 128-bit loads; there the up to 15 bytes that follow a row's K codes inside
+ * its leading dimension may be read, and their values do not matter.  Beyond that the
+ * conventions at the top of this file hold: asynchronous, no allocation, no
+ * workspace, results that are bit-identical from call to call, argument p
+ * invalid = -p and nothing enqueued.  Outputs must not overlap inputs, other
+ * than as s8_rmsnorm says.
+ */
+#define FP32GEMM_TYPE_F32 0
+#define FP32GEMM_TYPE_F16 1
+#define FP32GEMM_TYPE_BF16 2
+
+/*
+ * Codes and scales of the rows of op(X), M x K: X is M x K (ldx >= K) for
+ * FP32GEMM_OP_N, or stored K x M (ldx >= M) with op(X)[i][k] = X[k * ldx + i]
+ * for FP32GEMM_OP_T (a weight stored K x N gives the N x K codes that s8gemm
+ * reads).  Q is M x K (ldq >= K), scales has M values:
+ *
+ *   scales[i] = max_k |x_ik| / 127, rounded to fp32,
+ *   Q[i][k]   = x_ik / scales[i], rounded to the nearest integer, halves to
+ *               even, the quotient not rounded before.
+ *
+ * (In a row so small that its scale is subnormal or underflows to zero, codes
+ * past 127 become 127, and with a zero scale all are 0.)  A row that holds an
+ * infinity or a NaN gets the scale NaN and codes 0, so that the products of
+ * that row, and of no other, are NaN.  A row of zeros has scale 0; K == 0
+ * gives scale 0.  Bytes of Q past a row's K codes are left as they were.
+ * Argument positions for error codes: trans 1, M 2, K 3, type 4, X 5, ldx 6,
+ * Q 7, ldq 8, scales 9, stream 10.
+ */
+int s8_quantize(int trans, int M, int K, int type, const void *X, int ldx,
+                signed char *Q, int ldq, float *scales,
+                fp32gemm_stream_t stream);
+
+/*
+ * The residual stream's addition, the root-mean-square norm, and the codes of
+ * its result, row by row:
+ *
+ *   h_ik      = x_ik + r_ik, rounded to the operands' type (x_ik when R is
+ *               NULL); stored in H unless H is NULL,
+ *   v_ik      = h_ik * W[k], rounded to fp32,
+ *   step_i    = max_k |v_ik| / 127, rounded to fp32,
+ *   Q[i][k]   = v_ik / step_i, rounded as in s8_quantize,
+ *   scales[i] = step_i / sqrt(sum_k h_ik^2 / K + eps), rounded to fp32,
+ *
+ * so that Q * scales is rmsnorm(x + r) * W.  The norm divides a row by one
+ * number, which moves the scale and no code.  The sum of squares is kept in
+ * 64 bits.  H may be X or R itself (the same address and leading dimension)
+ * to update the residual stream in place; it must not overlap them otherwise.
+ * R's and H's leading dimensions are not looked at when they are NULL.  Rows
+ * with an infinity or a NaN, of zeros, or of no values, as in s8_quantize.
+ * Argument positions for error codes: M 1, K 2, type 3, X 4, ldx 5, R 6,
+ * ldr 7, H 8, ldh 9, W 10, eps 11 (negative or not finite), Q 12, ldq 13,
+ * scales 14, stream 15.
+ */
+int s8_rmsnorm(int M, int K, int type, const void *X, int ldx, const void *R,
+               int ldr, void *H, int ldh, const void *W, float eps,
+               signed char *Q, int ldq, float *scales,
+               fp32gemm_stream_t stream);
+
+/*
+ * C[i][j] <- act(scaleA[i] * scaleB[j] * sum_k A[i][k] B[j][k]
+ *                + beta * C[i][j] + bias[j]),
+ * A the M x K codes of the tokens (lda >= K), B the N x K codes of the weight
+ * (ldb >= K), C M x N of `type`.  The sum is exact; it is rounded to fp32,
+ * scaled and added to in fp32, and rounded once to C's type.  bias (N fp32
+ * values) may be NULL; act is FP32GEMM_ACT_NONE or FP32GEMM_ACT_RELU (as in
+ * sgemm_fused).  When beta == 0, C is not read.  K <= 131071, which keeps
+ * every sum inside 32 bits; K == 0 reads neither codes nor scales.  M == 0 or
+ * N == 0 does nothing.  Argument positions for error codes: M 1, N 2, K 3,
+ * A 4, lda 5, scaleA 6, B 7, ldb 8, scaleB 9, beta 10, type 11, C 12, ldc 13,
+ * bias 14, act 15, stream 16.
+ */
+int s8gemm(int M, int N, int K, const signed char *A, int lda,
+           const float *scaleA, const signed char *B, int ldb,
+           const float *scaleB, float beta, int type, void *C, int ldc,
+           const float *bias, int act, fp32gemm_stream_t stream);
+
 /* Human-readable text for a return code (static storage, never NULL). */
 const char *fp32gemm_strerror(int code);
 
@@ -281,7 +372,8 @@ const char *fp32gemm_strerror(int code);
  * enumerated, each candidate is timed on the target GPU, and the fastest per
  * shape goes into a table, because the best choice differs between GPUs.
  * The tuner (fp32_gemm_06_amd/tune.py) drives the sweep through these calls.
- * kind 0 = the SGEMM kernel family, kind 1 = the GEMV family.
+ * kind 0 = the SGEMM kernel family, kind 1 = the GEMV family, kind 2 = the
+ * 8-bit product (s8gemm; any M on any of its configurations).
  * Configurations are numbered 0 .. fp32gemm_num_configs(kind)-1 and named by
  * fp32gemm_config_name (NULL for an unknown id); an unknown kind gives 0
  * configurations, NULL names and FP32GEMM_ERR_CONFIG selections.
@@ -289,11 +381,12 @@ const char *fp32gemm_strerror(int code);
 int fp32gemm_num_configs(int kind);
 const char *fp32gemm_config_name(int kind, int cfg);
 
-/* The configuration sgemm()/sgemv() would pick for this shape (kind as above). */
+/* The configuration sgemm()/sgemv()/s8gemm() would pick for this shape (kind as above). */
 int fp32gemm_select_config(int kind, int M, int N, int K);
 
 /* The largest M a configuration runs (kind as above; -1 for an unknown id):
- * 8, 32, 64 or 128 for the GEMV family, INT_MAX for the tiled family. */
+ * 8, 32, 64 or 128 for the GEMV family, INT_MAX for the tiled family and the
+ * 8-bit product. */
 int fp32gemm_config_max_rows(int kind, int cfg);
 
 /* Whether the tiled kernel runs this product (batch entries of M x N x K) as
@@ -318,6 +411,16 @@ int fp32gemm_sgemv_with_config(int cfg, int M, int N, int K, float alpha,
                                const float *A, int lda, const float *B,
                                int ldb, float beta, float *C, int ldc,
                                fp32gemm_stream_t stream);
+
+/* s8gemm with a forced configuration (cfg = -1 picks as s8gemm does); error
+ * positions as s8gemm shifted by one (FP32GEMM_ERR_CONFIG for an unknown
+ * id). */
+int fp32gemm_s8gemm_with_config(int cfg, int M, int N, int K,
+                                const signed char *A, int lda,
+                                const float *scaleA, const signed char *B,
+                                int ldb, const float *scaleB, float beta,
+                                int type, void *C, int ldc, const float *bias,
+                                int act, fp32gemm_stream_t stream);
 
 /*
  * Stream-K tuning and testing hooks.  Tiles are numbered 0 ..
