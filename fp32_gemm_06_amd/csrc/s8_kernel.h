@@ -14,11 +14,10 @@
 //
 // Matrix cores.  The weight's rows are the instruction's rows and A's rows its
 // columns, so a lane ends up with several n of one m: C is row-major, and
-// those are next to each other in it.  Which n they are is ours to choose by
-// where a row of B is put in LDS: row r of block j of a wave's columns is put
-// so that a lane's registers, over all its blocks, hold WN / 4 (16 x 16
-// blocks) or WN / 2 (32 x 32) consecutive columns, a whole 16-byte store or
-// several.
+// those are next to each other in it.  Which n they are is ours to choose, by
+// which row of B is put where in LDS: a lane gets runs of 8 columns, a 16-byte
+// store of 16-bit values or two of 32-bit ones, and neighbouring lanes
+// neighbouring runs.
 //
 // K need not be a multiple of 16 on the 128-bit path: the last chunk of a row
 // of A is cleared past K in LDS, and what B's holds there meets zeros.
@@ -40,6 +39,7 @@ struct S8Tile {
   static constexpr int NV = MF == 32 ? 16 : 4;     // accumulator registers of a block
   static constexpr int STEPS = MF == 32 ? 4 : 2;   // instructions a block takes per slice
   static constexpr int LQ = 64 / MF;               // lanes with the same row of a block
+  static constexpr int RUN = MF == 32 || TN % 2 == 0 ? 8 : 4;  // columns next to each other in a lane
   static constexpr int SLICE = (BM + BN) * 128;    // bytes
   static constexpr int STAGE = SLICE * KS;
   static constexpr int NIA = KS * BM / 8 / WAVES;  // 1 KB loads per wave per stage
@@ -53,11 +53,12 @@ struct S8Tile {
 
 __device__ __forceinline__ int s8_swizzle(int row) { return (row & 7) ^ ((row >> 3) & 1); }
 
-// The column, within a wave's WN, of LDS row `pl` of them.
-template <class T> __device__ __forceinline__ int s8_column(int pl) {
-  const int j = pl / T::MF, r = pl % T::MF;
-  if constexpr (T::MF == 16) return (r >> 2) * (4 * T::TN) + j * 4 + (r & 3);
-  else return ((r >> 2) & 1) * (16 * T::TN) + j * 16 + (r >> 3) * 4 + (r & 3);
+// The column, within a wave's WN, of row r of block j: runs of RUN columns in
+// the registers of a lane, neighbouring runs in neighbouring lanes.
+template <class T> __device__ __forceinline__ int s8_column(int j, int r) {
+  if constexpr (T::MF == 32) return 32 * j + 16 * (r >> 4) + 8 * ((r >> 2) & 1) + 4 * ((r >> 3) & 1) + (r & 3);
+  else if constexpr (T::RUN == 8) return 32 * (j >> 1) + 8 * (r >> 2) + 4 * (j & 1) + (r & 3);
+  else return 16 * j + r;
 }
 
 __device__ __forceinline__ void s8_dma16(__amdgpu_buffer_rsrc_t rs, char *dst, uint32_t off, int soff) {
@@ -82,48 +83,63 @@ __device__ __forceinline__ intx4 s8_load16(const int8_t *p, int valid) {
   return v;
 }
 
-// What is left to do with the sums of one lane's row: scales, C, bias,
-// activation, rounding to C's type (once, from 32 bits).
-template <class F, int CW>
-__device__ __forceinline__ void s8_store_row(const S8Args &a, F *c, const float *sb, const float *bias,
-                                             int cols, float sa, const int (&acc)[CW], bool wide) {
-  constexpr int G = sizeof(F) == 2 && CW % 8 == 0 ? 8 : 4;  // 16 bytes, or 8
+// Buffer loads and stores of 4 elements or one, at a byte offset (kOob: zero,
+// or nothing stored).
+template <class F>
+__device__ __forceinline__ void s8_load4(__amdgpu_buffer_rsrc_t rs, uint32_t off, float (&v)[4]) {
+  if constexpr (sizeof(F) == 4) {
+    const floatx4 w = __builtin_bit_cast(floatx4, __builtin_amdgcn_raw_buffer_load_b128(rs, off, 0, 0));
 #pragma unroll
-  for (int t = 0; t < CW; t += G) {
-    if (t >= cols) break;
-    F out[G];
-    const bool whole = wide && t + G <= cols;
-    F c0[G];
-    if (a.beta != 0.0f) {
-      if (whole) {
-        __builtin_memcpy(c0, __builtin_assume_aligned(c + t, G * sizeof(F)), sizeof(c0));
-      } else {
+    for (int e = 0; e < 4; ++e) v[e] = w[e];
+  } else {
+    typedef F f4 __attribute__((ext_vector_type(4)));
+    const f4 w = __builtin_bit_cast(f4, __builtin_amdgcn_raw_buffer_load_b64(rs, off, 0, 0));
 #pragma unroll
-        for (int e = 0; e < G; ++e) c0[e] = t + e < cols ? c[t + e] : (F)0.0f;
-      }
-    }
-#pragma unroll
-    for (int e = 0; e < G; ++e) {
-      const bool in = t + e < cols;
-      float v = (float)acc[t + e] * sa * (in ? sb[t + e] : 0.0f);
-      if (a.beta != 0.0f) v += a.beta * (float)c0[e];
-      if (bias != nullptr) v += in ? bias[t + e] : 0.0f;
-      out[e] = (F)apply_act(v, a.act);
-    }
-    if (whole) {
-      __builtin_memcpy(__builtin_assume_aligned(c + t, G * sizeof(F)), out, sizeof(out));
-    } else {
-#pragma unroll
-      for (int e = 0; e < G; ++e)
-        if (t + e < cols) c[t + e] = out[e];
-    }
+    for (int e = 0; e < 4; ++e) v[e] = (float)w[e];
   }
 }
+template <class F>
+__device__ __forceinline__ float s8_load1(__amdgpu_buffer_rsrc_t rs, uint32_t off) {
+  if constexpr (sizeof(F) == 4)
+    return __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(rs, off, 0, 0));
+  else
+    return (float)__builtin_bit_cast(F, (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(rs, off, 0, 0));
+}
+template <class F, int RUN>
+__device__ __forceinline__ void s8_store_run(__amdgpu_buffer_rsrc_t rs, uint32_t off, const float (&v)[RUN]) {
+  typedef unsigned uintx4 __attribute__((ext_vector_type(4)));
+  typedef unsigned uintx2 __attribute__((ext_vector_type(2)));
+  if constexpr (sizeof(F) == 4) {
+    typedef F f4 __attribute__((ext_vector_type(4)));
+#pragma unroll
+    for (int g = 0; g < RUN; g += 4) {
+      const f4 w = {v[g], v[g + 1], v[g + 2], v[g + 3]};
+      __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(uintx4, w), rs, off + 4 * g, 0, 0);
+    }
+  } else {
+    typedef F fr __attribute__((ext_vector_type(RUN)));
+    fr w;
+#pragma unroll
+    for (int e = 0; e < RUN; ++e) w[e] = (F)v[e];
+    if constexpr (RUN == 8)
+      __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(uintx4, w), rs, off, 0, 0);
+    else
+      __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(uintx2, w), rs, off, 0, 0);
+  }
+}
+template <class F>
+__device__ __forceinline__ void s8_store1(__amdgpu_buffer_rsrc_t rs, uint32_t off, float v) {
+  if constexpr (sizeof(F) == 4)
+    __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(unsigned, v), rs, off, 0, 0);
+  else
+    __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, (F)v), rs, off, 0, 0);
+}
 
-// Whether the lanes' groups of columns can be moved 16 (8) bytes at a time.
-__device__ __forceinline__ bool s8_wide_c(const S8Args &a) {
+// Whether every run of `run` columns is inside C or outside it, and aligned
+// to its bytes (16 at most).
+__device__ __forceinline__ bool s8_whole_runs(const S8Args &a, int run) {
   const int size = a.type == kTypeF32 ? 4 : 2;
-  return ((uintptr_t)a.C & 15) == 0 && (a.ldc * size & 15) == 0;
+  return (uintptr_t)a.C % 16 == 0 && a.ldc * size % 16 == 0 && a.N % run == 0;
 }
 
 template <class T, bool DMA>
@@ -169,7 +185,7 @@ __global__ void __launch_bounds__(T::NT) s8_kernel(S8Args a, int tiles_m, int ti
   for (int q = 0; q < T::NIB; ++q) {
     const int f = (wave * T::NIB + q) * 8 + (lane >> 3);
     const int p = f % BN;
-    rowb[q] = p / T::WN * T::WN + s8_column<T>(p % T::WN);
+    rowb[q] = p / T::WN * T::WN + s8_column<T>(p % T::WN / T::MF, p % T::MF);
     colb[q] = f / BN * 128 + 16 * (pos ^ s8_swizzle(p));
   }
   auto set_offsets = [&](int kvalid) {
@@ -329,30 +345,78 @@ __global__ void __launch_bounds__(T::NT) s8_kernel(S8Args a, int tiles_m, int ti
     }
   }
 
-  // Epilogue: this lane's columns of each of its rows.
-  constexpr int CW = T::TN * T::NV;
-  const int nl = wn * T::WN + lq * CW;
-  const float *sb = a.sB + n0 + nl;
-  const float *bias = a.bias != nullptr ? a.bias + n0 + nl : nullptr;
-  const bool wide = s8_wide_c(a);
+  // Epilogue: scales, C, bias, activation, in 32 bits, and one rounding to C's
+  // type.  A lane has RUN columns at a time of one row.
+  constexpr int RUN = T::RUN, RUNS = T::TN * T::NV / RUN;
+  // the column of run t, and its sums of block row i
+  auto run_col = [&](int t) -> int {
+    return wn * T::WN + (T::MF == 32 ? 16 * t + 8 * lq : 4 * RUN * t + RUN * lq);
+  };
+  auto run_sum = [&](int i, int t, int e) -> int {
+    if constexpr (T::MF == 32) return acc[i][t >> 1][8 * (t & 1) + e];
+    else if constexpr (RUN == 8) return acc[i][2 * t + (e >> 2)][e & 3];
+    else return acc[i][t][e];
+  };
+  float sb[RUNS][RUN], bias[RUNS][RUN];
+  {
+    const __amdgpu_buffer_rsrc_t rs_sb = make_rsrc(a.sB + n0);
+    const __amdgpu_buffer_rsrc_t rs_bias = make_rsrc(a.bias != nullptr ? a.bias + n0 : a.sB);
 #pragma unroll
-  for (int i = 0; i < T::TM; ++i) {
-    const int m = wm * T::WM + i * T::MF + lr;
-    if (m >= rows) continue;
-    int sums[CW];
+    for (int t = 0; t < RUNS; ++t)
 #pragma unroll
-    for (int j = 0; j < T::TN; ++j)
-#pragma unroll
-      for (int v = 0; v < T::NV; ++v) sums[j * T::NV + v] = acc[i][j][v];
-    const float sa = a.sA[m0 + m];
-    const size_t at = (size_t)(m0 + m) * a.ldc + n0 + nl;
-    if (a.type == kTypeF32)
-      s8_store_row<float, CW>(a, static_cast<float *>(a.C) + at, sb, bias, cols - nl, sa, sums, wide);
-    else if (a.type == kTypeF16)
-      s8_store_row<_Float16, CW>(a, static_cast<_Float16 *>(a.C) + at, sb, bias, cols - nl, sa, sums, wide);
-    else
-      s8_store_row<__bf16, CW>(a, static_cast<__bf16 *>(a.C) + at, sb, bias, cols - nl, sa, sums, wide);
+      for (int e = 0; e < RUN; ++e) {
+        const int col = run_col(t) + e;
+        sb[t][e] = s8_load1<float>(rs_sb, col < cols ? 4u * col : kOob);
+        bias[t][e] = s8_load1<float>(rs_bias, a.bias != nullptr && col < cols ? 4u * col : kOob);
+      }
   }
+  const bool whole = s8_whole_runs(a, RUN);
+  const __amdgpu_buffer_rsrc_t rs_sa = make_rsrc(a.sA + m0);
+  auto finish = [&](auto zero) {
+    typedef decltype(zero) F;
+    const __amdgpu_buffer_rsrc_t rs_c = make_rsrc(static_cast<F *>(a.C) + (size_t)m0 * a.ldc + n0);
+#pragma unroll
+    for (int i = 0; i < T::TM; ++i) {
+      const int m = wm * T::WM + i * T::MF + lr;
+      const float sa = s8_load1<float>(rs_sa, m < rows ? 4u * m : kOob);
+#pragma unroll
+      for (int t = 0; t < RUNS; ++t) {
+        const int col = run_col(t);
+        const uint32_t off = (uint32_t)(m * a.ldc + col) * (uint32_t)sizeof(F);
+        const uint32_t run_off = m < rows && col < cols ? off : kOob;
+        float v[RUN];
+#pragma unroll
+        for (int e = 0; e < RUN; ++e) v[e] = (float)run_sum(i, t, e) * sa * sb[t][e];
+        if (a.beta != 0.0f) {
+          if (whole) {
+#pragma unroll
+            for (int g = 0; g < RUN; g += 4) {
+              float c0[4];
+              s8_load4<F>(rs_c, run_off + g * (uint32_t)sizeof(F), c0);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) v[g + e] += a.beta * c0[e];
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < RUN; ++e)
+              v[e] += a.beta * s8_load1<F>(rs_c, m < rows && col + e < cols ? off + e * (uint32_t)sizeof(F) : kOob);
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < RUN; ++e) v[e] = apply_act(v[e] + bias[t][e], a.act);
+        if (whole) {
+          s8_store_run<F, RUN>(rs_c, run_off, v);
+        } else {
+#pragma unroll
+          for (int e = 0; e < RUN; ++e)
+            s8_store1<F>(rs_c, m < rows && col + e < cols ? off + e * (uint32_t)sizeof(F) : kOob, v[e]);
+        }
+      }
+    }
+  };
+  if (a.type == kTypeF32) finish(0.0f);
+  else if (a.type == kTypeF16) finish((_Float16)0.0f);
+  else finish((__bf16)0.0f);
 }
 
 // 16-byte loads of whole chunks: rows that start at multiples of 16 bytes.
