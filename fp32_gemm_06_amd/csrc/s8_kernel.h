@@ -4,7 +4,9 @@
 // bits (K is at most 131071), so every split of K gives the same C.
 //
 // A workgroup owns a BM x BN tile of C and walks K in stages of KS slices of
-// 128 bytes; two stages' LDS buffers, the next one in flight during this one.
+// 128 bytes, a slice for each of KS groups of waves, whose sums meet in LDS at
+// the end.  NST stages of LDS: while one is multiplied, the next NST - 1 are
+// on their way.
 //
 // LDS.  A slice is a row of eight 16-byte chunks for each row of the operand,
 // chunk c of row p at position c ^ swizzle(p), which spreads the rows that one
@@ -28,9 +30,9 @@
 namespace fp32gemm {
 namespace {
 
-template <int BM_, int BN_, int WM_, int WN_, int MF_, int KS_>
+template <int BM_, int BN_, int WM_, int WN_, int MF_, int KS_, int NST_>
 struct S8Tile {
-  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, MF = MF_, KS = KS_;
+  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, MF = MF_, KS = KS_, NST = NST_;
   static constexpr int WAVES_N = BN / WN;
   static constexpr int WT = (BM / WM) * WAVES_N;  // waves per K group
   static constexpr int WAVES = WT * KS;
@@ -44,12 +46,20 @@ struct S8Tile {
   static constexpr int STAGE = SLICE * KS;
   static constexpr int NIA = KS * BM / 8 / WAVES;  // 1 KB loads per wave per stage
   static constexpr int NIB = KS * BN / 8 / WAVES;
+  // One wave a K group: it loads what it reads, and nothing is shared before the end.
+  static constexpr bool OWN = WT == 1;
   static_assert(MF == 16 || MF == 32, "16x16x64 or 32x32x32 blocks");
   static_assert(BM % WM == 0 && BN % WN == 0 && WM % MF == 0 && WN % MF == 0, "wave tiling");
   static_assert(KS * BM / 8 % WAVES == 0 && KS * BN / 8 % WAVES == 0, "whole loads per wave");
-  static_assert(2 * STAGE <= 160 * 1024, "LDS of a CU");
-  static_assert((KS - 1) * BM * BN * 4 <= 2 * STAGE, "the K groups' sums fit in the buffers");
+  static_assert(NST >= 2 && NST * STAGE <= 160 * 1024, "LDS of a CU");
+  static_assert((KS - 1) * BM * BN * 4 <= NST * STAGE, "the K groups' sums fit in the buffers");
+  static_assert((NST - 2) * (NIA + NIB) <= 63, "vmcnt");
 };
+
+// Wait until at most N of this wave's memory operations are in flight.
+template <int N> __device__ __forceinline__ void s8_wait_vm() {
+  __builtin_amdgcn_s_waitcnt((N & 15) | (N >> 4) << 14 | 0x0F70);
+}
 
 __device__ __forceinline__ int s8_swizzle(int row) { return (row & 7) ^ ((row >> 3) & 1); }
 
@@ -142,10 +152,49 @@ __device__ __forceinline__ bool s8_whole_runs(const S8Args &a, int run) {
   return (uintptr_t)a.C % 16 == 0 && a.ldc * size % 16 == 0 && a.N % run == 0;
 }
 
+// Four columns of one row, inside C: scaled, added to and stored.
+__device__ __forceinline__ void s8_finish4(const S8Args &a, int m, int n, intx4 sum, bool whole) {
+  const float sa = a.sA[m];
+  auto put = [&](auto *c) {
+    typedef std::remove_reference_t<decltype(*c)> F;
+    typedef F f4 __attribute__((ext_vector_type(4)));
+    c += (size_t)m * a.ldc + n;
+    f4 c0 = f4{};
+    if (a.beta != 0.0f) {
+      if (whole) {
+        c0 = *reinterpret_cast<const f4 *>(c);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (n + e < a.N) c0[e] = c[e];
+      }
+    }
+    f4 out;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int j = n + e < a.N ? n + e : n;
+      float v = (float)sum[e] * sa * a.sB[j];
+      if (a.beta != 0.0f) v += a.beta * (float)c0[e];
+      if (a.bias != nullptr) v += a.bias[j];
+      out[e] = (F)apply_act(v, a.act);
+    }
+    if (whole) {
+      *reinterpret_cast<f4 *>(c) = out;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (n + e < a.N) c[e] = out[e];
+    }
+  };
+  if (a.type == kTypeF32) put(static_cast<float *>(a.C));
+  else if (a.type == kTypeF16) put(static_cast<_Float16 *>(a.C));
+  else put(static_cast<__bf16 *>(a.C));
+}
+
 template <class T, bool DMA>
 __global__ void __launch_bounds__(T::NT) s8_kernel(S8Args a, int tiles_m, int tiles_n, int group_m) {
   constexpr int BM = T::BM, BN = T::BN, KS = T::KS;
-  __shared__ __attribute__((aligned(16))) char lds[2 * T::STAGE];
+  __shared__ __attribute__((aligned(16))) char lds[T::NST * T::STAGE];
   const int tid = threadIdx.x;
   const int lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -241,11 +290,19 @@ __global__ void __launch_bounds__(T::NT) s8_kernel(S8Args a, int tiles_m, int ti
       (void)buf;
     }
   };
+  // Publishes a stage to the waves that share it, or frees its buffer.
+  auto meet = [&]() {
+    if constexpr (T::OWN) {
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    } else {
+      __syncthreads();
+    }
+  };
   // After the last stage has landed: the chunk of A's rows that K ends in.
   auto clear_tail = [&](char *buf) {
     if constexpr (DMA) {
-      if ((a.K & 15) == 0) return;
-      for (int p = tid; p < BM; p += T::NT) {
+      if ((a.K & 15) == 0 || (T::OWN && kg != klast / 128)) return;
+      for (int p = T::OWN ? lane : tid; p < BM; p += T::OWN ? 64 : T::NT) {
         intx4 *c = reinterpret_cast<intx4 *>(buf + klast / 128 * T::SLICE + p * 128 +
                                              16 * ((klast % 128 / 16) ^ s8_swizzle(p)));
         intx4 v = *c;
@@ -256,7 +313,7 @@ __global__ void __launch_bounds__(T::NT) s8_kernel(S8Args a, int tiles_m, int ti
         }
         *c = v;
       }
-      __syncthreads();
+      meet();
     } else {
       (void)buf;
     }
@@ -297,25 +354,38 @@ __global__ void __launch_bounds__(T::NT) s8_kernel(S8Args a, int tiles_m, int ti
     }
   };
 
-  set_offsets(nst == 1 ? klast : 128 * KS);
-  fetch(lds, 0);
-  commit(lds);
-  if constexpr (DMA) __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0)
-  __syncthreads();
-  if (nst == 1) clear_tail(lds);
-  for (int st = 0; st < nst; ++st) {
-    char *cur = lds + (st & 1) * T::STAGE, *nxt = lds + ((st + 1) & 1) * T::STAGE;
-    const bool more = st + 1 < nst;
-    if (more) {
-      if (st + 2 == nst) set_offsets(klast);
-      fetch(nxt, st + 1);
+  if constexpr (DMA) {
+    // NST - 1 stages in flight ahead of the one that is multiplied; past the
+    // end of K they are masked loads, so the count of them in flight stays.
+    constexpr int NST = T::NST;
+    auto fetch_stage = [&](int st) {
+      if (st == nst - 1) set_offsets(klast);
+      else if (st == nst) set_offsets(0);
+      fetch(lds + st % NST * T::STAGE, st);
+    };
+    if (nst > 1) set_offsets(128 * KS);
+#pragma unroll
+    for (int st = 0; st < NST - 1; ++st) fetch_stage(st);
+    for (int st = 0; st < nst; ++st) {
+      char *cur = lds + st % NST * T::STAGE;
+      s8_wait_vm<(NST - 2) * (T::NIA + T::NIB)>();
+      meet();  // this stage is there, and the buffer of the one before is free
+      if (st == nst - 1) clear_tail(cur);
+      fetch_stage(st + NST - 1);
+      compute(cur);
     }
-    compute(cur);
-    if (more) commit(nxt);
-    if constexpr (DMA) __builtin_amdgcn_s_waitcnt(0x0F70);
-    __syncthreads();
-    if (st + 2 == nst) clear_tail(nxt);
+    s8_wait_vm<0>();  // the masked loads have written their zeros
+  } else {
+    fetch(lds, 0);
+    for (int st = 0; st < nst; ++st) {
+      char *cur = lds + (st & 1) * T::STAGE;
+      commit(cur);
+      meet();
+      if (st + 1 < nst) fetch(cur, st + 1);  // into registers
+      compute(cur);
+    }
   }
+  __syncthreads();
 
   // K groups 1.. leave their sums in LDS (free since the last barrier), group
   // 0 adds them.

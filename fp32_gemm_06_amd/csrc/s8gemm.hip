@@ -1,4 +1,6 @@
 // The 8-bit product's kernels, their choice by shape, and the launch.
+#include <limits.h>
+
 #include "s8_kernel.h"
 
 namespace fp32gemm {
@@ -9,15 +11,35 @@ constexpr int kMaxLaunchRows = 1 << 22;
 
 struct S8Config {
   const char *name;
+  int max_rows;
   hipError_t (*launch)(const S8Args &, hipStream_t);
 };
 
+#define S8_TILE(name, ...) {name, INT_MAX, s8_launch<S8Tile<__VA_ARGS__>>}
 const S8Config kConfigs[] = {
-    {"128x128_w64x64_m16", s8_launch<S8Tile<128, 128, 64, 64, 16, 1>>},
-    {"256x256_w128x64_m32", s8_launch<S8Tile<256, 256, 128, 64, 32, 1>>},
-    {"256x256_w128x64_m16", s8_launch<S8Tile<256, 256, 128, 64, 16, 1>>},
-    {"64x64_w32x32_m16_k2", s8_launch<S8Tile<64, 64, 32, 32, 16, 2>>},
-    {"16x64_w16x64_m16_k4", s8_launch<S8Tile<16, 64, 16, 64, 16, 4>>},
+    S8_TILE("16x16_k8_s4", 16, 16, 16, 16, 16, 8, 4),
+    S8_TILE("16x16_k4_s4", 16, 16, 16, 16, 16, 4, 4),
+    S8_TILE("16x32_k8_s3", 16, 32, 16, 32, 16, 8, 3),
+    S8_TILE("16x32_k4_s4", 16, 32, 16, 32, 16, 4, 4),
+    S8_TILE("16x64_k4_s3", 16, 64, 16, 64, 16, 4, 3),
+    S8_TILE("32x16_k8_s3", 32, 16, 32, 16, 16, 8, 3),
+    S8_TILE("32x32_k4_s4", 32, 32, 32, 32, 16, 4, 4),
+    S8_TILE("32x32_k8_s2", 32, 32, 32, 32, 16, 8, 2),
+    S8_TILE("32x64_k4_s3", 32, 64, 32, 64, 16, 4, 3),
+    S8_TILE("64x16_k4_s3", 64, 16, 64, 16, 16, 4, 3),
+    S8_TILE("64x32_k4_s3", 64, 32, 64, 32, 16, 4, 3),
+    S8_TILE("64x64_k2_s4", 64, 64, 32, 32, 16, 2, 4),
+    S8_TILE("64x64_k4o_s2", 64, 64, 64, 64, 16, 4, 2),
+    S8_TILE("64x64_k1_s4", 64, 64, 32, 32, 16, 1, 4),
+    S8_TILE("128x64_k1_s4", 128, 64, 64, 32, 16, 1, 4),
+    S8_TILE("128x64_k2_s3", 128, 64, 64, 32, 16, 2, 3),
+    S8_TILE("128x128_w64x64_s2", 128, 128, 64, 64, 16, 1, 2),
+    S8_TILE("128x128_w64x64_s4", 128, 128, 64, 64, 16, 1, 4),
+    S8_TILE("128x128_w64x32_s4", 128, 128, 64, 32, 16, 1, 4),
+    S8_TILE("128x256_w64x64_s3", 128, 256, 64, 64, 16, 1, 3),
+    S8_TILE("256x128_w64x64_s3", 256, 128, 64, 64, 16, 1, 3),
+    S8_TILE("256x256_w128x64_s2", 256, 256, 128, 64, 16, 1, 2),
+    {"skinny16", kS8SkinnyRows, launch_s8_skinny16},
 };
 
 __global__ void s8_epilogue_kernel(S8Args a) {
@@ -41,7 +63,7 @@ __global__ void s8_epilogue_kernel(S8Args a) {
 int pick(int M, int N, int K) {
   (void)N;
   (void)K;
-  return M <= 16 ? 4 : M <= 256 ? 3 : 1;
+  return M <= 128 ? 1 : M <= 256 ? 11 : 21;
 }
 
 }  // namespace
@@ -49,6 +71,9 @@ int pick(int M, int N, int K) {
 int s8_num_configs() { return (int)(sizeof(kConfigs) / sizeof(kConfigs[0])); }
 const char *s8_config_name(int cfg) {
   return cfg >= 0 && cfg < s8_num_configs() ? kConfigs[cfg].name : nullptr;
+}
+int s8_config_max_rows(int cfg) {
+  return cfg >= 0 && cfg < s8_num_configs() ? kConfigs[cfg].max_rows : -1;
 }
 int select_s8_config(int M, int N, int K) { return pick(M, N, K); }
 

@@ -15,6 +15,13 @@ from gpu_util import require_gpu
 
 gpu = pytest.mark.gpu
 CONFIGS = fg.config_names(fg.KIND_S8GEMM)
+
+
+def takes(cfg, M):
+    """Whether configuration cfg (-1: the library's choice) runs M rows."""
+    return cfg < 0 or M <= fg.fp32gemm_config_max_rows(fg.KIND_S8GEMM, cfg)
+
+
 # every configuration's tile edges, one less and one more, and sizes of one
 EDGES = [1, 2, 15, 16, 17, 31, 33, 63, 64, 65, 127, 129, 255, 257]
 
@@ -58,6 +65,10 @@ def run_gemm(M, N, K, type=0, cfg=-1, beta=0.0, bias=False, relu=False, lda=None
     bv = torch.randn(N, generator=g) if bias else None
     pad = lambda k: -(-k // 16) * 16
     lda, ldb, ldc = lda or pad(K), ldb or pad(K), ldc or N
+    if not takes(cfg, M):
+        assert fg.fp32gemm_s8gemm_with_config(cfg, M, N, K, 16, lda, 16, 16, ldb, 16, beta, type, 16, ldc,
+                                              None, 0, 0) == fg.ERR_CONFIG
+        return None
     dA, _ = device(A, lda, offa)
     dB, _ = device(B, ldb, offb)
     # beta = 0 must not read C: NaN in it
@@ -150,7 +161,8 @@ def test_row_operators_of_no_rows_need_no_gpu():
 def test_gemm_every_configuration(cfg, aligned):
     require_gpu()
     for n, (M, N, K) in enumerate([(257, 129, 300), (65, 257, 512), (1, 1, 1), (16, 64, 128), (3, 70, 127),
-                                   (130, 31, 1031), (300, 520, 2048)]):
+                                   (130, 31, 1031), (300, 520, 2048), (128, 100, 5000), (33, 48, 1300),
+                                   (17, 49, 640), (90, 16, 11008)]):
         ld = None if aligned else K + (n % 3)
         run_gemm(M, N, K, type=n % 3, cfg=cfg, lda=ld, ldb=ld, offa=0 if aligned else n % 5,
                  offb=0 if aligned else 3, beta=(0.0, 0.5)[n % 2], bias=n % 3 == 0, relu=n % 4 == 1, seed=cfg)
