@@ -4,13 +4,13 @@
 // bits (K is at most 131071), so every split of K gives the same C.
 //
 // A workgroup owns a BM x BN tile of C and walks K in stages of KS slices of
-// 128 bytes, a slice for each of KS groups of waves, whose sums meet in LDS at
+// SB bytes, a slice for each of KS groups of waves, whose sums meet in LDS at
 // the end.  NST stages of LDS: while one is multiplied, the next NST - 1 are
 // on their way.
 //
-// LDS.  A slice is a row of eight 16-byte chunks for each row of the operand,
-// chunk c of row p at position c ^ swizzle(p), which spreads the rows that one
-// ds_read_b128 reads at the same chunk over the banks.  The 128-bit path
+// LDS.  A slice is a row of SB / 16 16-byte chunks for each row of the operand,
+// chunk c of row p at position c ^ swizzle(p), which spreads the chunks that
+// a ds_read_b128 reads together over the banks.  The 128-bit path
 // writes it with buffer loads straight into LDS; the other path loads through
 // registers, at any alignment, into the same places.
 //
@@ -33,27 +33,30 @@ namespace {
 template <int BM_, int BN_, int WM_, int WN_, int MF_, int KS_, int NST_>
 struct S8Tile {
   static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, MF = MF_, KS = KS_, NST = NST_;
+  static constexpr int SB = 128, CP = SB / 16;     // bytes and chunks of a row of a slice
+  static constexpr int RL = 1024 / SB;             // rows of a 1 KB load
   static constexpr int WAVES_N = BN / WN;
   static constexpr int WT = (BM / WM) * WAVES_N;  // waves per K group
   static constexpr int WAVES = WT * KS;
   static constexpr int NT = WAVES * 64;
   static constexpr int TM = WM / MF, TN = WN / MF;
   static constexpr int NV = MF == 32 ? 16 : 4;     // accumulator registers of a block
-  static constexpr int STEPS = MF == 32 ? 4 : 2;   // instructions a block takes per slice
+  static constexpr int STEPS = SB * MF / 1024;     // instructions a block takes per slice
   static constexpr int LQ = 64 / MF;               // lanes with the same row of a block
   static constexpr int RUN = MF == 32 || TN % 2 == 0 ? 8 : 4;  // columns next to each other in a lane
-  static constexpr int SLICE = (BM + BN) * 128;    // bytes
+  static constexpr int SLICE = (BM + BN) * SB;    // bytes
   static constexpr int STAGE = SLICE * KS;
-  static constexpr int NIA = KS * BM / 8 / WAVES;  // 1 KB loads per wave per stage
-  static constexpr int NIB = KS * BN / 8 / WAVES;
+  static constexpr int NIA = KS * BM / RL / WAVES;  // 1 KB loads per wave per stage
+  static constexpr int NIB = KS * BN / RL / WAVES;
   // One wave a K group: it loads what it reads, and nothing is shared before the end.
   static constexpr bool OWN = WT == 1;
   static_assert(MF == 16 || MF == 32, "16x16x64 or 32x32x32 blocks");
   static_assert(BM % WM == 0 && BN % WN == 0 && WM % MF == 0 && WN % MF == 0, "wave tiling");
-  static_assert(KS * BM / 8 % WAVES == 0 && KS * BN / 8 % WAVES == 0, "whole loads per wave");
+  static_assert(KS * BM / RL % WAVES == 0 && KS * BN / RL % WAVES == 0, "whole loads per wave");
   static_assert(NST >= 2 && NST * STAGE <= 160 * 1024, "LDS of a CU");
   static_assert((KS - 1) * BM * BN * 4 <= NST * STAGE, "the K groups' sums fit in the buffers");
-  static_assert((NST - 2) * (NIA + NIB) <= 63, "vmcnt");
+  static_assert((NST - 1) * (NIA + NIB) <= 63, "vmcnt");
+  static_assert(STEPS % 2 == 0, "operands in two register sets");
 };
 
 // Wait until at most N of this wave's memory operations are in flight.
@@ -61,7 +64,14 @@ template <int N> __device__ __forceinline__ void s8_wait_vm() {
   __builtin_amdgcn_s_waitcnt((N & 15) | (N >> 4) << 14 | 0x0F70);
 }
 
-__device__ __forceinline__ int s8_swizzle(int row) { return (row & 7) ^ ((row >> 3) & 1); }
+// What chunk positions of row p are exclusive-ored with.  A ds_read_b128 takes
+// 16 lanes a cycle (0-3, 12-15, 20-23 and 24-27, and so on), and their 16
+// chunks have to lie in different ones of the 64 banks: (row parity, position)
+// has to differ.  32 x 32 blocks read one chunk of those rows, 16 x 16 blocks
+// two neighbouring chunks of eight each.  Counted on gfx950: no conflicts.
+template <class T> __device__ __forceinline__ int s8_swizzle(int p) {
+  return T::MF == 32 ? (p & 7) ^ ((p >> 3) & 1) : p & 7;
+}
 
 // The column, within a wave's WN, of row r of block j: runs of RUN columns in
 // the registers of a lane, neighbouring runs in neighbouring lanes.
@@ -215,27 +225,29 @@ __global__ void __launch_bounds__(T::NT) s8_kernel(S8Args a, int tiles_m, int ti
   const int8_t *Ag = a.A + (size_t)m0 * a.lda;
   const int8_t *Bg = a.B + (size_t)n0 * a.ldb;
 
-  const int nst = (a.K + 128 * KS - 1) / (128 * KS);
-  const int klast = a.K - (nst - 1) * 128 * KS;  // valid k of the last stage
+  constexpr int SB = T::SB;
+  const int nst = (a.K + SB * KS - 1) / (SB * KS);
+  const int klast = a.K - (nst - 1) * SB * KS;  // valid k of the last stage
 
-  // Lane l of load `inst` moves the chunk at position l % 8 of LDS row
-  // 8 inst + l / 8, counted over a slice's rows and then the stage's slices.
-  const int pos = lane & 7;
+  // Lane l of load `inst` moves the chunk at position l % CP of LDS row
+  // RL inst + l / CP, counted over a slice's rows and then the stage's slices:
+  // neighbouring lanes read a row's neighbouring chunks.
+  const int pos = lane % T::CP;
   uint32_t offa[T::NIA], offb[T::NIB];
   int cola[T::NIA], colb[T::NIB];
   int rowa[T::NIA], rowb[T::NIB];
 #pragma unroll
   for (int q = 0; q < T::NIA; ++q) {
-    const int f = (wave * T::NIA + q) * 8 + (lane >> 3);
+    const int f = (wave * T::NIA + q) * T::RL + lane / T::CP;
     rowa[q] = f % BM;
-    cola[q] = f / BM * 128 + 16 * (pos ^ s8_swizzle(f % BM));
+    cola[q] = f / BM * SB + 16 * (pos ^ s8_swizzle<T>(f % BM));
   }
 #pragma unroll
   for (int q = 0; q < T::NIB; ++q) {
-    const int f = (wave * T::NIB + q) * 8 + (lane >> 3);
+    const int f = (wave * T::NIB + q) * T::RL + lane / T::CP;
     const int p = f % BN;
     rowb[q] = p / T::WN * T::WN + s8_column<T>(p % T::WN / T::MF, p % T::MF);
-    colb[q] = f / BN * 128 + 16 * (pos ^ s8_swizzle(p));
+    colb[q] = f / BN * SB + 16 * (pos ^ s8_swizzle<T>(p));
   }
   auto set_offsets = [&](int kvalid) {
 #pragma unroll
@@ -247,12 +259,12 @@ __global__ void __launch_bounds__(T::NT) s8_kernel(S8Args a, int tiles_m, int ti
   };
   // where a load goes: 1 KB a load, over the slices' operand areas
   auto dst_a = [&](int q) -> int {
-    const int f = (wave * T::NIA + q) * 8;
-    return f / BM * T::SLICE + f % BM * 128;
+    const int f = (wave * T::NIA + q) * T::RL;
+    return f / BM * T::SLICE + f % BM * SB;
   };
   auto dst_b = [&](int q) -> int {
-    const int f = (wave * T::NIB + q) * 8;
-    return f / BN * T::SLICE + BM * 128 + f % BN * 128;
+    const int f = (wave * T::NIB + q) * T::RL;
+    return f / BN * T::SLICE + BM * SB + f % BN * SB;
   };
 
   const __amdgpu_buffer_rsrc_t rs_a = make_rsrc(Ag);
@@ -260,16 +272,10 @@ __global__ void __launch_bounds__(T::NT) s8_kernel(S8Args a, int tiles_m, int ti
   intx4 sta[DMA ? 1 : T::NIA], stb[DMA ? 1 : T::NIB];
   (void)sta;
   (void)stb;
-  auto fetch = [&](char *buf, int st) {
-    const int k0 = st * 128 * KS;
-    if constexpr (DMA) {
-#pragma unroll
-      for (int q = 0; q < T::NIA; ++q) s8_dma16(rs_a, buf + dst_a(q), offa[q], k0);
-#pragma unroll
-      for (int q = 0; q < T::NIB; ++q) s8_dma16(rs_b, buf + dst_b(q), offb[q], k0);
-    } else {
-      (void)buf;
-      const int kvalid = a.K - k0;
+  // the register path: global loads of a stage, and the writes to LDS
+  auto fetch = [&](int st) {
+    if constexpr (!DMA) {
+      const int k0 = st * SB * KS, kvalid = a.K - k0;
 #pragma unroll
       for (int q = 0; q < T::NIA; ++q)
         sta[q] = s8_load16(Ag + (size_t)rowa[q] * a.lda + k0 + cola[q],
@@ -301,10 +307,10 @@ __global__ void __launch_bounds__(T::NT) s8_kernel(S8Args a, int tiles_m, int ti
   // After the last stage has landed: the chunk of A's rows that K ends in.
   auto clear_tail = [&](char *buf) {
     if constexpr (DMA) {
-      if ((a.K & 15) == 0 || (T::OWN && kg != klast / 128)) return;
+      if ((a.K & 15) == 0 || (T::OWN && kg != klast / SB)) return;
       for (int p = T::OWN ? lane : tid; p < BM; p += T::OWN ? 64 : T::NT) {
-        intx4 *c = reinterpret_cast<intx4 *>(buf + klast / 128 * T::SLICE + p * 128 +
-                                             16 * ((klast % 128 / 16) ^ s8_swizzle(p)));
+        intx4 *c = reinterpret_cast<intx4 *>(buf + klast / SB * T::SLICE + p * SB +
+                                             16 * ((klast % SB / 16) ^ s8_swizzle<T>(p)));
         intx4 v = *c;
 #pragma unroll
         for (int d = 0; d < 4; ++d) {
@@ -328,61 +334,106 @@ __global__ void __launch_bounds__(T::NT) s8_kernel(S8Args a, int tiles_m, int ti
 
   const int lr = lane % T::MF, lq = lane / T::MF;
   const int pa = wm * T::WM + lr, pb = wn * T::WN + lr;  // LDS rows of block 0
-  auto compute = [&](const char *buf) {
-    const char *As = buf + kg * T::SLICE, *Bs = As + BM * 128;
+  // The operands of one instruction step of every block.
+  struct Frag {
+    intx4 a[T::TM], b[T::TN];
+  };
+  auto read = [&](const char *buf, int step, Frag &f) {
+    const char *As = buf + kg * T::SLICE, *Bs = As + BM * SB;
+    const int c = step * T::LQ + lq;
 #pragma unroll
-    for (int s = 0; s < T::STEPS; ++s) {
-      intx4 fa[T::TM], fb[T::TN];
-      const int c = s * T::LQ + lq;
+    for (int j = 0; j < T::TN; ++j)
+      f.b[j] = *reinterpret_cast<const intx4 *>(Bs + (pb + j * T::MF) * SB +
+                                                16 * (c ^ s8_swizzle<T>(pb + j * T::MF)));
 #pragma unroll
-      for (int i = 0; i < T::TM; ++i)
-        fa[i] = *reinterpret_cast<const intx4 *>(As + (pa + i * T::MF) * 128 +
-                                                 16 * (c ^ s8_swizzle(pa + i * T::MF)));
+    for (int i = 0; i < T::TM; ++i)
+      f.a[i] = *reinterpret_cast<const intx4 *>(As + (pa + i * T::MF) * SB +
+                                                16 * (c ^ s8_swizzle<T>(pa + i * T::MF)));
+  };
+  auto mma_row = [&](const Frag &f, int i) {
 #pragma unroll
-      for (int j = 0; j < T::TN; ++j)
-        fb[j] = *reinterpret_cast<const intx4 *>(Bs + (pb + j * T::MF) * 128 +
-                                                 16 * (c ^ s8_swizzle(pb + j * T::MF)));
-#pragma unroll
-      for (int i = 0; i < T::TM; ++i)
-#pragma unroll
-        for (int j = 0; j < T::TN; ++j) {
-          if constexpr (T::MF == 32)
-            acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fb[j], fa[i], acc[i][j], 0, 0, 0);
-          else
-            acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fb[j], fa[i], acc[i][j], 0, 0, 0);
-        }
+    for (int j = 0; j < T::TN; ++j) {
+      if constexpr (T::MF == 32)
+        acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(f.b[j], f.a[i], acc[i][j], 0, 0, 0);
+      else
+        acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(f.b[j], f.a[i], acc[i][j], 0, 0, 0);
     }
   };
+  Frag fr[2];
 
   if constexpr (DMA) {
-    // NST - 1 stages in flight ahead of the one that is multiplied; past the
-    // end of K they are masked loads, so the count of them in flight stays.
-    constexpr int NST = T::NST;
-    auto fetch_stage = [&](int st) {
+    // NST stages in LDS.  A load instruction waits for its place in the
+    // memory pipeline, and the wave with it, so a stage's loads follow the
+    // barrier that freed their buffer a few at a time, between the first half
+    // of the matrix instructions that follow it too.  Operands are read one
+    // step ahead; the last step's instructions run after the barrier and cover
+    // the first reads of the next stage.  Past the end of K the loads are
+    // masked, so the count of them in flight stays.  The scheduling barriers
+    // keep the order written here.  At 4096^3, 256 x 256 tiles: all loads
+    // first, then reads and instructions as the compiler orders them, 1.75 us
+    // a stage; spread and read ahead 1.59; with the order kept 1.49 (the
+    // instructions and LDS reads alone 1.24, the loads alone 1.02).
+    constexpr int NST = T::NST, NL = T::NIA + T::NIB, STEPS = T::STEPS;
+    constexpr int PER_ROW = T::TM == 1 ? NL : (NL + T::TM / 2 - 1) / (T::TM / 2);
+    auto load = [&](int q, char *buf, int k0) {
+      if (q < T::NIA) s8_dma16(rs_a, buf + dst_a(q), offa[q < T::NIA ? q : 0], k0);
+      else s8_dma16(rs_b, buf + dst_b(q - T::NIA), offb[q >= T::NIA ? q - T::NIA : 0], k0);
+    };
+    auto mask_stage = [&](int st) {
       if (st == nst - 1) set_offsets(klast);
       else if (st == nst) set_offsets(0);
-      fetch(lds + st % NST * T::STAGE, st);
     };
-    if (nst > 1) set_offsets(128 * KS);
+    if (nst > 1) set_offsets(SB * KS);
 #pragma unroll
-    for (int st = 0; st < NST - 1; ++st) fetch_stage(st);
+    for (int st = 0; st < NST; ++st) {
+      mask_stage(st);
+#pragma unroll
+      for (int q = 0; q < NL; ++q) load(q, lds + st * T::STAGE, st * SB * KS);
+    }
+    s8_wait_vm<(NST - 1) * NL>();
+    meet();
+    if (nst == 1) clear_tail(lds);
+    read(lds, 0, fr[0]);
+    int at = 0;  // buffer of stage st
     for (int st = 0; st < nst; ++st) {
-      char *cur = lds + st % NST * T::STAGE;
-      s8_wait_vm<(NST - 2) * (T::NIA + T::NIB)>();
-      meet();  // this stage is there, and the buffer of the one before is free
-      if (st == nst - 1) clear_tail(cur);
-      fetch_stage(st + NST - 1);
-      compute(cur);
+      char *cur = lds + at * T::STAGE;
+#pragma unroll
+      for (int s = 0; s + 1 < STEPS; ++s) {
+        read(cur, s + 1, fr[(s + 1) & 1]);
+#pragma unroll
+        for (int i = 0; i < T::TM; ++i) mma_row(fr[s & 1], i);
+      }
+      s8_wait_vm<(NST - 2) * NL>();  // stage st + 1 has landed
+      meet();                        // for every wave, and this stage's buffer is free
+      at = at + 1 == NST ? 0 : at + 1;
+      if (st + 1 < nst) {
+        if (st + 2 == nst) clear_tail(lds + at * T::STAGE);
+        read(lds + at * T::STAGE, 0, fr[0]);
+      }
+      mask_stage(st + NST);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int i = 0; i < T::TM; ++i) {
+        mma_row(fr[(STEPS - 1) & 1], i);
+#pragma unroll
+        for (int q = i * PER_ROW; q < (i + 1) * PER_ROW && q < NL; ++q) load(q, cur, (st + NST) * SB * KS);
+        __builtin_amdgcn_sched_barrier(0);
+      }
     }
     s8_wait_vm<0>();  // the masked loads have written their zeros
   } else {
-    fetch(lds, 0);
+    fetch(0);
     for (int st = 0; st < nst; ++st) {
       char *cur = lds + (st & 1) * T::STAGE;
       commit(cur);
       meet();
-      if (st + 1 < nst) fetch(cur, st + 1);  // into registers
-      compute(cur);
+      if (st + 1 < nst) fetch(st + 1);  // into registers
+#pragma unroll
+      for (int s = 0; s < T::STEPS; ++s) {
+        read(cur, s, fr[s & 1]);
+#pragma unroll
+        for (int i = 0; i < T::TM; ++i) mma_row(fr[s & 1], i);
+      }
     }
   }
   __syncthreads();
