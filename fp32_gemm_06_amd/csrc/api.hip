@@ -264,7 +264,6 @@ int s8gemm_call(int cfg, int base, int M, int N, int K, const signed char *A, in
                 int type, void *C, int ldc, const float *bias, int act, hipStream_t s) {
   const int off = base - 1;  // `base`: the 1-based position of M
   if (M < 0) return -(1 + off);
-  if (cfg >= 0 && M > s8_config_max_rows(cfg)) return FP32GEMM_ERR_CONFIG;
   if (N < 0) return -(2 + off);
   if (K < 0 || K > kMaxS8K) return -(3 + off);
   if (lda < imax(1, K) || lda > kMaxLd) return -(5 + off);
@@ -559,7 +558,7 @@ int fp32gemm_config_max_rows(int kind, int cfg) {
     return (cfg >= 0 && cfg < n) ? c[cfg].max_rows : -1;
   }
   if (kind == 0) return (cfg >= 0 && cfg < num_gemm_config_ids()) ? 0x7fffffff : -1;
-  if (kind == 2) return s8_config_max_rows(cfg);
+  if (kind == 2) return (cfg >= 0 && cfg < s8_num_configs()) ? 0x7fffffff : -1;
   return -1;
 }
 

@@ -7,7 +7,6 @@
 namespace fp32gemm {
 
 typedef int intx4 __attribute__((ext_vector_type(4)));
-typedef int intx16 __attribute__((ext_vector_type(16)));
 
 // Element types of the float operands (the header's FP32GEMM_TYPE_*).
 constexpr int kTypeF32 = 0, kTypeF16 = 1, kTypeBf16 = 2;
@@ -33,14 +32,7 @@ struct S8Args {
 hipError_t launch_s8(int cfg, const S8Args &a, hipStream_t s);
 int s8_num_configs();
 const char *s8_config_name(int cfg);
-int s8_config_max_rows(int cfg);
 int select_s8_config(int M, int N, int K);
-
-// The kernel for M <= kS8SkinnyRows (s8_skinny.hip), 16 or 32 columns of C a
-// workgroup.
-constexpr int kS8SkinnyRows = 128;
-hipError_t launch_s8_skinny16(const S8Args &a, hipStream_t s);
-hipError_t launch_s8_skinny32(const S8Args &a, hipStream_t s);
 
 // C <- act(beta C + bias): the product over an empty K.
 hipError_t launch_s8_epilogue_only(const S8Args &a, hipStream_t s);

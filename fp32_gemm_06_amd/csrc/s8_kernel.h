@@ -30,28 +30,25 @@
 namespace fp32gemm {
 namespace {
 
-template <int BM_, int BN_, int WM_, int WN_, int MF_, int KS_, int NST_>
+template <int BM_, int BN_, int WM_, int WN_, int KS_, int NST_>
 struct S8Tile {
-  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, MF = MF_, KS = KS_, NST = NST_;
+  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, KS = KS_, NST = NST_;
   static constexpr int SB = 128, CP = SB / 16;     // bytes and chunks of a row of a slice
   static constexpr int RL = 1024 / SB;             // rows of a 1 KB load
   static constexpr int WAVES_N = BN / WN;
   static constexpr int WT = (BM / WM) * WAVES_N;  // waves per K group
   static constexpr int WAVES = WT * KS;
   static constexpr int NT = WAVES * 64;
-  static constexpr int TM = WM / MF, TN = WN / MF;
-  static constexpr int NV = MF == 32 ? 16 : 4;     // accumulator registers of a block
-  static constexpr int STEPS = SB * MF / 1024;     // instructions a block takes per slice
-  static constexpr int LQ = 64 / MF;               // lanes with the same row of a block
-  static constexpr int RUN = MF == 32 || TN % 2 == 0 ? 8 : 4;  // columns next to each other in a lane
+  static constexpr int TM = WM / 16, TN = WN / 16;  // 16 x 16 blocks of a wave
+  static constexpr int STEPS = SB / 64;             // instructions a block takes per slice
+  static constexpr int RUN = TN % 2 == 0 ? 8 : 4;   // columns next to each other in a lane
   static constexpr int SLICE = (BM + BN) * SB;    // bytes
   static constexpr int STAGE = SLICE * KS;
   static constexpr int NIA = KS * BM / RL / WAVES;  // 1 KB loads per wave per stage
   static constexpr int NIB = KS * BN / RL / WAVES;
   // One wave a K group: it loads what it reads, and nothing is shared before the end.
   static constexpr bool OWN = WT == 1;
-  static_assert(MF == 16 || MF == 32, "16x16x64 or 32x32x32 blocks");
-  static_assert(BM % WM == 0 && BN % WN == 0 && WM % MF == 0 && WN % MF == 0, "wave tiling");
+  static_assert(BM % WM == 0 && BN % WN == 0 && WM % 16 == 0 && WN % 16 == 0, "wave tiling");
   static_assert(KS * BM / RL % WAVES == 0 && KS * BN / RL % WAVES == 0, "whole loads per wave");
   static_assert(NST >= 2 && NST * STAGE <= 160 * 1024, "LDS of a CU");
   static_assert((KS - 1) * BM * BN * 4 <= NST * STAGE, "the K groups' sums fit in the buffers");
@@ -64,20 +61,17 @@ template <int N> __device__ __forceinline__ void s8_wait_vm() {
   __builtin_amdgcn_s_waitcnt((N & 15) | (N >> 4) << 14 | 0x0F70);
 }
 
-// What chunk positions of row p are exclusive-ored with.  A ds_read_b128 takes
-// 16 lanes a cycle (0-3, 12-15, 20-23 and 24-27, and so on), and their 16
-// chunks have to lie in different ones of the 64 banks: (row parity, position)
-// has to differ.  32 x 32 blocks read one chunk of those rows, 16 x 16 blocks
-// two neighbouring chunks of eight each.  Counted on gfx950: no conflicts.
-template <class T> __device__ __forceinline__ int s8_swizzle(int p) {
-  return T::MF == 32 ? (p & 7) ^ ((p >> 3) & 1) : p & 7;
-}
+// What the chunk positions of row p are exclusive-ored with.  A ds_read_b128
+// takes 16 lanes a cycle (0-3, 12-15, 20-23 and 24-27, and so on): rows 0-3
+// and 12-15 at chunk c and rows 4-11 at chunk c + 1, c even.  Row and position
+// together have to put their 16 chunks in different ones of the 64 banks.
+// Counted on gfx950: no conflicts.
+__device__ __forceinline__ int s8_swizzle(int p) { return p & 7; }
 
 // The column, within a wave's WN, of row r of block j: runs of RUN columns in
 // the registers of a lane, neighbouring runs in neighbouring lanes.
 template <class T> __device__ __forceinline__ int s8_column(int j, int r) {
-  if constexpr (T::MF == 32) return 32 * j + 16 * (r >> 4) + 8 * ((r >> 2) & 1) + 4 * ((r >> 3) & 1) + (r & 3);
-  else if constexpr (T::RUN == 8) return 32 * (j >> 1) + 8 * (r >> 2) + 4 * (j & 1) + (r & 3);
+  if constexpr (T::RUN == 8) return 32 * (j >> 1) + 8 * (r >> 2) + 4 * (j & 1) + (r & 3);
   else return 16 * j + r;
 }
 
@@ -162,45 +156,6 @@ __device__ __forceinline__ bool s8_whole_runs(const S8Args &a, int run) {
   return (uintptr_t)a.C % 16 == 0 && a.ldc * size % 16 == 0 && a.N % run == 0;
 }
 
-// Four columns of one row, inside C: scaled, added to and stored.
-__device__ __forceinline__ void s8_finish4(const S8Args &a, int m, int n, intx4 sum, bool whole) {
-  const float sa = a.sA[m];
-  auto put = [&](auto *c) {
-    typedef std::remove_reference_t<decltype(*c)> F;
-    typedef F f4 __attribute__((ext_vector_type(4)));
-    c += (size_t)m * a.ldc + n;
-    f4 c0 = f4{};
-    if (a.beta != 0.0f) {
-      if (whole) {
-        c0 = *reinterpret_cast<const f4 *>(c);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (n + e < a.N) c0[e] = c[e];
-      }
-    }
-    f4 out;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int j = n + e < a.N ? n + e : n;
-      float v = (float)sum[e] * sa * a.sB[j];
-      if (a.beta != 0.0f) v += a.beta * (float)c0[e];
-      if (a.bias != nullptr) v += a.bias[j];
-      out[e] = (F)apply_act(v, a.act);
-    }
-    if (whole) {
-      *reinterpret_cast<f4 *>(c) = out;
-    } else {
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (n + e < a.N) c[e] = out[e];
-    }
-  };
-  if (a.type == kTypeF32) put(static_cast<float *>(a.C));
-  else if (a.type == kTypeF16) put(static_cast<_Float16 *>(a.C));
-  else put(static_cast<__bf16 *>(a.C));
-}
-
 template <class T, bool DMA>
 __global__ void __launch_bounds__(T::NT) s8_kernel(S8Args a, int tiles_m, int tiles_n, int group_m) {
   constexpr int BM = T::BM, BN = T::BN, KS = T::KS;
@@ -240,14 +195,14 @@ __global__ void __launch_bounds__(T::NT) s8_kernel(S8Args a, int tiles_m, int ti
   for (int q = 0; q < T::NIA; ++q) {
     const int f = (wave * T::NIA + q) * T::RL + lane / T::CP;
     rowa[q] = f % BM;
-    cola[q] = f / BM * SB + 16 * (pos ^ s8_swizzle<T>(f % BM));
+    cola[q] = f / BM * SB + 16 * (pos ^ s8_swizzle(f % BM));
   }
 #pragma unroll
   for (int q = 0; q < T::NIB; ++q) {
     const int f = (wave * T::NIB + q) * T::RL + lane / T::CP;
     const int p = f % BN;
-    rowb[q] = p / T::WN * T::WN + s8_column<T>(p % T::WN / T::MF, p % T::MF);
-    colb[q] = f / BN * SB + 16 * (pos ^ s8_swizzle<T>(p));
+    rowb[q] = p / T::WN * T::WN + s8_column<T>(p % T::WN / 16, p % 16);
+    colb[q] = f / BN * SB + 16 * (pos ^ s8_swizzle(p));
   }
   auto set_offsets = [&](int kvalid) {
 #pragma unroll
@@ -310,7 +265,7 @@ __global__ void __launch_bounds__(T::NT) s8_kernel(S8Args a, int tiles_m, int ti
       if ((a.K & 15) == 0 || (T::OWN && kg != klast / SB)) return;
       for (int p = T::OWN ? lane : tid; p < BM; p += T::OWN ? 64 : T::NT) {
         intx4 *c = reinterpret_cast<intx4 *>(buf + klast / SB * T::SLICE + p * SB +
-                                             16 * ((klast % SB / 16) ^ s8_swizzle<T>(p)));
+                                             16 * ((klast % SB / 16) ^ s8_swizzle(p)));
         intx4 v = *c;
 #pragma unroll
         for (int d = 0; d < 4; ++d) {
@@ -325,14 +280,13 @@ __global__ void __launch_bounds__(T::NT) s8_kernel(S8Args a, int tiles_m, int ti
     }
   };
 
-  typedef int acc_t __attribute__((ext_vector_type(T::NV)));
-  acc_t acc[T::TM][T::TN];
+  intx4 acc[T::TM][T::TN];
 #pragma unroll
   for (int i = 0; i < T::TM; ++i)
 #pragma unroll
-    for (int j = 0; j < T::TN; ++j) acc[i][j] = acc_t{};
+    for (int j = 0; j < T::TN; ++j) acc[i][j] = intx4{0, 0, 0, 0};
 
-  const int lr = lane % T::MF, lq = lane / T::MF;
+  const int lr = lane & 15, lq = lane >> 4;
   const int pa = wm * T::WM + lr, pb = wn * T::WN + lr;  // LDS rows of block 0
   // The operands of one instruction step of every block.
   struct Frag {
@@ -340,24 +294,20 @@ __global__ void __launch_bounds__(T::NT) s8_kernel(S8Args a, int tiles_m, int ti
   };
   auto read = [&](const char *buf, int step, Frag &f) {
     const char *As = buf + kg * T::SLICE, *Bs = As + BM * SB;
-    const int c = step * T::LQ + lq;
+    const int c = 4 * step + lq;
 #pragma unroll
     for (int j = 0; j < T::TN; ++j)
-      f.b[j] = *reinterpret_cast<const intx4 *>(Bs + (pb + j * T::MF) * SB +
-                                                16 * (c ^ s8_swizzle<T>(pb + j * T::MF)));
+      f.b[j] = *reinterpret_cast<const intx4 *>(Bs + (pb + j * 16) * SB +
+                                                16 * (c ^ s8_swizzle(pb + j * 16)));
 #pragma unroll
     for (int i = 0; i < T::TM; ++i)
-      f.a[i] = *reinterpret_cast<const intx4 *>(As + (pa + i * T::MF) * SB +
-                                                16 * (c ^ s8_swizzle<T>(pa + i * T::MF)));
+      f.a[i] = *reinterpret_cast<const intx4 *>(As + (pa + i * 16) * SB +
+                                                16 * (c ^ s8_swizzle(pa + i * 16)));
   };
   auto mma_row = [&](const Frag &f, int i) {
 #pragma unroll
-    for (int j = 0; j < T::TN; ++j) {
-      if constexpr (T::MF == 32)
-        acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(f.b[j], f.a[i], acc[i][j], 0, 0, 0);
-      else
-        acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(f.b[j], f.a[i], acc[i][j], 0, 0, 0);
-    }
+    for (int j = 0; j < T::TN; ++j)
+      acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(f.b[j], f.a[i], acc[i][j], 0, 0, 0);
   };
   Frag fr[2];
 
@@ -441,7 +391,7 @@ __global__ void __launch_bounds__(T::NT) s8_kernel(S8Args a, int tiles_m, int ti
   // K groups 1.. leave their sums in LDS (free since the last barrier), group
   // 0 adds them.
   if constexpr (KS > 1) {
-    constexpr int PER = T::TM * T::TN * T::NV * 64;
+    constexpr int PER = T::TM * T::TN * 4 * 64;
     int *red = reinterpret_cast<int *>(lds);
     if (kg > 0) {
       int *mine = red + ((kg - 1) * T::WT + wt) * PER + lane;
@@ -450,7 +400,7 @@ __global__ void __launch_bounds__(T::NT) s8_kernel(S8Args a, int tiles_m, int ti
 #pragma unroll
         for (int j = 0; j < T::TN; ++j)
 #pragma unroll
-          for (int v = 0; v < T::NV; ++v) mine[((i * T::TN + j) * T::NV + v) * 64] = acc[i][j][v];
+          for (int v = 0; v < 4; ++v) mine[((i * T::TN + j) * 4 + v) * 64] = acc[i][j][v];
     }
     __syncthreads();
     if (kg > 0) return;
@@ -462,20 +412,19 @@ __global__ void __launch_bounds__(T::NT) s8_kernel(S8Args a, int tiles_m, int ti
 #pragma unroll
         for (int j = 0; j < T::TN; ++j)
 #pragma unroll
-          for (int v = 0; v < T::NV; ++v) acc[i][j][v] += theirs[((i * T::TN + j) * T::NV + v) * 64];
+          for (int v = 0; v < 4; ++v) acc[i][j][v] += theirs[((i * T::TN + j) * 4 + v) * 64];
     }
   }
 
   // Epilogue: scales, C, bias, activation, in 32 bits, and one rounding to C's
   // type.  A lane has RUN columns at a time of one row.
-  constexpr int RUN = T::RUN, RUNS = T::TN * T::NV / RUN;
+  constexpr int RUN = T::RUN, RUNS = T::TN * 4 / RUN;
   // the column of run t, and its sums of block row i
   auto run_col = [&](int t) -> int {
-    return wn * T::WN + (T::MF == 32 ? 16 * t + 8 * lq : 4 * RUN * t + RUN * lq);
+    return wn * T::WN + 4 * RUN * t + RUN * lq;
   };
   auto run_sum = [&](int i, int t, int e) -> int {
-    if constexpr (T::MF == 32) return acc[i][t >> 1][8 * (t & 1) + e];
-    else if constexpr (RUN == 8) return acc[i][2 * t + (e >> 2)][e & 3];
+    if constexpr (RUN == 8) return acc[i][2 * t + (e >> 2)][e & 3];
     else return acc[i][t][e];
   };
   float sb[RUNS][RUN], bias[RUNS][RUN];
@@ -498,7 +447,7 @@ __global__ void __launch_bounds__(T::NT) s8_kernel(S8Args a, int tiles_m, int ti
     const __amdgpu_buffer_rsrc_t rs_c = make_rsrc(static_cast<F *>(a.C) + (size_t)m0 * a.ldc + n0);
 #pragma unroll
     for (int i = 0; i < T::TM; ++i) {
-      const int m = wm * T::WM + i * T::MF + lr;
+      const int m = wm * T::WM + i * 16 + lr;
       const float sa = s8_load1<float>(rs_sa, m < rows ? 4u * m : kOob);
 #pragma unroll
       for (int t = 0; t < RUNS; ++t) {
@@ -549,7 +498,7 @@ inline bool s8_dma_ok(const S8Args &a) {
 
 template <class T> hipError_t s8_launch(const S8Args &a, hipStream_t s) {
   const int tm = (a.M + T::BM - 1) / T::BM, tn = (a.N + T::BN - 1) / T::BN;
-  const int group_m = 4;
+  constexpr int group_m = 4;
   if (s8_dma_ok(a))
     s8_kernel<T, true><<<tm * tn, T::NT, 0, s>>>(a, tm, tn, group_m);
   else

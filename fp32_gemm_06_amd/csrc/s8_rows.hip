@@ -13,44 +13,44 @@
 // pass, and no value is normalised before it is coded.  The row stays in
 // registers between that pass and the codes, so memory is read once.  The
 // sum of squares is kept in 64 bits: squares of float32 values pass its range.
+// Bound by memory: 8192 x 4096 bf16 with residual 40.9 us, 5.74 TB/s; what
+// comes before one row's last byte is one wave's latency (1 x 4096: 3.3 us).
 #include "s8_common.h"
 
 namespace fp32gemm {
 namespace {
 
-constexpr int E = 8;  // elements per thread and step
+constexpr int E = 8;  // elements of a thread's chunk of a row
 
-// E elements from an address aligned to the element only.
-template <class T> struct Chunk {
-  T v[E];
+// E elements in registers, and at any address of an element (the hardware
+// takes wide accesses at any alignment).
+template <class T> struct ChunkOf {
+  typedef T type __attribute__((ext_vector_type(E)));
+  typedef T anywhere __attribute__((ext_vector_type(E), aligned(alignof(T))));
 };
-template <class T> __device__ __forceinline__ Chunk<T> load_chunk(const T *p) {
-  Chunk<T> c;
-  __builtin_memcpy(&c, p, sizeof(c));
-  return c;
-}
 
-// Elements [k, k + E) of a row of K, zero past its end.
-template <class T>
-__device__ __forceinline__ void load_row(const T *row, int k, int K, float (&v)[E]) {
-  if (k + E <= K) {
-    const Chunk<T> c = load_chunk(row + k);
-#pragma unroll
-    for (int e = 0; e < E; ++e) v[e] = (float)c.v[e];
-  } else {
-#pragma unroll
-    for (int e = 0; e < E; ++e) v[e] = k + e < K ? (float)row[k + e] : 0.0f;
-  }
-}
-
-template <class T>
-__device__ __forceinline__ void store_row(T *row, int k, int K, const T (&v)[E]) {
-  if (k + E <= K) {
-    __builtin_memcpy(row + k, v, sizeof(v));
+// Elements [k, k + E) of a row of K, zero past its end; and back.  WHOLE: K is
+// a multiple of E, and no chunk ends past it.
+template <class T, bool WHOLE>
+__device__ __forceinline__ typename ChunkOf<T>::type load_chunk(const T *row, int k, int K) {
+  typename ChunkOf<T>::type c = {};
+  if (WHOLE || k + E <= K) {
+    c = *reinterpret_cast<const typename ChunkOf<T>::anywhere *>(row + k);
   } else {
 #pragma unroll
     for (int e = 0; e < E; ++e)
-      if (k + e < K) row[k + e] = v[e];
+      if (k + e < K) c[e] = row[k + e];
+  }
+  return c;
+}
+template <class T, bool WHOLE>
+__device__ __forceinline__ void store_chunk(T *row, int k, int K, typename ChunkOf<T>::type c) {
+  if (WHOLE || k + E <= K) {
+    *reinterpret_cast<typename ChunkOf<T>::anywhere *>(row + k) = c;
+  } else {
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+      if (k + e < K) row[k + e] = c[e];
   }
 }
 
@@ -59,40 +59,69 @@ struct RowStat {
   double ss;     // sum of h^2
 };
 
-__device__ __forceinline__ RowStat wave_stat(RowStat s, bool norm) {
-#pragma unroll
-  for (int d = 32; d > 0; d >>= 1) {
-    const uint32_t t = (uint32_t)__shfl_xor((int)s.top, d, 64);
-    s.top = t > s.top ? t : s.top;
-    if (norm) s.ss += __shfl_xor(s.ss, d, 64);
+// Sum and maximum over the wave's lanes, by cross-lane moves in the vector
+// unit (towards lane 63, then to all).
+template <int CTRL, int ROWS> __device__ __forceinline__ int lanes(int v) {
+  return __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xf, false);
+}
+template <int CTRL, int ROWS, bool NORM> __device__ __forceinline__ void fold(RowStat &s) {
+  const uint32_t t = (uint32_t)lanes<CTRL, ROWS>((int)s.top);
+  s.top = t > s.top ? t : s.top;
+  if constexpr (NORM) {
+    const unsigned long long b = __builtin_bit_cast(unsigned long long, s.ss);
+    const uint32_t lo = (uint32_t)lanes<CTRL, ROWS>((int)(uint32_t)b);
+    const uint32_t hi = (uint32_t)lanes<CTRL, ROWS>((int)(uint32_t)(b >> 32));
+    s.ss += __builtin_bit_cast(double, (unsigned long long)hi << 32 | lo);
+  }
+}
+template <bool NORM> __device__ __forceinline__ RowStat wave_stat(RowStat s) {
+  fold<0x111, 0xf, NORM>(s);  // from 1, 2, 4, 8 lanes below in a row of 16
+  fold<0x112, 0xf, NORM>(s);
+  fold<0x114, 0xf, NORM>(s);
+  fold<0x118, 0xf, NORM>(s);
+  fold<0x142, 0xa, NORM>(s);  // lane 15 of a row to the next row
+  fold<0x143, 0xc, NORM>(s);  // lane 31 to the upper half
+  s.top = (uint32_t)__builtin_amdgcn_readlane((int)s.top, 63);
+  if constexpr (NORM) {
+    const unsigned long long b = __builtin_bit_cast(unsigned long long, s.ss);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)b, 63);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(b >> 32), 63);
+    s.ss = __builtin_bit_cast(double, (unsigned long long)hi << 32 | lo);
   }
   return s;
 }
 
-// v (and h, stored) of one chunk, and its part of the row's statistics.
-template <class T, bool NORM>
-__device__ __forceinline__ void chunk_values(const S8RowArgs &a, const T *x, const T *r, const T *w,
-                                             T *hout, int k, float (&v)[E], RowStat &st) {
-  load_row(x, k, a.K, v);
+// A chunk as it is read: X, and for the norm R and W.
+template <class T> struct Raw {
+  typename ChunkOf<T>::type x, r, w;
+};
+template <class T, bool NORM, bool WHOLE>
+__device__ __forceinline__ void read_raw(Raw<T> &c, const T *x, const T *r, const T *w, int k, int K) {
+  c.x = load_chunk<T, WHOLE>(x, k, K);
   if constexpr (NORM) {
-    if (r != nullptr) {
-      float q[E];
-      load_row(r, k, a.K, q);
+    if (r != nullptr) c.r = load_chunk<T, WHOLE>(r, k, K);
+    c.w = load_chunk<T, WHOLE>(w, k, K);
+  }
+}
+
+// v (and h, stored) of one chunk, and its part of the row's statistics.
+template <class T, bool NORM, bool WHOLE>
+__device__ __forceinline__ void chunk_values(const Raw<T> &c, bool residual, T *hout, int k, int K,
+                                             float (&v)[E], RowStat &st) {
 #pragma unroll
-      for (int e = 0; e < E; ++e) v[e] = (float)(T)(v[e] + q[e]);
-    }
-    if (hout != nullptr) {
-      T h[E];
+  for (int e = 0; e < E; ++e) v[e] = (float)c.x[e];
+  if constexpr (NORM) {
+    typename ChunkOf<T>::type h = c.x;
+    if (residual) {
 #pragma unroll
-      for (int e = 0; e < E; ++e) h[e] = (T)v[e];
-      store_row(hout, k, a.K, h);
+      for (int e = 0; e < E; ++e) h[e] = (T)(v[e] + (float)c.r[e]);
     }
-    float g[E];
-    load_row(w, k, a.K, g);
+    if (hout != nullptr) store_chunk<T, WHOLE>(hout, k, K, h);
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-      st.ss = __builtin_fma((double)v[e], (double)v[e], st.ss);
-      v[e] *= g[e];
+      const float f = (float)h[e];
+      st.ss = __builtin_fma((double)f, (double)f, st.ss);
+      v[e] = f * (float)c.w[e];
     }
   }
 #pragma unroll
@@ -102,164 +131,325 @@ __device__ __forceinline__ void chunk_values(const S8RowArgs &a, const T *x, con
   }
 }
 
-__device__ __forceinline__ void chunk_codes(const S8RowArgs &a, int8_t *qrow, int k,
-                                            const float (&v)[E], const RowStep &rs) {
-  int8_t c[E];
-#pragma unroll
-  for (int e = 0; e < E; ++e) c[e] = (int8_t)row_code(v[e], rs);
-  store_row(qrow, k, a.K, c);
+// 1 / step, and NaN where the codes have to go the long way.
+__device__ __forceinline__ float quick_inv(float scale) {
+  const RowStep r = row_step(scale);
+  return r.lift == 1.0f && r.step > 0.0f ? r.inv : __builtin_nanf("");
 }
 
-// NT threads a row (a wave or more), ROWS rows a workgroup; NV chunks of a
-// row in each thread's registers.  NV = 0: rows of any length, whose chunks
-// are read again for the codes (from the stored sum, where there is one).
-template <class T, bool NORM, int NT, int ROWS, int NV>
-__global__ void __launch_bounds__(NT *ROWS) rows_kernel(S8RowArgs a) {
-  constexpr int WAVES = NT / 64;
-  __shared__ uint32_t tops[ROWS * WAVES];
-  __shared__ double sums[ROWS * WAVES];
-  const int tid = threadIdx.x % NT, sub = threadIdx.x / NT;
-  const long long row = (long long)blockIdx.x * ROWS + sub;
-  const bool live = row < a.M;
-  const long long i = live ? row : a.M - 1;  // a row to read; nothing is written for it
+// Four codes in a word.  Adding 1.5 2^23 leaves round(v inv), to even, in the
+// low bits, and its low byte is the code; v inv is within 8e-6 of v / step, so
+// only values that near to a half are done again by the residual (row_code),
+// as are the rows that are lifted or have no codes, for which inv is NaN.
+__device__ __forceinline__ uint32_t code_word(const float (&v)[4], float inv, float scale) {
+  constexpr float kMagic = 12582912.0f;
+  uint32_t u[4];
+  float off[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float f = __builtin_fmaf(v[e], inv, kMagic);
+    u[e] = __builtin_bit_cast(uint32_t, f);
+    off[e] = __builtin_fabsf(__builtin_fmaf(v[e], inv, kMagic - f));
+  }
+  const float far = __builtin_fmaxf(__builtin_fmaxf(off[0], off[1]), __builtin_fmaxf(off[2], off[3]));
+  if (!(far < 0.49999f)) {
+    const RowStep rs = row_step(scale);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) u[e] = (uint32_t)row_code(v[e], rs);
+  }
+  return __builtin_amdgcn_perm(u[1], u[0], 0x0c0c0400u) | __builtin_amdgcn_perm(u[3], u[2], 0x04000c0cu);
+}
+
+// Codes of one chunk of a row with this scale.
+template <bool WHOLE>
+__device__ __forceinline__ void chunk_codes(int8_t *qrow, int k, int K, const float (&v)[E], float inv,
+                                            float scale) {
+  uint32_t w[2];
+#pragma unroll
+  for (int g = 0; g < 2; ++g) {
+    const float f[4] = {v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3]};
+    w[g] = code_word(f, inv, scale);
+  }
+  if (WHOLE || k + E <= K) {
+    typedef uint32_t words __attribute__((ext_vector_type(2)));
+    typedef uint32_t anywhere __attribute__((ext_vector_type(2), aligned(1)));
+    *reinterpret_cast<anywhere *>(qrow + k) = words{w[0], w[1]};
+  } else {
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+      if (k + e < K) qrow[k + e] = (int8_t)(w[e / 4] >> 8 * (e % 4));
+  }
+}
+
+// A row for each blockDim.x / ROWS threads; NV chunks of it in each thread's
+// registers, all read before the first is used.  NV = 0: rows of any length,
+// whose chunks are read again for the codes (from the stored sum, where there
+// is one).  More than one row a workgroup: one wave each.
+template <class T, bool NORM, int ROWS, int NV, bool WHOLE>
+__global__ void __launch_bounds__(ROWS > 1 ? 64 * ROWS : 1024) rows_kernel(S8RowArgs a) {
+  __shared__ uint32_t tops[16];
+  __shared__ double sums[16];
+  const int nt = ROWS > 1 ? 64 : blockDim.x;
+  const int tid = ROWS > 1 ? threadIdx.x & 63 : threadIdx.x;
+  const long long i = (long long)blockIdx.x * ROWS + (ROWS > 1 ? threadIdx.x >> 6 : 0);
+  if (i >= a.M) return;  // whole waves, and only where there is no barrier
+  const int K = a.K;
   const T *x = static_cast<const T *>(a.X) + i * a.ldx;
   const T *r = a.R ? static_cast<const T *>(a.R) + i * a.ldr : nullptr;
   const T *w = static_cast<const T *>(a.W);
-  T *hout = a.H && live ? static_cast<T *>(a.H) + i * a.ldh : nullptr;
+  T *hout = a.H ? static_cast<T *>(a.H) + i * a.ldh : nullptr;
   int8_t *q = a.Q + i * a.ldq;
 
   RowStat st = {0u, 0.0};
   float v[NV > 0 ? NV : 1][E];
   if constexpr (NV > 0) {
+    Raw<T> raw[NV];
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int k = (tid + j * NT) * E;
-      if (k < a.K) chunk_values<T, NORM>(a, x, r, w, hout, k, v[j], st);
+      const int k = (tid + j * nt) * E;
+      if (k < K) read_raw<T, NORM, WHOLE>(raw[j], x, r, w, k, K);
+    }
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int k = (tid + j * nt) * E;
+      if (k < K) chunk_values<T, NORM, WHOLE>(raw[j], r != nullptr, hout, k, K, v[j], st);
     }
   } else {
-    for (int k = tid * E; k < a.K; k += NT * E) chunk_values<T, NORM>(a, x, r, w, hout, k, v[0], st);
+    for (int k = tid * E; k < K; k += nt * E) {
+      Raw<T> raw;
+      read_raw<T, NORM, WHOLE>(raw, x, r, w, k, K);
+      chunk_values<T, NORM, WHOLE>(raw, r != nullptr, hout, k, K, v[0], st);
+    }
   }
-  st = wave_stat(st, NORM);
-  if constexpr (WAVES > 1) {
-    const int wave = threadIdx.x / 64;
-    if (threadIdx.x % 64 == 0) {
-      tops[wave] = st.top;
-      sums[wave] = st.ss;
+  st = wave_stat<NORM>(st);
+  if constexpr (ROWS == 1) {
+    const int waves = nt / 64;
+    if (tid % 64 == 0) {
+      tops[tid / 64] = st.top;
+      if constexpr (NORM) sums[tid / 64] = st.ss;
     }
     __syncthreads();
     st = {0u, 0.0};
-#pragma unroll
-    for (int u = 0; u < WAVES; ++u) {
-      const uint32_t t = tops[sub * WAVES + u];
-      st.top = t > st.top ? t : st.top;
-      st.ss += sums[sub * WAVES + u];
+    for (int u = 0; u < waves; ++u) {
+      st.top = tops[u] > st.top ? tops[u] : st.top;
+      if constexpr (NORM) st.ss += sums[u];
     }
   }
   const float step = row_scale(st.top);
-  if (live && tid == 0) {
-    float scale = step;
-    if (NORM && step > 0.0f) scale = (float)((double)step / __builtin_sqrt(st.ss / a.K + (double)a.eps));
-    a.scales[i] = scale;
-  }
-  if (!live) return;
-  const RowStep rs = row_step(step);
+  const float inv = quick_inv(step);
   if constexpr (NV > 0) {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int k = (tid + j * NT) * E;
-      if (k < a.K) chunk_codes(a, q, k, v[j], rs);
+      const int k = (tid + j * nt) * E;
+      if (k < K) chunk_codes<WHOLE>(q, k, K, v[j], inv, step);
     }
   } else {
     // With an H the sum is read back from it (by the thread that wrote it),
     // since X or R may be the same memory.
     const T *src = hout ? hout : x;
-    S8RowArgs b = a;
+    const T *add = hout ? nullptr : r;
     RowStat none = {0u, 0.0};
-    for (int k = tid * E; k < a.K; k += NT * E) {
-      chunk_values<T, NORM>(b, src, hout ? nullptr : r, w, nullptr, k, v[0], none);
-      chunk_codes(a, q, k, v[0], rs);
+    for (int k = tid * E; k < K; k += nt * E) {
+      Raw<T> raw;
+      read_raw<T, NORM, WHOLE>(raw, src, add, w, k, K);
+      chunk_values<T, NORM, WHOLE>(raw, add != nullptr, static_cast<T *>(nullptr), k, K, v[0], none);
+      chunk_codes<WHOLE>(q, k, K, v[0], inv, step);
     }
+  }
+  if (tid == 0) {
+    float scale = step;
+    if (NORM && step > 0.0f) scale = (float)((double)step / __builtin_sqrt(st.ss / K + (double)a.eps));
+    a.scales[i] = scale;
   }
 }
 
-template <class T, bool NORM> hipError_t launch_rows(const S8RowArgs &a, hipStream_t s) {
-  auto go = [&](auto kernel, int threads, int rows) {
-    kernel<<<(a.M + rows - 1) / rows, threads, 0, s>>>(a);
-    return hipGetLastError();
-  };
-  if (a.K <= 512) return go(rows_kernel<T, NORM, 64, 4, 1>, 256, 4);
-  if (a.K <= 4096) return go(rows_kernel<T, NORM, 256, 1, 2>, 256, 1);
-  if (a.K <= 8192) return go(rows_kernel<T, NORM, 256, 1, 4>, 256, 1);
-  if (a.K <= 16384) return go(rows_kernel<T, NORM, 512, 1, 4>, 512, 1);
-  return go(rows_kernel<T, NORM, 1024, 1, 0>, 1024, 1);
+// Rows of one launch: keeps the grid's threads below 2^32 for any M.
+constexpr int kMaxLaunchRows = 1 << 21;
+
+template <class T, bool NORM, bool WHOLE> hipError_t launch_rows(const S8RowArgs &all, hipStream_t s) {
+  const int chunks = (all.K + E - 1) / E;
+  for (long long m0 = 0; m0 < all.M; m0 += kMaxLaunchRows) {
+    S8RowArgs a = all;
+    a.M = (int)(all.M - m0 < kMaxLaunchRows ? all.M - m0 : kMaxLaunchRows);
+    a.X = static_cast<const T *>(all.X) + m0 * all.ldx;
+    if (all.R) a.R = static_cast<const T *>(all.R) + m0 * all.ldr;
+    if (all.H) a.H = static_cast<T *>(all.H) + m0 * all.ldh;
+    a.Q += m0 * all.ldq;
+    a.scales += m0;
+    // Whole waves of threads with NV chunks each.  With a row or less for each
+    // CU its latency counts, and one chunk a thread is the quicker (bf16 norm,
+    // 128 x 4096: 3.7 against 4.9 us); with more rows two chunks in flight
+    // are (8192 x 4096: 40.9 against 47.9).  Four spill in fp32.
+    auto threads = [&](int nv) { return (chunks + 64 * nv - 1) / (64 * nv) * 64; };
+    if (chunks <= 64)
+      rows_kernel<T, NORM, 4, 1, WHOLE><<<(a.M + 3) / 4, 256, 0, s>>>(a);
+    else if (chunks <= 128)
+      rows_kernel<T, NORM, 4, 2, WHOLE><<<(a.M + 3) / 4, 256, 0, s>>>(a);
+    else if (chunks <= 1024 && a.M <= 256)
+      rows_kernel<T, NORM, 1, 1, WHOLE><<<a.M, threads(1), 0, s>>>(a);
+    else if (chunks <= 2048)
+      rows_kernel<T, NORM, 1, 2, WHOLE><<<a.M, threads(2), 0, s>>>(a);
+    else
+      rows_kernel<T, NORM, 1, 0, WHOLE><<<a.M, 1024, 0, s>>>(a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
-// Columns of X stored K x M, to rows of codes.  A workgroup takes CB columns
-// over all of K: their largest values first, then 64 k at a time through LDS,
-// where the codes turn from k-major to column-major.
-constexpr int CB = 32;
-constexpr int CT = 512;
+// Columns of X stored K x M, to rows of codes.  A workgroup takes 64 bytes of
+// each row of X over all of K, 1024 k at a time: four lanes read a row's 64
+// bytes, a thread four consecutive k, whose codes of a column make a word.
+// The words turn in LDS from k-major to column-major.  The first HELD times
+// 1024 k stay in registers between the columns' largest values and their
+// codes; the rest is read twice.
+constexpr int CT = 1024, CK = 1024;
 
-template <class T>
+template <class T, int HELD>
 __global__ void __launch_bounds__(CT) columns_kernel(S8RowArgs a) {
-  constexpr int KR = CT / CB;  // k read at a time
-  constexpr int KT = 64;       // k per turn through LDS
-  __shared__ uint32_t tops[KR][CB];
-  __shared__ int8_t turn[CB][KT + 4];
-  const int c = threadIdx.x % CB, kr = threadIdx.x / CB;
-  const long long col0 = (long long)blockIdx.x * CB;
-  const bool live = col0 + c < a.M;
-  const T *x = static_cast<const T *>(a.X) + (live ? col0 + c : a.M - 1);
-  uint32_t top = 0;
-  for (int k = kr; k < a.K; k += KR) {
-    const uint32_t b = abs_bits((float)x[(long long)k * a.ldx]);
-    top = b > top ? b : top;
-  }
-  tops[kr][c] = top;
-  __syncthreads();
+  constexpr int VE = 16 / sizeof(T);  // columns of a thread
+  constexpr int CB = 4 * VE;          // of the workgroup
+  constexpr int PITCH = CK / 4 + 4;   // words of a column in LDS: 4 columns apart are 16 banks apart
+  typedef T vec __attribute__((ext_vector_type(VE)));
+  typedef T anywhere __attribute__((ext_vector_type(VE), aligned(alignof(T))));
+  __shared__ uint32_t tops[CT / 64][CB];
+  __shared__ float scale[CB];
+  __shared__ __attribute__((aligned(16))) uint32_t turn[2][CB * PITCH];
+  const int tid = threadIdx.x;
+  // neighbouring columns, which share lines of X, to the same XCD
+  const int xcd = (int)blockIdx.x & 7, per = gridDim.x >> 3, extra = gridDim.x & 7;
+  const int lid = xcd * per + min(xcd, extra) + ((int)blockIdx.x >> 3);
+  const int col0 = lid * CB;
+  const int c = tid % 4 * VE, g = tid / 4;  // the thread's columns, and its word of 4 k
+  const int cols = a.M - col0 - c;          // of the thread's, valid ones
+  const T *x = static_cast<const T *>(a.X) + col0 + c;
+
+  auto load = [&](int k) -> vec {
+    vec v = {};
+    if (k < a.K) {
+      const T *p = x + (long long)k * a.ldx;
+      if (cols >= VE) {
+        v = *reinterpret_cast<const anywhere *>(p);
+      } else {
 #pragma unroll
-  for (int u = 0; u < KR; ++u) top = tops[u][c] > top ? tops[u][c] : top;
-  const float step = row_scale(top);
-  if (live && kr == 0) a.scales[col0 + c] = step;
-  const RowStep rs = row_step(step);
-  for (int k0 = 0; k0 < a.K; k0 += KT) {
-#pragma unroll
-    for (int u = 0; u < KT / KR; ++u) {
-      const int k = k0 + u * KR + kr;
-      const float v = k < a.K ? (float)x[(long long)k * a.ldx] : 0.0f;
-      turn[c][u * KR + kr] = (int8_t)row_code(v, rs);
-    }
-    __syncthreads();
-    for (int f = threadIdx.x; f < CB * (KT / 4); f += CT) {
-      const int cc = f / (KT / 4), k4 = f % (KT / 4) * 4;
-      if (col0 + cc < a.M) {
-        int8_t *q = a.Q + (col0 + cc) * a.ldq + k0 + k4;
-        if (k0 + k4 + 4 <= a.K) {
-          __builtin_memcpy(q, &turn[cc][k4], 4);
-        } else {
-          for (int e = 0; e < 4; ++e)
-            if (k0 + k4 + e < a.K) q[e] = turn[cc][k4 + e];
-        }
+        for (int e = 0; e < VE; ++e)
+          if (e < cols) v[e] = p[e];
       }
     }
+    return v;
+  };
+  uint32_t top[VE];
+#pragma unroll
+  for (int e = 0; e < VE; ++e) top[e] = 0;
+  auto see = [&](const vec (&v)[4]) {
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+#pragma unroll
+      for (int e = 0; e < VE; ++e) {
+        const uint32_t b = abs_bits((float)v[u][e]);
+        top[e] = b > top[e] ? b : top[e];
+      }
+  };
+  vec held[HELD][4];
+#pragma unroll
+  for (int h = 0; h < HELD; ++h)
+#pragma unroll
+    for (int u = 0; u < 4; ++u) held[h][u] = load(h * CK + 4 * g + u);
+#pragma unroll
+  for (int h = 0; h < HELD; ++h) see(held[h]);
+  for (int k0 = HELD * CK; k0 < a.K; k0 += CK) {
+    vec v[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) v[u] = load(k0 + 4 * g + u);
+    see(v);
+  }
+#pragma unroll
+  for (int e = 0; e < VE; ++e) {
+#pragma unroll
+    for (int d = 4; d < 64; d <<= 1) {
+      const uint32_t t = (uint32_t)__shfl_xor((int)top[e], d, 64);
+      top[e] = t > top[e] ? t : top[e];
+    }
+    if (tid % 64 < 4) tops[tid / 64][c + e] = top[e];
+  }
+  __syncthreads();
+  if (tid < CB) {
+    uint32_t t = 0;
+#pragma unroll
+    for (int w = 0; w < CT / 64; ++w) t = tops[w][tid] > t ? tops[w][tid] : t;
+    scale[tid] = row_scale(t);
+    if (col0 + tid < a.M) a.scales[col0 + tid] = row_scale(t);
+  }
+  __syncthreads();
+  float inv[VE];
+#pragma unroll
+  for (int e = 0; e < VE; ++e) inv[e] = quick_inv(scale[c + e]);
+
+  auto put = [&](const vec (&v)[4], int k0) {
+    uint32_t *words = turn[k0 / CK & 1];
+#pragma unroll
+    for (int e = 0; e < VE; ++e) {
+      const float f[4] = {(float)v[0][e], (float)v[1][e], (float)v[2][e], (float)v[3][e]};
+      words[(c + e) * PITCH + g] = code_word(f, inv[e], scale[c + e]);
+    }
     __syncthreads();
+    const int left = a.K - k0;
+    for (int f = tid; f < CB * (CK / 16); f += CT) {
+      const int col = f / (CK / 16), k = f % (CK / 16) * 16;
+      if (col0 + col >= a.M || k >= left) continue;
+      int8_t *q = a.Q + (long long)(col0 + col) * a.ldq + k0 + k;
+      const uint32_t *from = words + col * PITCH + k / 4;
+      if (k + 16 <= left) {
+        typedef uint32_t four __attribute__((ext_vector_type(4)));
+        typedef uint32_t four_anywhere __attribute__((ext_vector_type(4), aligned(1)));
+        *reinterpret_cast<four_anywhere *>(q) = *reinterpret_cast<const four *>(from);
+      } else {
+        for (int e = 0; e < left - k; ++e) q[e] = (int8_t)(from[e / 4] >> 8 * (e % 4));
+      }
+    }
+    // the other half of `turn` is written next, and this one after the next barrier
+  };
+#pragma unroll
+  for (int h = 0; h < HELD; ++h)
+    if (h * CK < a.K) put(held[h], h * CK);
+  for (int k0 = HELD * CK; k0 < a.K; k0 += CK) {
+    vec v[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) v[u] = load(k0 + 4 * g + u);
+    put(v, k0);
   }
 }
 
 template <class T> hipError_t launch_columns(const S8RowArgs &a, hipStream_t s) {
-  columns_kernel<T><<<(a.M + CB - 1) / CB, CT, 0, s>>>(a);
+  constexpr int CB = 4 * (16 / sizeof(T));
+  const int groups = (a.M + CB - 1) / CB;
+  // Registers for 4096 k of fp32 save the second reading, and cost the second
+  // workgroup of a CU (11008 columns of 4096: 61.8 us, holding 1024 k 70.0);
+  // up to K = 1024, and for 16-bit values, whose second reading is half as
+  // long, the two workgroups are worth more (16384 of 1024: 18.0 against
+  // 23.4; bf16, 11008 of 4096: 49.6 against 53.2).
+  if constexpr (sizeof(T) == 4) {
+    if (a.K > CK) {
+      columns_kernel<T, 4><<<groups, CT, 0, s>>>(a);
+      return hipGetLastError();
+    }
+  }
+  columns_kernel<T, 1><<<groups, CT, 0, s>>>(a);
   return hipGetLastError();
 }
 
 }  // namespace
 
+template <class T> hipError_t rows_of(const S8RowArgs &a, hipStream_t s) {
+  if (a.W != nullptr)
+    return a.K % E == 0 ? launch_rows<T, true, true>(a, s) : launch_rows<T, true, false>(a, s);
+  return a.K % E == 0 ? launch_rows<T, false, true>(a, s) : launch_rows<T, false, false>(a, s);
+}
+
 hipError_t launch_s8_rows(const S8RowArgs &a, int type, hipStream_t s) {
-  const bool norm = a.W != nullptr;
-  if (type == kTypeF32)
-    return norm ? launch_rows<float, true>(a, s) : launch_rows<float, false>(a, s);
-  if (type == kTypeF16)
-    return norm ? launch_rows<_Float16, true>(a, s) : launch_rows<_Float16, false>(a, s);
-  return norm ? launch_rows<__bf16, true>(a, s) : launch_rows<__bf16, false>(a, s);
+  if (type == kTypeF32) return rows_of<float>(a, s);
+  if (type == kTypeF16) return rows_of<_Float16>(a, s);
+  return rows_of<__bf16>(a, s);
 }
 
 hipError_t launch_s8_columns(const S8RowArgs &a, int type, hipStream_t s) {

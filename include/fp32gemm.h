@@ -385,8 +385,8 @@ const char *fp32gemm_config_name(int kind, int cfg);
 int fp32gemm_select_config(int kind, int M, int N, int K);
 
 /* The largest M a configuration runs (kind as above; -1 for an unknown id):
- * 8, 32, 64 or 128 for the GEMV family, INT_MAX for the tiled family; either
- * 128 or INT_MAX for the 8-bit product. */
+ * 8, 32, 64 or 128 for the GEMV family, INT_MAX for the tiled family and the
+ * 8-bit product. */
 int fp32gemm_config_max_rows(int kind, int cfg);
 
 /* Whether the tiled kernel runs this product (batch entries of M x N x K) as
@@ -414,7 +414,7 @@ int fp32gemm_sgemv_with_config(int cfg, int M, int N, int K, float alpha,
 
 /* s8gemm with a forced configuration (cfg = -1 picks as s8gemm does); error
  * positions as s8gemm shifted by one (FP32GEMM_ERR_CONFIG for an unknown
- * id, or an M above fp32gemm_config_max_rows of it). */
+ * id). */
 int fp32gemm_s8gemm_with_config(int cfg, int M, int N, int K,
                                 const signed char *A, int lda,
                                 const float *scaleA, const signed char *B,
