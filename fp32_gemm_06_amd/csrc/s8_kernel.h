@@ -46,6 +46,8 @@ struct S8Tile {
   static constexpr int STAGE = SLICE * KS;
   static constexpr int NIA = KS * BM / RL / WAVES;  // 1 KB loads per wave per stage
   static constexpr int NIB = KS * BN / RL / WAVES;
+  // stages in registers on the path that loads through them
+  static constexpr int REG = NIA + NIB <= 4 ? 3 : NIA + NIB <= 6 ? 2 : 1;
   // One wave a K group: it loads what it reads, and nothing is shared before the end.
   static constexpr bool OWN = WT == 1;
   static_assert(BM % WM == 0 && BN % WN == 0 && WM % 16 == 0 && WN % 16 == 0, "wave tiling");
@@ -84,11 +86,13 @@ __device__ __forceinline__ void s8_dma16(__amdgpu_buffer_rsrc_t rs, char *dst, u
 #endif
 }
 
-// 16 codes from any address, the last 16 - valid of them zero and not read.
+// 16 codes from any address (the hardware takes wide accesses at any
+// alignment), the last 16 - valid of them zero and not read.
 __device__ __forceinline__ intx4 s8_load16(const int8_t *p, int valid) {
+  typedef int anywhere __attribute__((ext_vector_type(4), aligned(1)));
   intx4 v = {0, 0, 0, 0};
   if (valid >= 16) {
-    __builtin_memcpy(&v, p, 16);
+    v = *reinterpret_cast<const anywhere *>(p);
   } else if (valid > 0) {
 #pragma unroll
     for (int e = 0; e < 15; ++e)
@@ -97,63 +101,40 @@ __device__ __forceinline__ intx4 s8_load16(const int8_t *p, int valid) {
   return v;
 }
 
-// Buffer loads and stores of 4 elements or one, at a byte offset (kOob: zero,
-// or nothing stored).
-template <class F>
-__device__ __forceinline__ void s8_load4(__amdgpu_buffer_rsrc_t rs, uint32_t off, float (&v)[4]) {
-  if constexpr (sizeof(F) == 4) {
-    const floatx4 w = __builtin_bit_cast(floatx4, __builtin_amdgcn_raw_buffer_load_b128(rs, off, 0, 0));
-#pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = w[e];
-  } else {
-    typedef F f4 __attribute__((ext_vector_type(4)));
-    const f4 w = __builtin_bit_cast(f4, __builtin_amdgcn_raw_buffer_load_b64(rs, off, 0, 0));
-#pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = (float)w[e];
-  }
-}
-template <class F>
-__device__ __forceinline__ float s8_load1(__amdgpu_buffer_rsrc_t rs, uint32_t off) {
-  if constexpr (sizeof(F) == 4)
-    return __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(rs, off, 0, 0));
-  else
-    return (float)__builtin_bit_cast(F, (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(rs, off, 0, 0));
-}
-template <class F, int RUN>
-__device__ __forceinline__ void s8_store_run(__amdgpu_buffer_rsrc_t rs, uint32_t off, const float (&v)[RUN]) {
-  typedef unsigned uintx4 __attribute__((ext_vector_type(4)));
-  typedef unsigned uintx2 __attribute__((ext_vector_type(2)));
-  if constexpr (sizeof(F) == 4) {
-    typedef F f4 __attribute__((ext_vector_type(4)));
-#pragma unroll
-    for (int g = 0; g < RUN; g += 4) {
-      const f4 w = {v[g], v[g + 1], v[g + 2], v[g + 3]};
-      __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(uintx4, w), rs, off + 4 * g, 0, 0);
-    }
-  } else {
-    typedef F fr __attribute__((ext_vector_type(RUN)));
-    fr w;
-#pragma unroll
-    for (int e = 0; e < RUN; ++e) w[e] = (F)v[e];
-    if constexpr (RUN == 8)
-      __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(uintx4, w), rs, off, 0, 0);
-    else
-      __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(uintx2, w), rs, off, 0, 0);
-  }
-}
-template <class F>
-__device__ __forceinline__ void s8_store1(__amdgpu_buffer_rsrc_t rs, uint32_t off, float v) {
-  if constexpr (sizeof(F) == 4)
-    __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(unsigned, v), rs, off, 0, 0);
-  else
-    __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, (F)v), rs, off, 0, 0);
+// One float at a byte offset of a buffer (kOob: zero).
+__device__ __forceinline__ float s8_float(__amdgpu_buffer_rsrc_t rs, uint32_t off) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(rs, off, 0, 0));
 }
 
-// Whether every run of `run` columns is inside C or outside it, and aligned
-// to its bytes (16 at most).
-__device__ __forceinline__ bool s8_whole_runs(const S8Args &a, int run) {
-  const int size = a.type == kTypeF32 ? 4 : 2;
-  return (uintptr_t)a.C % 16 == 0 && a.ldc * size % 16 == 0 && a.N % run == 0;
+// A run of columns of C: scaled sums, plus beta C and the bias, through the
+// activation, in 32 bits, rounded once to C's type.  `cols`: the run's columns
+// that are in C.  Wide accesses at any alignment of the element.
+template <class F, int RUN>
+__device__ __forceinline__ void s8_finish_run(const S8Args &a, F *c, int cols, float (&v)[RUN],
+                                              const float (&bias)[RUN]) {
+  typedef F fr __attribute__((ext_vector_type(RUN)));
+  typedef F anywhere __attribute__((ext_vector_type(RUN), aligned(alignof(F))));
+  fr w = {};
+  if (a.beta != 0.0f) {
+    if (cols >= RUN) {
+      w = *reinterpret_cast<const anywhere *>(c);
+    } else {
+#pragma unroll
+      for (int e = 0; e < RUN; ++e)
+        if (e < cols) w[e] = c[e];
+    }
+#pragma unroll
+    for (int e = 0; e < RUN; ++e) v[e] += a.beta * (float)w[e];
+  }
+#pragma unroll
+  for (int e = 0; e < RUN; ++e) w[e] = (F)apply_act(v[e] + bias[e], a.act);
+  if (cols >= RUN) {
+    *reinterpret_cast<anywhere *>(c) = w;
+  } else {
+#pragma unroll
+    for (int e = 0; e < RUN; ++e)
+      if (e < cols) c[e] = w[e];
+  }
 }
 
 template <class T, bool DMA>
@@ -224,31 +205,39 @@ __global__ void __launch_bounds__(T::NT) s8_kernel(S8Args a, int tiles_m, int ti
 
   const __amdgpu_buffer_rsrc_t rs_a = make_rsrc(Ag);
   const __amdgpu_buffer_rsrc_t rs_b = make_rsrc(Bg);
-  intx4 sta[DMA ? 1 : T::NIA], stb[DMA ? 1 : T::NIB];
-  (void)sta;
-  (void)stb;
-  // the register path: global loads of a stage, and the writes to LDS
-  auto fetch = [&](int st) {
+  // The register path: D stages' global loads in registers, and the writes to
+  // LDS.  Rows past the matrix read its last row instead (they are multiplied,
+  // and not stored), so only the last stage has anything to mask.
+  constexpr int D = DMA ? 1 : T::REG;
+  struct Regs {
+    intx4 a[DMA ? 1 : T::NIA], b[DMA ? 1 : T::NIB];
+  };
+  Regs ring[D];
+  (void)ring;
+  auto fetch = [&](Regs &f, int st) {
     if constexpr (!DMA) {
-      const int k0 = st * SB * KS, kvalid = a.K - k0;
+      const int k0 = st * SB * KS;
+      const bool inside = st + 1 < nst;
 #pragma unroll
-      for (int q = 0; q < T::NIA; ++q)
-        sta[q] = s8_load16(Ag + (size_t)rowa[q] * a.lda + k0 + cola[q],
-                           rowa[q] < rows ? kvalid - cola[q] : 0);
+      for (int q = 0; q < T::NIA; ++q) {
+        const int8_t *p = Ag + k0 + (uint32_t)(min(rowa[q], rows - 1) * a.lda + cola[q]);
+        f.a[q] = s8_load16(p, inside ? 16 : a.K - k0 - cola[q]);
+      }
 #pragma unroll
-      for (int q = 0; q < T::NIB; ++q)
-        stb[q] = s8_load16(Bg + (size_t)rowb[q] * a.ldb + k0 + colb[q],
-                           rowb[q] < cols ? kvalid - colb[q] : 0);
+      for (int q = 0; q < T::NIB; ++q) {
+        const int8_t *p = Bg + k0 + (uint32_t)(min(rowb[q], cols - 1) * a.ldb + colb[q]);
+        f.b[q] = s8_load16(p, inside ? 16 : a.K - k0 - colb[q]);
+      }
     }
   };
-  auto commit = [&](char *buf) {
+  auto commit = [&](const Regs &f, char *buf) {
     if constexpr (!DMA) {
 #pragma unroll
-      for (int q = 0; q < T::NIA; ++q) *reinterpret_cast<intx4 *>(buf + dst_a(q) + 16 * lane) = sta[q];
+      for (int q = 0; q < T::NIA; ++q) *reinterpret_cast<intx4 *>(buf + dst_a(q) + 16 * lane) = f.a[q];
 #pragma unroll
-      for (int q = 0; q < T::NIB; ++q) *reinterpret_cast<intx4 *>(buf + dst_b(q) + 16 * lane) = stb[q];
+      for (int q = 0; q < T::NIB; ++q) *reinterpret_cast<intx4 *>(buf + dst_b(q) + 16 * lane) = f.b[q];
     } else {
-      (void)buf;
+      (void)f; (void)buf;
     }
   };
   // Publishes a stage to the waves that share it, or frees its buffer.
@@ -372,17 +361,24 @@ __global__ void __launch_bounds__(T::NT) s8_kernel(S8Args a, int tiles_m, int ti
     }
     s8_wait_vm<0>();  // the masked loads have written their zeros
   } else {
-    fetch(0);
-    for (int st = 0; st < nst; ++st) {
-      char *cur = lds + (st & 1) * T::STAGE;
-      commit(cur);
-      meet();
-      if (st + 1 < nst) fetch(st + 1);  // into registers
 #pragma unroll
-      for (int s = 0; s < T::STEPS; ++s) {
-        read(cur, s, fr[s & 1]);
+    for (int u = 0; u < D; ++u)
+      if (u < nst) fetch(ring[u], u);
+    for (int s0 = 0; s0 < nst; s0 += D) {
 #pragma unroll
-        for (int i = 0; i < T::TM; ++i) mma_row(fr[s & 1], i);
+      for (int u = 0; u < D; ++u) {
+        const int st = s0 + u;
+        if (st >= nst) break;
+        char *cur = lds + (st & 1) * T::STAGE;
+        commit(ring[u], cur);
+        meet();
+        if (st + D < nst) fetch(ring[u], st + D);
+#pragma unroll
+        for (int s = 0; s < T::STEPS; ++s) {
+          read(cur, s, fr[s & 1]);
+#pragma unroll
+          for (int i = 0; i < T::TM; ++i) mma_row(fr[s & 1], i);
+        }
       }
     }
   }
@@ -416,13 +412,10 @@ __global__ void __launch_bounds__(T::NT) s8_kernel(S8Args a, int tiles_m, int ti
     }
   }
 
-  // Epilogue: scales, C, bias, activation, in 32 bits, and one rounding to C's
-  // type.  A lane has RUN columns at a time of one row.
+  // Epilogue.  A lane has RUN columns at a time of one row.
   constexpr int RUN = T::RUN, RUNS = T::TN * 4 / RUN;
   // the column of run t, and its sums of block row i
-  auto run_col = [&](int t) -> int {
-    return wn * T::WN + 4 * RUN * t + RUN * lq;
-  };
+  auto run_col = [&](int t) -> int { return wn * T::WN + 4 * RUN * t + RUN * lq; };
   auto run_sum = [&](int i, int t, int e) -> int {
     if constexpr (RUN == 8) return acc[i][2 * t + (e >> 2)][e & 3];
     else return acc[i][t][e];
@@ -436,51 +429,26 @@ __global__ void __launch_bounds__(T::NT) s8_kernel(S8Args a, int tiles_m, int ti
 #pragma unroll
       for (int e = 0; e < RUN; ++e) {
         const int col = run_col(t) + e;
-        sb[t][e] = s8_load1<float>(rs_sb, col < cols ? 4u * col : kOob);
-        bias[t][e] = s8_load1<float>(rs_bias, a.bias != nullptr && col < cols ? 4u * col : kOob);
+        sb[t][e] = s8_float(rs_sb, col < cols ? 4u * col : kOob);
+        bias[t][e] = s8_float(rs_bias, a.bias != nullptr && col < cols ? 4u * col : kOob);
       }
   }
-  const bool whole = s8_whole_runs(a, RUN);
   const __amdgpu_buffer_rsrc_t rs_sa = make_rsrc(a.sA + m0);
   auto finish = [&](auto zero) {
     typedef decltype(zero) F;
-    const __amdgpu_buffer_rsrc_t rs_c = make_rsrc(static_cast<F *>(a.C) + (size_t)m0 * a.ldc + n0);
+    F *Cg = static_cast<F *>(a.C) + (size_t)m0 * a.ldc + n0;
 #pragma unroll
     for (int i = 0; i < T::TM; ++i) {
       const int m = wm * T::WM + i * 16 + lr;
-      const float sa = s8_load1<float>(rs_sa, m < rows ? 4u * m : kOob);
+      const float sa = s8_float(rs_sa, m < rows ? 4u * m : kOob);
 #pragma unroll
       for (int t = 0; t < RUNS; ++t) {
         const int col = run_col(t);
-        const uint32_t off = (uint32_t)(m * a.ldc + col) * (uint32_t)sizeof(F);
-        const uint32_t run_off = m < rows && col < cols ? off : kOob;
         float v[RUN];
 #pragma unroll
         for (int e = 0; e < RUN; ++e) v[e] = (float)run_sum(i, t, e) * sa * sb[t][e];
-        if (a.beta != 0.0f) {
-          if (whole) {
-#pragma unroll
-            for (int g = 0; g < RUN; g += 4) {
-              float c0[4];
-              s8_load4<F>(rs_c, run_off + g * (uint32_t)sizeof(F), c0);
-#pragma unroll
-              for (int e = 0; e < 4; ++e) v[g + e] += a.beta * c0[e];
-            }
-          } else {
-#pragma unroll
-            for (int e = 0; e < RUN; ++e)
-              v[e] += a.beta * s8_load1<F>(rs_c, m < rows && col + e < cols ? off + e * (uint32_t)sizeof(F) : kOob);
-          }
-        }
-#pragma unroll
-        for (int e = 0; e < RUN; ++e) v[e] = apply_act(v[e] + bias[t][e], a.act);
-        if (whole) {
-          s8_store_run<F, RUN>(rs_c, run_off, v);
-        } else {
-#pragma unroll
-          for (int e = 0; e < RUN; ++e)
-            s8_store1<F>(rs_c, m < rows && col + e < cols ? off + e * (uint32_t)sizeof(F) : kOob, v[e]);
-        }
+        if (m < rows && col < cols)
+          s8_finish_run<F, RUN>(a, Cg + (uint32_t)(m * a.ldc + col), cols - col, v, bias[t]);
       }
     }
   };

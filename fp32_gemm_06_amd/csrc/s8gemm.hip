@@ -9,37 +9,42 @@ namespace {
 // Rows of one launch: keeps the grid's threads below 2^32 for any M.
 constexpr int kMaxLaunchRows = 1 << 22;
 
-// A configuration, and its time on a shape in microseconds (M, N large against
-// the tile):  fixed + each * rounds + (first + more * (rounds - 1)) * K / 1000,
-// rounds = the tiles that a CU gets, ceil(tiles / 256).
+// A configuration, and its time on a shape in microseconds:
+//   each * rounds + fixed + (first + full * fill + more * (rounds - 1)) K / 1000
+// with rounds = ceil(tiles / 256), the tiles that a CU gets, and fill = the
+// share of those places that have one (a full chip shares L2 and power).
 struct S8Config {
   const char *name;
   int BM, BN;
-  float fixed, each, first, more;
+  float fixed, each, first, full, more;
   hipError_t (*launch)(const S8Args &, hipStream_t);
 };
 
 // BMxBN_kKS_sNST: KS slices of K a stage, NST stages in LDS.  The small tiles
 // split K over their waves and fill the CUs for few rows or columns; the
-// large ones move fewer bytes for each product.  The four numbers are fitted
-// to each configuration's times over 508 shapes (M 1 .. 4096, N 64 .. 11008,
-// K 128 .. 11008, bf16 out), and the shortest fitted time chosen: over those
-// shapes it is 2.8% above the best of them (geometric mean; 64x64_k1_s4 alone
-// 42%).
+// large ones move fewer bytes for each product.  The five numbers are fitted
+// to each configuration's times on 4645 shapes (M 1 .. 4096, N and K 64 ..
+// 11008, most of them drawn, bf16 out), and the shortest fitted time is
+// chosen: 1.5% above the best of the thirteen (geometric mean), 0.3% on the
+// shapes that take 20 us or more.  64x64_k1_s4, the best one by itself, is
+// 33% above.  On rows without alignment (2267 shapes) the same choice is 4%
+// and 0.9% above.
 #define S8_TILE(name, BM, BN, WM, WN, KS, NST, ...) \
   {name, BM, BN, __VA_ARGS__, s8_launch<S8Tile<BM, BN, WM, WN, KS, NST>>}
 const S8Config kConfigs[] = {
-    S8_TILE("16x16_k8_s4", 16, 16, 16, 16, 8, 4, 1.80f, 2.19f, 0.32f, 0.33f),
-    S8_TILE("16x16_k4_s4", 16, 16, 16, 16, 4, 4, 2.45f, 0.97f, 0.40f, 0.29f),
-    S8_TILE("16x32_k4_s4", 16, 32, 16, 32, 4, 4, 1.82f, 2.12f, 0.51f, 0.55f),
-    S8_TILE("32x32_k4_s4", 32, 32, 32, 32, 4, 4, 2.24f, 2.79f, 0.58f, 0.73f),
-    S8_TILE("64x32_k4_s3", 64, 32, 64, 32, 4, 3, 1.63f, 4.53f, 0.92f, 1.11f),
-    S8_TILE("64x64_k2_s4", 64, 64, 32, 32, 2, 4, 1.65f, 3.58f, 1.33f, 1.72f),
-    S8_TILE("64x64_k1_s4", 64, 64, 32, 32, 1, 4, 3.05f, 1.43f, 2.06f, 1.50f),
-    S8_TILE("128x64_k2_s3", 128, 64, 64, 32, 2, 3, 1.25f, 5.01f, 2.22f, 2.76f),
-    S8_TILE("128x128_k1_s4", 128, 128, 64, 32, 1, 4, 0.65f, 5.11f, 3.27f, 4.51f),
-    S8_TILE("256x128_k1_s3", 256, 128, 64, 64, 1, 3, 0.03f, 6.76f, 5.41f, 7.42f),
-    S8_TILE("256x256_k1_s2", 256, 256, 128, 64, 1, 2, 0.00f, 9.01f, 9.40f, 15.11f),
+    S8_TILE("16x16_k8_s4", 16, 16, 16, 16, 8, 4, 3.46f, 1.53f, 0.10f, 0.24f, 0.47f),
+    S8_TILE("16x16_k4_s4", 16, 16, 16, 16, 4, 4, 4.40f, 0.48f, 0.15f, 0.14f, 0.38f),
+    S8_TILE("16x32_k4_s4", 16, 32, 16, 32, 4, 4, 3.22f, 1.73f, 0.31f, 0.31f, 0.62f),
+    S8_TILE("32x32_k4_s4", 32, 32, 32, 32, 4, 4, 2.55f, 2.64f, 0.46f, 0.37f, 0.79f),
+    S8_TILE("64x32_k4_s3", 64, 32, 64, 32, 4, 3, 1.55f, 4.48f, 0.82f, 0.45f, 1.12f),
+    S8_TILE("64x64_k2_s4", 64, 64, 32, 32, 2, 4, 1.34f, 4.05f, 1.23f, 0.50f, 1.43f),
+    S8_TILE("64x64_k1_s4", 64, 64, 32, 32, 1, 4, 3.38f, 1.50f, 1.62f, 0.42f, 1.24f),
+    S8_TILE("96x64_k2_s3", 96, 64, 48, 32, 2, 3, 0.76f, 5.01f, 1.69f, 0.55f, 1.87f),
+    S8_TILE("128x128_k1_s4", 128, 128, 64, 32, 1, 4, 0.00f, 5.70f, 3.10f, 1.30f, 3.53f),
+    S8_TILE("192x128_k1_s3", 192, 128, 96, 32, 1, 3, 0.00f, 6.13f, 3.99f, 2.01f, 4.89f),
+    S8_TILE("256x128_k1_s3", 256, 128, 64, 64, 1, 3, 0.00f, 7.17f, 4.97f, 2.28f, 6.46f),
+    S8_TILE("256x192_k1_s2", 256, 192, 64, 96, 1, 2, 0.00f, 8.22f, 7.40f, 4.57f, 9.19f),
+    S8_TILE("256x256_k1_s2", 256, 256, 64, 128, 1, 2, 0.00f, 9.37f, 8.97f, 5.18f, 11.11f),
 };
 #undef S8_TILE
 constexpr int kNumConfigs = sizeof(kConfigs) / sizeof(kConfigs[0]);
@@ -50,8 +55,9 @@ int pick(int M, int N, int K) {
   for (int c = 0; c < kNumConfigs; ++c) {
     const S8Config &f = kConfigs[c];
     const float tiles = (float)((M + f.BM - 1) / f.BM) * (float)((N + f.BN - 1) / f.BN);
-    const float rounds = ceilf(tiles / 256.0f);
-    const float t = f.fixed + f.each * rounds + (f.first + f.more * (rounds - 1.0f)) * K * 1e-3f;
+    const float rounds = ceilf(tiles / 256.0f), fill = tiles / (256.0f * rounds);
+    const float t = f.fixed + f.each * rounds +
+                    (f.first + f.full * fill + f.more * (rounds - 1.0f)) * (float)K * 1e-3f;
     if (c == 0 || t < least) {
       best = c;
       least = t;
