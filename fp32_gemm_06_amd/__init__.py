@@ -1,10 +1,13 @@
-"""Python binding of libfp32gemm.so (fp32 SGEMM / small-M SGEMV for MI355X).
+"""Python binding of libfp32gemm.so (fp32 SGEMM / small-M SGEMV, and an 8-bit
+linear layer, for MI355X).
 
 Argument marshalling only: every step of the computation runs in the HIP
 kernels of the shared library.  The functions with the C names (``sgemm``,
 ``sgemv``, ``fp32gemm_*``) take the same arguments as the C entry points,
 with device pointers given as ints or torch tensors, and return the C return
-code.  ``gemm`` is a torch-tensor convenience wrapper that raises on error.
+code.  ``gemm``, ``gemm_s8``, ``quantize_s8`` and ``rmsnorm_s8`` are
+torch-tensor convenience wrappers that raise on error; the last three run on
+the tensors' device and on one of its streams, whichever device is current.
 
 PyTorch serves only for device memory and streams.  The library must be built
 (``python -m fp32_gemm_06_amd.build``); there is no fallback of any kind when
@@ -404,4 +407,193 @@ def gemm(A, B, C=None, alpha: float = 1.0, beta: float = 0.0, config: int | None
         rc = sgemm(M, N, K, float(alpha), A, lda, B, ldb, float(beta), C, ldc, stream)
     if rc != 0:
         raise Fp32GemmError(rc)
+    return C
+
+
+def _float_type(t, name):
+    import torch
+    types = {torch.float32: TYPE_F32, torch.float16: TYPE_F16, torch.bfloat16: TYPE_BF16}
+    if t.dtype not in types:
+        raise TypeError(f"{name} must be float32, float16 or bfloat16")
+    return types[t.dtype]
+
+
+def _matrix(t, name, dtype=None, allow_transposed=False):
+    """(transposed, leading dimension) of a 2-D GPU tensor, rows or columns
+    contiguous, as _layout."""
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be 2-D")
+    if t.device.type != "cuda":
+        raise ValueError(f"{name} must be a GPU tensor")
+    r, c = t.shape
+    if c <= 1 or t.stride(1) == 1:
+        ld = t.stride(0) if r > 1 else max(1, c)
+        if ld >= c:
+            return 0, max(1, ld)
+    elif allow_transposed and (r <= 1 or t.stride(0) == 1):
+        ld = t.stride(1)
+        if ld >= r:
+            return 1, ld
+    raise ValueError(f"{name} must be row-major" +
+                     (" or a transposed view of a row-major matrix" if allow_transposed else ""))
+
+
+def _vector(t, name, n, dtype):
+    if tuple(t.shape) != (n,) or t.dtype != dtype or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} vector of {n} values")
+    if t.device.type != "cuda":
+        raise ValueError(f"{name} must be a GPU tensor")
+    return t
+
+
+def _one_device(*named):
+    """The device that all the given tensors are on."""
+    dev = None
+    for name, t in named:
+        if t is None:
+            continue
+        if dev is not None and t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, the operands before it on {dev}")
+        dev = t.device
+    return dev
+
+
+class _On:
+    """The device and stream that a wrapper's call runs on: what it allocates
+    belongs to that stream, and a stream of another device is refused."""
+
+    def __init__(self, device, stream):
+        import torch
+        if stream is None:
+            stream = torch.cuda.current_stream(device)
+        elif isinstance(stream, int):
+            stream = (torch.cuda.ExternalStream(stream, device=device) if stream else
+                      torch.cuda.default_stream(device))
+        if stream.device != device:
+            raise ValueError(f"the stream is on {stream.device}, the operands on {device}")
+        self.stream = stream
+        self._context = torch.cuda.stream(stream)  # sets the device too
+
+    def __enter__(self):
+        self._context.__enter__()
+        return self.stream.cuda_stream
+
+    def __exit__(self, *exc):
+        return self._context.__exit__(*exc)
+
+
+def _codes_out(M, K, out, scales, device):
+    """Codes (rows from multiples of 16 bytes, which s8gemm reads fastest) and scales, as given or new."""
+    import torch
+    if out is None:
+        out = torch.empty((M, -(-K // 16) * 16), dtype=torch.int8, device=device)[:, :K]
+    if tuple(out.shape) != (M, K):
+        raise ValueError(f"out has shape {tuple(out.shape)}, expected {(M, K)}")
+    _, ldq = _matrix(out, "out", torch.int8)
+    if scales is None:
+        scales = torch.empty((M,), dtype=torch.float32, device=device)
+    _vector(scales, "scales", M, torch.float32)
+    return out, max(ldq, K, 1), scales
+
+
+def quantize_s8(X, out=None, scales=None, stream=None):
+    """Torch wrapper of s8_quantize: (codes, scales) of the rows of ``X``, so
+    that ``codes * scales[:, None]`` is near it.
+
+    ``X`` (float32, float16 or bfloat16) is row-major or a transposed view of
+    a row-major matrix: ``quantize_s8(W.t())`` of a weight stored K x N gives
+    its N x K codes.
+    """
+    type = _float_type(X, "X")
+    trans, ldx = _matrix(X, "X", allow_transposed=True)
+    M, K = X.shape
+    device = _one_device(("X", X), ("out", out), ("scales", scales))
+    with _On(device, stream) as s:
+        out, ldq, scales = _codes_out(M, K, out, scales, device)
+        rc = s8_quantize(trans, M, K, type, X, ldx, out, ldq, scales, s)
+    if rc != 0:
+        raise Fp32GemmError(rc)
+    return out, scales
+
+
+def rmsnorm_s8(X, weight, eps=1e-6, residual=None, residual_out=None, out=None, scales=None,
+               stream=None):
+    """Torch wrapper of s8_rmsnorm: (codes, scales, h) with ``h = X +
+    residual`` (``X`` without a residual) in their type and ``codes *
+    scales[:, None]`` near ``rmsnorm(h) * weight``.
+
+    ``residual_out`` receives h; it may be ``X`` or ``residual`` itself.  Where
+    it is None, h is a new tensor if there is a residual and ``X`` if not.
+    """
+    import torch
+    type = _float_type(X, "X")
+    _, ldx = _matrix(X, "X")
+    M, K = X.shape
+    _vector(weight, "weight", K, X.dtype)
+    device = _one_device(("X", X), ("weight", weight), ("residual", residual),
+                         ("residual_out", residual_out), ("out", out), ("scales", scales))
+    with _On(device, stream) as s:
+        h = residual_out
+        if h is None and residual is not None:
+            h = torch.empty((M, K), dtype=X.dtype, device=device)
+        lds = []
+        for name, t in (("residual", residual), ("residual_out", h)):
+            if t is not None and tuple(t.shape) != (M, K):
+                raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(M, K)}")
+            lds.append(0 if t is None else _matrix(t, name, X.dtype)[1])
+        out, ldq, scales = _codes_out(M, K, out, scales, device)
+        rc = s8_rmsnorm(M, K, type, X, ldx, residual, lds[0], h, lds[1], weight, float(eps), out, ldq,
+                        scales, s)
+    if rc != 0:
+        raise Fp32GemmError(rc)
+    return out, scales, X if h is None else h
+
+
+def gemm_s8(A, scale_a, B, scale_b, C=None, beta: float = 0.0, dtype=None, bias=None,
+            act: int | str | None = None, config: int = -1, stream=None):
+    """Torch wrapper of s8gemm: returns C = act(scale_a scale_b (A @ B) +
+    beta C + bias), C of ``dtype`` (float32 by default) allocated when None.
+
+    ``A`` (M x K int8 codes) is row-major with a scale for each row, ``B``
+    (K x N) the transposed view ``codes.t()`` of a weight's N x K codes, with
+    a scale for each of its rows.  ``bias`` (N floats) and ``act`` ("relu" or
+    ACT_RELU) as in gemm; ``config`` forces a configuration.
+    """
+    import torch
+    M, K = A.shape
+    K2, N = B.shape
+    if K2 != K:
+        raise ValueError(f"inner dimensions differ: {A.shape} @ {B.shape}")
+    _, lda = _matrix(A, "A", torch.int8)
+    try:
+        _, ldb = _matrix(B.t(), "B", torch.int8)
+    except ValueError:
+        raise ValueError("B must be the transposed view of row-major N x K codes") from None
+    _vector(scale_a, "scale_a", M, torch.float32)
+    _vector(scale_b, "scale_b", N, torch.float32)
+    if bias is not None:
+        _vector(bias, "bias", N, torch.float32)
+    if act in (None, "none"):
+        act = ACT_NONE
+    elif act == "relu":
+        act = ACT_RELU
+    if C is None and beta != 0.0:
+        raise ValueError("beta != 0 needs C")
+    device = _one_device(("A", A), ("scale_a", scale_a), ("B", B), ("scale_b", scale_b), ("bias", bias),
+                         ("C", C))
+    with _On(device, stream) as s:
+        if C is None:
+            C = torch.empty((M, N), dtype=dtype or torch.float32, device=device)
+        elif dtype is not None and C.dtype != dtype:
+            raise TypeError(f"C must be {dtype}")
+        if tuple(C.shape) != (M, N):
+            raise ValueError(f"C has shape {tuple(C.shape)}, expected {(M, N)}")
+        type = _float_type(C, "C")
+        _, ldc = _matrix(C, "C")
+        rc = fp32gemm_s8gemm_with_config(config, M, N, K, A, max(lda, K, 1), scale_a, B, max(ldb, K, 1),
+                                         scale_b, float(beta), type, C, max(ldc, N, 1), bias, int(act), s)
+    if rc != 0:
+        raise Fp32GemmError(rc if rc >= 0 or rc <= -100 else rc + 1)
     return C
