@@ -30,8 +30,9 @@
 namespace fp32gemm {
 namespace {
 
-template <int BM_, int BN_, int WM_, int WN_, int KS_, int NST_>
+template <int BM_, int BN_, int WM_, int WN_, int KS_, int NST_, bool AHEAD_>
 struct S8Tile {
+  static constexpr bool AHEAD = AHEAD_;             // operands a step ahead, in two register sets
   static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, KS = KS_, NST = NST_;
   static constexpr int SB = 128, CP = SB / 16;     // bytes and chunks of a row of a slice
   static constexpr int RL = 1024 / SB;             // rows of a 1 KB load
@@ -304,17 +305,17 @@ __global__ void __launch_bounds__(T::NT) s8_kernel(S8Args a, int tiles_m, int ti
     // NST stages in LDS.  A load instruction waits for its place in the
     // memory pipeline, and the wave with it, so a stage's loads follow the
     // barrier that freed their buffer a few at a time, between the first half
-    // of the matrix instructions that follow it too.  Operands are read one
-    // step ahead; the last step's instructions run after the barrier and cover
-    // the first reads of the next stage.  Past the end of K the loads are
-    // masked, so the count of them in flight stays.  The scheduling barriers
-    // keep the order written here.  At 4096^3, 256 x 256 tiles: all loads
-    // first, then reads and instructions as the compiler orders them, 1.75 us
-    // a stage; spread and read ahead 1.59; with the order kept 1.49 (the
-    // instructions and LDS reads alone 1.24, the loads alone 1.02).
+    // of the matrix instructions that follow it too.  Past the end of K the
+    // loads are masked, so the count of them in flight stays.  The scheduling
+    // barriers keep the order written here.  At 4096^3, 256 x 256 tiles of 8
+    // waves: all loads first, then reads and instructions as the compiler
+    // orders them, 1.75 us a stage; spread and read ahead 1.59; with the order
+    // kept 1.49 (the instructions and LDS reads alone 1.24, the loads alone
+    // 1.02).
     constexpr int NST = T::NST, NL = T::NIA + T::NIB, STEPS = T::STEPS;
     constexpr int PER_ROW = T::TM == 1 ? NL : (NL + T::TM / 2 - 1) / (T::TM / 2);
-    auto load = [&](int q, char *buf, int k0) {
+    auto load = [&](int q, char *buf, int st) {
+      const int k0 = st * SB * KS;
       if (q < T::NIA) s8_dma16(rs_a, buf + dst_a(q), offa[q < T::NIA ? q : 0], k0);
       else s8_dma16(rs_b, buf + dst_b(q - T::NIA), offb[q >= T::NIA ? q - T::NIA : 0], k0);
     };
@@ -322,41 +323,70 @@ __global__ void __launch_bounds__(T::NT) s8_kernel(S8Args a, int tiles_m, int ti
       if (st == nst - 1) set_offsets(klast);
       else if (st == nst) set_offsets(0);
     };
-    if (nst > 1) set_offsets(SB * KS);
-#pragma unroll
-    for (int st = 0; st < NST; ++st) {
-      mask_stage(st);
-#pragma unroll
-      for (int q = 0; q < NL; ++q) load(q, lds + st * T::STAGE, st * SB * KS);
-    }
-    s8_wait_vm<(NST - 1) * NL>();
-    meet();
-    if (nst == 1) clear_tail(lds);
-    read(lds, 0, fr[0]);
-    int at = 0;  // buffer of stage st
-    for (int st = 0; st < nst; ++st) {
-      char *cur = lds + at * T::STAGE;
-#pragma unroll
-      for (int s = 0; s + 1 < STEPS; ++s) {
-        read(cur, s + 1, fr[(s + 1) & 1]);
-#pragma unroll
-        for (int i = 0; i < T::TM; ++i) mma_row(fr[s & 1], i);
-      }
-      s8_wait_vm<(NST - 2) * NL>();  // stage st + 1 has landed
-      meet();                        // for every wave, and this stage's buffer is free
-      at = at + 1 == NST ? 0 : at + 1;
-      if (st + 1 < nst) {
-        if (st + 2 == nst) clear_tail(lds + at * T::STAGE);
-        read(lds + at * T::STAGE, 0, fr[0]);
-      }
-      mask_stage(st + NST);
+    // one step's instructions, and stage st's loads into buf between them
+    auto multiply_and_load = [&](const Frag &f, char *buf, int st) {
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int i = 0; i < T::TM; ++i) {
-        mma_row(fr[(STEPS - 1) & 1], i);
+        mma_row(f, i);
 #pragma unroll
-        for (int q = i * PER_ROW; q < (i + 1) * PER_ROW && q < NL; ++q) load(q, cur, (st + NST) * SB * KS);
+        for (int q = i * PER_ROW; q < (i + 1) * PER_ROW && q < NL; ++q) load(q, buf, st);
         __builtin_amdgcn_sched_barrier(0);
+      }
+    };
+    // stages in flight before the first is multiplied
+    constexpr int FIRST = T::AHEAD ? NST : NST - 1;
+    if (nst > 1) set_offsets(SB * KS);
+#pragma unroll
+    for (int st = 0; st < FIRST; ++st) {
+      mask_stage(st);
+#pragma unroll
+      for (int q = 0; q < NL; ++q) load(q, lds + st * T::STAGE, st);
+    }
+    int at = 0;  // buffer of stage st
+    if constexpr (T::AHEAD) {
+      // The last step's instructions run after the barrier and cover the
+      // first reads of the next stage.
+      s8_wait_vm<(NST - 1) * NL>();
+      meet();
+      if (nst == 1) clear_tail(lds);
+      read(lds, 0, fr[0]);
+      for (int st = 0; st < nst; ++st) {
+        char *cur = lds + at * T::STAGE;
+#pragma unroll
+        for (int s = 0; s + 1 < STEPS; ++s) {
+          read(cur, s + 1, fr[(s + 1) & 1]);
+#pragma unroll
+          for (int i = 0; i < T::TM; ++i) mma_row(fr[s & 1], i);
+        }
+        s8_wait_vm<(NST - 2) * NL>();  // stage st + 1 has landed
+        meet();                        // for every wave, and this stage's buffer is free
+        at = at + 1 == NST ? 0 : at + 1;
+        if (st + 1 < nst) {
+          if (st + 2 == nst) clear_tail(lds + at * T::STAGE);
+          read(lds + at * T::STAGE, 0, fr[0]);
+        }
+        mask_stage(st + NST);
+        multiply_and_load(fr[(STEPS - 1) & 1], cur, st + NST);
+      }
+    } else {
+      // One register set: four waves on a SIMD cover each other's reads.
+      for (int st = 0; st < nst; ++st) {
+        char *cur = lds + at * T::STAGE;
+        char *old = lds + (at == 0 ? NST - 1 : at - 1) * T::STAGE;
+        s8_wait_vm<(NST - 2) * NL>();  // this stage has landed
+        meet();                        // for every wave, and the buffer of the one before is free
+        if (st + 1 == nst) clear_tail(cur);
+        mask_stage(st + NST - 1);
+        read(cur, 0, fr[0]);
+        multiply_and_load(fr[0], old, st + NST - 1);
+#pragma unroll
+        for (int s = 1; s < STEPS; ++s) {
+          read(cur, s, fr[0]);
+#pragma unroll
+          for (int i = 0; i < T::TM; ++i) mma_row(fr[0], i);
+        }
+        at = at + 1 == NST ? 0 : at + 1;
       }
     }
     s8_wait_vm<0>();  // the masked loads have written their zeros
@@ -375,9 +405,9 @@ __global__ void __launch_bounds__(T::NT) s8_kernel(S8Args a, int tiles_m, int ti
         if (st + D < nst) fetch(ring[u], st + D);
 #pragma unroll
         for (int s = 0; s < T::STEPS; ++s) {
-          read(cur, s, fr[s & 1]);
+          read(cur, s, fr[0]);
 #pragma unroll
-          for (int i = 0; i < T::TM; ++i) mma_row(fr[s & 1], i);
+          for (int i = 0; i < T::TM; ++i) mma_row(fr[0], i);
         }
       }
     }
@@ -464,13 +494,14 @@ inline bool s8_dma_ok(const S8Args &a) {
   return (uintptr_t)a.A % 16 == 0 && (uintptr_t)a.B % 16 == 0 && a.lda % 16 == 0 && a.ldb % 16 == 0;
 }
 
-template <class T> hipError_t s8_launch(const S8Args &a, hipStream_t s) {
+// T on rows of 16-byte chunks, TR (the same tile) through registers.
+template <class T, class TR> hipError_t s8_launch(const S8Args &a, hipStream_t s) {
   const int tm = (a.M + T::BM - 1) / T::BM, tn = (a.N + T::BN - 1) / T::BN;
   constexpr int group_m = 4;
   if (s8_dma_ok(a))
     s8_kernel<T, true><<<tm * tn, T::NT, 0, s>>>(a, tm, tn, group_m);
   else
-    s8_kernel<T, false><<<tm * tn, T::NT, 0, s>>>(a, tm, tn, group_m);
+    s8_kernel<TR, false><<<tm * tn, TR::NT, 0, s>>>(a, tm, tn, group_m);
   return hipGetLastError();
 }
 

@@ -22,29 +22,35 @@ struct S8Config {
 
 // BMxBN_kKS_sNST: KS slices of K a stage, NST stages in LDS.  The small tiles
 // split K over their waves and fill the CUs for few rows or columns; the
-// large ones move fewer bytes for each product.  The five numbers are fitted
-// to each configuration's times on 4645 shapes (M 1 .. 4096, N and K 64 ..
-// 11008, most of them drawn, bf16 out), and the shortest fitted time is
-// chosen: 1.5% above the best of the thirteen (geometric mean), 0.3% on the
-// shapes that take 20 us or more.  64x64_k1_s4, the best one by itself, is
-// 33% above.  On rows without alignment (2267 shapes) the same choice is 4%
-// and 0.9% above.
-#define S8_TILE(name, BM, BN, WM, WN, KS, NST, ...) \
-  {name, BM, BN, __VA_ARGS__, s8_launch<S8Tile<BM, BN, WM, WN, KS, NST>>}
+// large ones move fewer bytes for each product.  Sixteen waves where a CU
+// holds one workgroup: a wave's loads reach LDS at 8 to 13 bytes/ns, and more
+// waves move more (256 x 128 tiles, 1536 x 4096 x 4096: 31.8 us with 16
+// waves, 35.7 with 8).  The five numbers are fitted to each configuration's
+// times on 4339 shapes (M 1 .. 4096, N and K 64 .. 11008, most of them drawn,
+// bf16 out), and the shortest fitted time is chosen: 1.5% above the best of
+// the fourteen (geometric mean), 0.8% on the shapes that take 20 us or more.
+// 64x64_k1_s4, the best one by itself, is 31% above.  On rows without
+// alignment (1902 shapes) the same choice is 5% above.
+#define S8_TILE(name, BM, BN, WM, WN, KS, NST, AHEAD, ...) \
+  {name, BM, BN, __VA_ARGS__,                                               \
+   s8_launch<S8Tile<BM, BN, WM, WN, KS, NST, AHEAD>, S8Tile<BM, BN, WM, WN, KS, NST, AHEAD>>}
 const S8Config kConfigs[] = {
-    S8_TILE("16x16_k8_s4", 16, 16, 16, 16, 8, 4, 3.46f, 1.53f, 0.10f, 0.24f, 0.47f),
-    S8_TILE("16x16_k4_s4", 16, 16, 16, 16, 4, 4, 4.40f, 0.48f, 0.15f, 0.14f, 0.38f),
-    S8_TILE("16x32_k4_s4", 16, 32, 16, 32, 4, 4, 3.22f, 1.73f, 0.31f, 0.31f, 0.62f),
-    S8_TILE("32x32_k4_s4", 32, 32, 32, 32, 4, 4, 2.55f, 2.64f, 0.46f, 0.37f, 0.79f),
-    S8_TILE("64x32_k4_s3", 64, 32, 64, 32, 4, 3, 1.55f, 4.48f, 0.82f, 0.45f, 1.12f),
-    S8_TILE("64x64_k2_s4", 64, 64, 32, 32, 2, 4, 1.34f, 4.05f, 1.23f, 0.50f, 1.43f),
-    S8_TILE("64x64_k1_s4", 64, 64, 32, 32, 1, 4, 3.38f, 1.50f, 1.62f, 0.42f, 1.24f),
-    S8_TILE("96x64_k2_s3", 96, 64, 48, 32, 2, 3, 0.76f, 5.01f, 1.69f, 0.55f, 1.87f),
-    S8_TILE("128x128_k1_s4", 128, 128, 64, 32, 1, 4, 0.00f, 5.70f, 3.10f, 1.30f, 3.53f),
-    S8_TILE("192x128_k1_s3", 192, 128, 96, 32, 1, 3, 0.00f, 6.13f, 3.99f, 2.01f, 4.89f),
-    S8_TILE("256x128_k1_s3", 256, 128, 64, 64, 1, 3, 0.00f, 7.17f, 4.97f, 2.28f, 6.46f),
-    S8_TILE("256x192_k1_s2", 256, 192, 64, 96, 1, 2, 0.00f, 8.22f, 7.40f, 4.57f, 9.19f),
-    S8_TILE("256x256_k1_s2", 256, 256, 64, 128, 1, 2, 0.00f, 9.37f, 8.97f, 5.18f, 11.11f),
+    S8_TILE("16x16_k8_s4", 16, 16, 16, 16, 8, 4, true, 3.65f, 1.46f, 0.09f, 0.22f, 0.49f),
+    S8_TILE("16x16_k4_s4", 16, 16, 16, 16, 4, 4, true, 4.58f, 0.43f, 0.14f, 0.14f, 0.39f),
+    S8_TILE("16x32_k4_s4", 16, 32, 16, 32, 4, 4, true, 3.40f, 1.66f, 0.28f, 0.31f, 0.63f),
+    S8_TILE("32x32_k4_s4", 32, 32, 32, 32, 4, 4, true, 2.55f, 2.68f, 0.44f, 0.40f, 0.77f),
+    S8_TILE("64x32_k4_s3", 64, 32, 32, 32, 4, 3, true, 1.90f, 3.65f, 0.82f, 0.39f, 1.15f),
+    S8_TILE("64x64_k2_s4", 64, 64, 16, 32, 2, 4, true, 1.76f, 3.61f, 1.16f, 0.64f, 1.64f),
+    S8_TILE("64x64_k1_s4", 64, 64, 16, 32, 1, 4, true, 3.50f, 1.37f, 1.39f, 0.55f, 1.41f),
+    S8_TILE("96x64_k2_s3", 96, 64, 48, 32, 2, 3, true, 0.77f, 4.98f, 1.66f, 0.61f, 1.99f),
+    S8_TILE("128x64_k1_s3", 128, 64, 32, 32, 1, 3, true, 2.93f, 2.11f, 1.85f, 0.97f, 2.01f),
+    S8_TILE("128x128_k1_s4", 128, 128, 32, 32, 1, 4, true, 0.00f, 5.65f, 2.32f, 2.23f, 3.55f),
+    S8_TILE("192x128_k1_s2", 192, 128, 96, 32, 1, 2, false, 0.28f, 5.07f, 4.93f, 2.94f, 3.14f),
+    S8_TILE("256x128_k1_s3", 256, 128, 64, 32, 1, 3, true, 0.00f, 6.13f, 3.94f, 3.39f, 6.64f),
+    S8_TILE("256x192_k1_s2", 256, 192, 64, 96, 1, 2, false, 0.00f, 7.47f, 7.80f, 3.96f, 10.63f),
+    // 16 waves have no registers left for the path through them
+    {"256x256_k1_s2", 256, 256, 0.00f, 6.82f, 8.54f, 6.08f, 12.60f,
+     s8_launch<S8Tile<256, 256, 64, 64, 1, 2, false>, S8Tile<256, 256, 64, 128, 1, 2, true>>},
 };
 #undef S8_TILE
 constexpr int kNumConfigs = sizeof(kConfigs) / sizeof(kConfigs[0]);
