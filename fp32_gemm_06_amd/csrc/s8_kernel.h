@@ -107,12 +107,29 @@ __device__ __forceinline__ float s8_float(__amdgpu_buffer_rsrc_t rs, uint32_t of
   return __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(rs, off, 0, 0));
 }
 
-// A run of columns of C: scaled sums, plus beta C and the bias, through the
+// N floats from p, zeros past the first n of them (which are all there is).
+template <int N> struct Floats {
+  typedef float type __attribute__((ext_vector_type(N)));
+  typedef float anywhere __attribute__((ext_vector_type(N), aligned(4)));
+};
+template <int N> __device__ __forceinline__ void s8_floats(const float *p, int n, float (&v)[N]) {
+  typename Floats<N>::type w = {};
+  if (n >= N) {
+    w = *reinterpret_cast<const typename Floats<N>::anywhere *>(p);
+  } else {
+#pragma unroll
+    for (int e = 0; e < N; ++e)
+      if (e < n) w[e] = p[e];
+  }
+#pragma unroll
+  for (int e = 0; e < N; ++e) v[e] = w[e];
+}
+
+// A run of columns of C: scaled sums and bias in v, plus beta C, through the
 // activation, in 32 bits, rounded once to C's type.  `cols`: the run's columns
 // that are in C.  Wide accesses at any alignment of the element.
 template <class F, int RUN>
-__device__ __forceinline__ void s8_finish_run(const S8Args &a, F *c, int cols, float (&v)[RUN],
-                                              const float (&bias)[RUN]) {
+__device__ __forceinline__ void s8_finish_run(const S8Args &a, F *c, int cols, float (&v)[RUN]) {
   typedef F fr __attribute__((ext_vector_type(RUN)));
   typedef F anywhere __attribute__((ext_vector_type(RUN), aligned(alignof(F))));
   fr w = {};
@@ -125,10 +142,14 @@ __device__ __forceinline__ void s8_finish_run(const S8Args &a, F *c, int cols, f
         if (e < cols) w[e] = c[e];
     }
 #pragma unroll
-    for (int e = 0; e < RUN; ++e) v[e] += a.beta * (float)w[e];
+    for (int e = 0; e < RUN; ++e) v[e] = __builtin_fmaf(a.beta, (float)w[e], v[e]);
+  }
+  if (a.act != kActNone) {
+#pragma unroll
+    for (int e = 0; e < RUN; ++e) v[e] = apply_act(v[e], kActRelu);
   }
 #pragma unroll
-  for (int e = 0; e < RUN; ++e) w[e] = (F)apply_act(v[e] + bias[e], a.act);
+  for (int e = 0; e < RUN; ++e) w[e] = (F)v[e];
   if (cols >= RUN) {
     *reinterpret_cast<anywhere *>(c) = w;
   } else {
@@ -442,7 +463,10 @@ __global__ void __launch_bounds__(T::NT) s8_kernel(S8Args a, int tiles_m, int ti
     }
   }
 
-  // Epilogue.  A lane has RUN columns at a time of one row.
+  // Epilogue.  A lane has RUN columns at a time of one row.  What it costs is
+  // instructions (64 elements a lane of a 256 x 256 tile): the conversion, a
+  // multiplication, a fused one with the bias, the rounding, and the rest only
+  // where it is asked for.
   constexpr int RUN = T::RUN, RUNS = T::TN * 4 / RUN;
   // the column of run t, and its sums of block row i
   auto run_col = [&](int t) -> int { return wn * T::WN + 4 * RUN * t + RUN * lq; };
@@ -450,18 +474,12 @@ __global__ void __launch_bounds__(T::NT) s8_kernel(S8Args a, int tiles_m, int ti
     if constexpr (RUN == 8) return acc[i][2 * t + (e >> 2)][e & 3];
     else return acc[i][t][e];
   };
-  float sb[RUNS][RUN], bias[RUNS][RUN];
-  {
-    const __amdgpu_buffer_rsrc_t rs_sb = make_rsrc(a.sB + n0);
-    const __amdgpu_buffer_rsrc_t rs_bias = make_rsrc(a.bias != nullptr ? a.bias + n0 : a.sB);
+  float sb[RUNS][RUN], bias[RUNS][RUN] = {};
 #pragma unroll
-    for (int t = 0; t < RUNS; ++t)
+  for (int t = 0; t < RUNS; ++t) s8_floats<RUN>(a.sB + n0 + run_col(t), cols - run_col(t), sb[t]);
+  if (a.bias != nullptr) {
 #pragma unroll
-      for (int e = 0; e < RUN; ++e) {
-        const int col = run_col(t) + e;
-        sb[t][e] = s8_float(rs_sb, col < cols ? 4u * col : kOob);
-        bias[t][e] = s8_float(rs_bias, a.bias != nullptr && col < cols ? 4u * col : kOob);
-      }
+    for (int t = 0; t < RUNS; ++t) s8_floats<RUN>(a.bias + n0 + run_col(t), cols - run_col(t), bias[t]);
   }
   const __amdgpu_buffer_rsrc_t rs_sa = make_rsrc(a.sA + m0);
   auto finish = [&](auto zero) {
@@ -476,9 +494,9 @@ __global__ void __launch_bounds__(T::NT) s8_kernel(S8Args a, int tiles_m, int ti
         const int col = run_col(t);
         float v[RUN];
 #pragma unroll
-        for (int e = 0; e < RUN; ++e) v[e] = (float)run_sum(i, t, e) * sa * sb[t][e];
+        for (int e = 0; e < RUN; ++e) v[e] = __builtin_fmaf((float)run_sum(i, t, e) * sa, sb[t][e], bias[t][e]);
         if (m < rows && col < cols)
-          s8_finish_run<F, RUN>(a, Cg + (uint32_t)(m * a.ldc + col), cols - col, v, bias[t]);
+          s8_finish_run<F, RUN>(a, Cg + (uint32_t)(m * a.ldc + col), cols - col, v);
       }
     }
   };
