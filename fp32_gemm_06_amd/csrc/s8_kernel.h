@@ -262,13 +262,12 @@ __global__ void __launch_bounds__(T::NT) s8_kernel(S8Args a, int tiles_m, int ti
       (void)f; (void)buf;
     }
   };
-  // Publishes a stage to the waves that share it, or frees its buffer.
+  // Publishes a stage to the waves that share it, or frees its buffer: this
+  // wave's LDS accesses are done, and the others' too.  (Not __syncthreads,
+  // whose fence may wait for the loads in flight as well.)
   auto meet = [&]() {
-    if constexpr (T::OWN) {
-      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    } else {
-      __syncthreads();
-    }
+    if constexpr (T::OWN) asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    else asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
   };
   // After the last stage has landed: the chunk of A's rows that K ends in.
   auto clear_tail = [&](char *buf) {
