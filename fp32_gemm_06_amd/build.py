@@ -20,7 +20,7 @@ PROBES = {"hbm_probe.hip": os.path.join(HERE, "libhbmprobe.so"),
           "mfma_probe.hip": os.path.join(HERE, "libmfmaprobe.so")}
 SOURCES = ["api.hip", "dispatch.hip", "sgemm_configs.hip", "sgemm_nn.hip", "sgemm_nt.hip",
            "sgemm_tn.hip", "sgemm_tt.hip", "sgemv.hip", "gemv_split.hip", "skinny.hip",
-           "splitk.hip", "streamk.hip", "s8gemm.hip", "s8_rows.hip"]
+           "splitk.hip", "streamk.hip", "s8gemm.hip", "s8_gemv.hip", "s8_rows.hip"]
 ARCH = "gfx950"
 
 FLAGS = [

@@ -34,6 +34,10 @@ int s8_num_configs();
 const char *s8_config_name(int cfg);
 int select_s8_config(int M, int N, int K);
 
+// Dot products for few rows (s8_gemv.hip).
+hipError_t launch_s8_gemv_r2(const S8Args &a, hipStream_t s);
+hipError_t launch_s8_gemv_r2k4(const S8Args &a, hipStream_t s);
+
 // C <- act(beta C + bias): the product over an empty K.
 hipError_t launch_s8_epilogue_only(const S8Args &a, hipStream_t s);
 

@@ -87,17 +87,30 @@ __device__ __forceinline__ void s8_dma16(__amdgpu_buffer_rsrc_t rs, char *dst, u
 #endif
 }
 
-// 16 codes from any address (the hardware takes wide accesses at any
-// alignment), the last 16 - valid of them zero and not read.
-__device__ __forceinline__ intx4 s8_load16(const int8_t *p, int valid) {
+// 16 codes of a row of K from any address (the hardware takes wide accesses at
+// any alignment), zero past the first `valid` of them, which end the row.  The
+// row's last 16 are read then and moved down; only a row shorter than that is
+// read byte by byte.
+__device__ __forceinline__ intx4 s8_load16(const int8_t *p, int valid, int K) {
   typedef int anywhere __attribute__((ext_vector_type(4), aligned(1)));
+  typedef unsigned long long longx2 __attribute__((ext_vector_type(2)));
   intx4 v = {0, 0, 0, 0};
   if (valid >= 16) {
     v = *reinterpret_cast<const anywhere *>(p);
   } else if (valid > 0) {
+    if (K >= 16) {
+      v = *reinterpret_cast<const anywhere *>(p + valid - 16);
+      const longx2 w = __builtin_bit_cast(longx2, v);
+      const unsigned long long lo = w[0], hi = w[1];
+      const int bits = 8 * (16 - valid);  // 8 .. 120
+      const longx2 moved = {bits < 64 ? lo >> bits | hi << (64 - bits) : hi >> (bits - 64),
+                            bits < 64 ? hi >> bits : 0ull};
+      v = __builtin_bit_cast(intx4, moved);
+    } else {
 #pragma unroll
-    for (int e = 0; e < 15; ++e)
-      if (e < valid) v[e / 4] |= (int)(uint8_t)p[e] << (8 * (e % 4));
+      for (int e = 0; e < 15; ++e)
+        if (e < valid) v[e / 4] |= (int)(uint8_t)p[e] << (8 * (e % 4));
+    }
   }
   return v;
 }
@@ -157,6 +170,12 @@ __device__ __forceinline__ void s8_finish_run(const S8Args &a, F *c, int cols, f
     for (int e = 0; e < RUN; ++e)
       if (e < cols) c[e] = w[e];
   }
+}
+
+// One element of C, the same way.
+template <class F> __device__ __forceinline__ void s8_finish_one(const S8Args &a, F *c, float v) {
+  if (a.beta != 0.0f) v = __builtin_fmaf(a.beta, (float)*c, v);
+  *c = (F)apply_act(v, a.act);
 }
 
 template <class T, bool DMA>
@@ -243,12 +262,12 @@ __global__ void __launch_bounds__(T::NT) s8_kernel(S8Args a, int tiles_m, int ti
 #pragma unroll
       for (int q = 0; q < T::NIA; ++q) {
         const int8_t *p = Ag + k0 + (uint32_t)(min(rowa[q], rows - 1) * a.lda + cola[q]);
-        f.a[q] = s8_load16(p, inside ? 16 : a.K - k0 - cola[q]);
+        f.a[q] = s8_load16(p, inside ? 16 : a.K - k0 - cola[q], a.K);
       }
 #pragma unroll
       for (int q = 0; q < T::NIB; ++q) {
         const int8_t *p = Bg + k0 + (uint32_t)(min(rowb[q], cols - 1) * a.ldb + colb[q]);
-        f.b[q] = s8_load16(p, inside ? 16 : a.K - k0 - colb[q]);
+        f.b[q] = s8_load16(p, inside ? 16 : a.K - k0 - colb[q], a.K);
       }
     }
   };

@@ -6,8 +6,9 @@
 namespace fp32gemm {
 namespace {
 
-// Rows of one launch: keeps the grid's threads below 2^32 for any M.
-constexpr int kMaxLaunchRows = 1 << 22;
+// Tiles of one launch: keeps the grid's threads below 2^32 (and its second
+// dimension, which the dot products use for rows, below 2^16).
+constexpr long long kMaxLaunchTiles = 1 << 21;
 
 // A configuration, and its time on a shape in microseconds:
 //   each * rounds + fixed + (first + full * fill + more * (rounds - 1)) K / 1000
@@ -20,51 +21,61 @@ struct S8Config {
   hipError_t (*launch)(const S8Args &, hipStream_t);
 };
 
+// gemv_rR: dot products, R rows of W a wave (kKW: KW waves split K).
 // BMxBN_kKS_sNST: KS slices of K a stage, NST stages in LDS.  The small tiles
 // split K over their waves and fill the CUs for few rows or columns; the
 // large ones move fewer bytes for each product.  Sixteen waves where a CU
 // holds one workgroup: a wave's loads reach LDS at 8 to 13 bytes/ns, and more
 // waves move more (256 x 128 tiles, 1536 x 4096 x 4096: 31.8 us with 16
 // waves, 35.7 with 8).  The five numbers are fitted to each configuration's
-// times on 4339 shapes (M 1 .. 4096, N and K 64 .. 11008, most of them drawn,
-// bf16 out), and the shortest fitted time is chosen: 1.5% above the best of
-// the fourteen (geometric mean), 0.8% on the shapes that take 20 us or more.
-// 64x64_k1_s4, the best one by itself, is 31% above.  On rows without
-// alignment (1902 shapes) the same choice is 5% above.
+// times on 6831 shapes (M 1 .. 4096, N and K 64 .. 11008, most of them drawn,
+// bf16 out), and the shortest fitted time is chosen: 2.5% above the best of
+// the sixteen (geometric mean), 0.9% on the shapes that take 20 us or more.
+// 64x64_k1_s4, the best one by itself, is 40% above.  On rows without
+// alignment (4618 shapes) the same choice is 4% and 2% above.
 #define S8_TILE(name, BM, BN, WM, WN, KS, NST, AHEAD, ...) \
   {name, BM, BN, __VA_ARGS__,                                               \
    s8_launch<S8Tile<BM, BN, WM, WN, KS, NST, AHEAD>, S8Tile<BM, BN, WM, WN, KS, NST, AHEAD>>}
 const S8Config kConfigs[] = {
-    S8_TILE("16x16_k8_s4", 16, 16, 16, 16, 8, 4, true, 3.65f, 1.46f, 0.09f, 0.22f, 0.49f),
-    S8_TILE("16x16_k4_s4", 16, 16, 16, 16, 4, 4, true, 4.58f, 0.43f, 0.14f, 0.14f, 0.39f),
-    S8_TILE("16x32_k4_s4", 16, 32, 16, 32, 4, 4, true, 3.40f, 1.66f, 0.28f, 0.31f, 0.63f),
-    S8_TILE("32x32_k4_s4", 32, 32, 32, 32, 4, 4, true, 2.55f, 2.68f, 0.44f, 0.40f, 0.77f),
-    S8_TILE("64x32_k4_s3", 64, 32, 32, 32, 4, 3, true, 1.90f, 3.65f, 0.82f, 0.39f, 1.15f),
-    S8_TILE("64x64_k2_s4", 64, 64, 16, 32, 2, 4, true, 1.76f, 3.61f, 1.16f, 0.64f, 1.64f),
-    S8_TILE("64x64_k1_s4", 64, 64, 16, 32, 1, 4, true, 3.50f, 1.37f, 1.39f, 0.55f, 1.41f),
-    S8_TILE("96x64_k2_s3", 96, 64, 48, 32, 2, 3, true, 0.77f, 4.98f, 1.66f, 0.61f, 1.99f),
-    S8_TILE("128x64_k1_s3", 128, 64, 32, 32, 1, 3, true, 2.93f, 2.11f, 1.85f, 0.97f, 2.01f),
-    S8_TILE("128x128_k1_s4", 128, 128, 32, 32, 1, 4, true, 0.00f, 5.65f, 2.32f, 2.23f, 3.55f),
-    S8_TILE("192x128_k1_s2", 192, 128, 96, 32, 1, 2, false, 0.28f, 5.07f, 4.93f, 2.94f, 3.14f),
-    S8_TILE("256x128_k1_s3", 256, 128, 64, 32, 1, 3, true, 0.00f, 6.13f, 3.94f, 3.39f, 6.64f),
-    S8_TILE("256x192_k1_s2", 256, 192, 64, 96, 1, 2, false, 0.00f, 7.47f, 7.80f, 3.96f, 10.63f),
+    {"gemv_r2", 4, 8, 3.03f, 0.00f, 0.23f, 0.09f, 0.27f, launch_s8_gemv_r2},
+    {"gemv_r2k4", 4, 2, 3.34f, 0.11f, 0.03f, 0.00f, 0.06f, launch_s8_gemv_r2k4},
+    S8_TILE("16x16_k8_s4", 16, 16, 16, 16, 8, 4, true, 3.43f, 1.35f, 0.09f, 0.25f, 0.54f),
+    S8_TILE("16x16_k4_s4", 16, 16, 16, 16, 4, 4, true, 2.91f, 0.83f, 0.28f, 0.20f, 0.35f),
+    S8_TILE("16x32_k4_s4", 16, 32, 16, 32, 4, 4, true, 2.80f, 1.60f, 0.31f, 0.48f, 0.62f),
+    S8_TILE("32x32_k4_s4", 32, 32, 32, 32, 4, 4, true, 2.49f, 2.29f, 0.43f, 0.44f, 0.81f),
+    S8_TILE("64x32_k4_s3", 64, 32, 32, 32, 4, 3, true, 1.90f, 3.10f, 0.84f, 0.32f, 1.18f),
+    S8_TILE("64x64_k2_s4", 64, 64, 16, 32, 2, 4, true, 1.49f, 3.40f, 1.07f, 0.69f, 1.56f),
+    S8_TILE("64x64_k1_s4", 64, 64, 16, 32, 1, 4, true, 2.70f, 1.46f, 1.58f, 0.47f, 1.34f),
+    S8_TILE("96x64_k2_s3", 96, 64, 48, 32, 2, 3, true, 0.48f, 4.54f, 1.60f, 0.67f, 2.02f),
+    S8_TILE("128x64_k1_s3", 128, 64, 32, 32, 1, 3, true, 2.51f, 2.14f, 1.77f, 1.12f, 1.96f),
+    S8_TILE("128x128_k1_s4", 128, 128, 32, 32, 1, 4, true, 0.00f, 4.99f, 2.33f, 2.24f, 3.75f),
+    S8_TILE("192x128_k1_s2", 192, 128, 96, 32, 1, 2, false, 0.00f, 4.71f, 4.55f, 3.80f, 3.16f),
+    S8_TILE("256x128_k1_s3", 256, 128, 64, 32, 1, 3, true, 0.00f, 5.17f, 3.99f, 3.62f, 6.79f),
+    S8_TILE("256x192_k1_s2", 256, 192, 64, 96, 1, 2, false, 0.00f, 5.66f, 7.95f, 4.36f, 10.81f),
     // 16 waves have no registers left for the path through them
-    {"256x256_k1_s2", 256, 256, 0.00f, 6.82f, 8.54f, 6.08f, 12.60f,
+    {"256x256_k1_s2", 256, 256, 0.00f, 5.41f, 8.90f, 5.44f, 13.67f,
      s8_launch<S8Tile<256, 256, 64, 64, 1, 2, false>, S8Tile<256, 256, 64, 128, 1, 2, true>>},
 };
 #undef S8_TILE
 constexpr int kNumConfigs = sizeof(kConfigs) / sizeof(kConfigs[0]);
 
+// The dot products read W once for each kGemvRows rows of A, and stand to
+// choice up to twice that: from M = 9 on the tiles are always the quicker
+// (8 x 4096 x 4096: 6.9 us, tiles 6.1; 1: 4.9 against 5.4; 3 x 11008 x 4096:
+// 9.3 against 10.7).
+constexpr int kGemvRows = 4;
+
 int pick(int M, int N, int K) {
-  int best = 0;
+  int best = -1;
   float least = 0.0f;
   for (int c = 0; c < kNumConfigs; ++c) {
     const S8Config &f = kConfigs[c];
-    const float tiles = (float)((M + f.BM - 1) / f.BM) * (float)((N + f.BN - 1) / f.BN);
+    if (f.BM == kGemvRows && M > 2 * kGemvRows) continue;
+    const float tiles = (float)((M - 1) / f.BM + 1) * (float)((N - 1) / f.BN + 1);
     const float rounds = ceilf(tiles / 256.0f), fill = tiles / (256.0f * rounds);
     const float t = f.fixed + f.each * rounds +
                     (f.first + f.full * fill + f.more * (rounds - 1.0f)) * (float)K * 1e-3f;
-    if (c == 0 || t < least) {
+    if (best < 0 || t < least) {
       best = c;
       least = t;
     }
@@ -100,16 +111,19 @@ int select_s8_config(int M, int N, int K) { return pick(M > 0 ? M : 1, N > 0 ? N
 
 hipError_t launch_s8(int cfg, const S8Args &a, hipStream_t s) {
   if (cfg < 0) cfg = pick(a.M, a.N, a.K);
+  const S8Config &c = kConfigs[cfg];
   const size_t size = a.type == kTypeF32 ? 4 : 2;
-  for (int m0 = 0; m0 < a.M; m0 += kMaxLaunchRows) {
+  const long long across = (a.N + c.BN - 1) / c.BN;
+  long long down = kMaxLaunchTiles / across;  // at least 2: N is at most 2^20
+  if (c.BM == kGemvRows && down > 65535) down = 65535;
+  for (long long m0 = 0; m0 < a.M; m0 += down * c.BM) {
     S8Args b = a;
-    b.M = a.M - m0 < kMaxLaunchRows ? a.M - m0 : kMaxLaunchRows;
-    b.A = a.A + (size_t)m0 * a.lda;
+    b.M = (int)(a.M - m0 < down * c.BM ? a.M - m0 : down * c.BM);
+    b.A = a.A + m0 * a.lda;
     b.sA = a.sA + m0;
     b.C = static_cast<char *>(a.C) + (size_t)m0 * a.ldc * size;
-    const hipError_t e = kConfigs[cfg].launch(b, s);
+    const hipError_t e = c.launch(b, s);
     if (e != hipSuccess) return e;
-    if (b.M == a.M - m0) break;  // m0 + the step may pass the int range
   }
   return hipSuccess;
 }

@@ -112,6 +112,22 @@ def test_gemm_quick_returns_need_no_gpu():
     assert call_gemm(cfg=-2) == fg.ERR_CONFIG
 
 
+def test_gemm_configurations_and_their_choice():
+    assert len(CONFIGS) == fg.fp32gemm_num_configs(fg.KIND_S8GEMM) == len(set(CONFIGS))
+    assert fg.fp32gemm_config_name(fg.KIND_S8GEMM, len(CONFIGS)) is None
+    assert fg.fp32gemm_config_name(fg.KIND_S8GEMM, -1) is None
+    assert fg.fp32gemm_config_max_rows(fg.KIND_S8GEMM, 0) == 2 ** 31 - 1
+    assert fg.fp32gemm_config_max_rows(fg.KIND_S8GEMM, len(CONFIGS)) == -1
+    name = lambda *s: CONFIGS[fg.fp32gemm_select_config(fg.KIND_S8GEMM, *s)]
+    big = 2 ** 31 - 1
+    for shape in [(1, 1, 1), (big, 1, 1), (big, 1 << 20, 131071), (1, 1 << 20, 131071), (0, 0, 0)]:
+        assert name(*shape) in CONFIGS
+    # dot products for a token, never above eight; tiles that grow with the shape
+    assert name(1, 4096, 4096).startswith("gemv") and name(1, 512, 11008).startswith("gemv")
+    assert not any(name(9, N, K).startswith("gemv") for N in (1, 64, 4096, 1 << 20) for K in (1, 4096, 131071))
+    assert name(16, 11008, 4096).startswith("16x16") and name(4096, 4096, 4096).startswith("256x256")
+
+
 @pytest.mark.parametrize("kw,pos", [
     (dict(trans=2), 1), (dict(M=-1), 2), (dict(K=-1), 3), (dict(type=3), 4), (dict(X=None), 5),
     (dict(X=18), 5), (dict(type=1, X=17), 5), (dict(ldx=7), 6), (dict(trans=1, ldx=3), 6),
