@@ -247,6 +247,9 @@ def test_gemm_scales_that_are_not_numbers_stay_in_their_row_and_column():
         want = torch.zeros(20, 40, dtype=torch.bool)
         want[7], want[:, 11] = True, True
         assert torch.equal(nan, want)
+        assert fg.fp32gemm_s8gemm_with_config(cfg, 20, 40, 96, A, 96, sA, B, 96, sB, 0.0, 0, C, 40, None,
+                                              fg.ACT_RELU) == 0
+        assert torch.equal(torch.isnan(C.cpu()), want) and not bool((C < 0).any())
         assert bool((C[3][~torch.isnan(C[3])] == 0).all())
 
 
@@ -440,3 +443,91 @@ def test_rmsnorm_odd_rows(dtype):
     check_rmsnorm(X, None, W, 1e-5)
     check_rmsnorm(X, None, torch.zeros_like(W), 1e-5)
     check_rmsnorm(torch.nn.functional.pad(X, (0, 20000)), None, torch.nn.functional.pad(one, (0, 20000)), 1e-5)
+
+
+# ---- sizes past one launch, offsets past 32 bits ----------------------------------------
+
+@gpu
+def test_more_rows_than_one_launch_takes():
+    """Row operators beyond 2^21 rows, and a product whose configuration runs in several launches."""
+    require_gpu()
+    M, K = 2 ** 21 + 77, 5
+    X = torch.randn(M, K, device="cuda")
+    Q, S = torch.empty(M, K, dtype=torch.int8, device="cuda"), torch.empty(M, device="cuda")
+    assert fg.s8_quantize(0, M, K, 0, X, K, Q, K, S) == 0
+    q, s = ref.codes(X.cpu().double())
+    assert torch.equal(Q.cpu().long(), q) and torch.equal(S.cpu(), s)
+    H = torch.empty_like(X)
+    w = torch.rand(K)
+    assert fg.s8_rmsnorm(M, K, 0, X, K, X, K, H, K, w.cuda(), 1e-5, Q, K, S) == 0
+    h, q, _, s = ref.rmsnorm(X.cpu(), X.cpu(), w, 1e-5)
+    assert torch.equal(H.cpu(), h) and torch.equal(Q.cpu().long(), q)
+    assert bool(((S.cpu().double() - s).abs() <= s * (ref.U32 + 1e-11)).all())
+    g = torch.Generator().manual_seed(1)
+    M, N, K = 4 * 65535 * 2 + 9, 3, 33
+    A, B = make_codes(g, M, K), make_codes(g, N, K)
+    sA, sB = torch.rand(M, generator=g), torch.rand(N, generator=g)
+    z, bound = ref.gemm(A, sA, B, sB, 0.0, None, None, False, 0)
+    for cfg in (-1, CONFIGS.index("gemv_r2"), CONFIGS.index("16x16_k4_s4")):
+        C = torch.full((M, N), float("nan"), device="cuda")
+        assert fg.fp32gemm_s8gemm_with_config(cfg, M, N, K, A.cuda(), K, sA.cuda(), B.cuda(), K, sB.cuda(),
+                                              0.0, 0, C, N) == 0
+        assert bool(((C.cpu().double() - z).abs() <= bound).all()), cfg
+
+
+@gpu
+def test_offsets_past_32_bits():
+    """The largest leading dimension with enough rows that byte offsets pass 2^32 in every operand."""
+    require_gpu()
+    ld, M, K, N = 1 << 20, 4100, 70, 50
+    g = torch.Generator().manual_seed(2)
+    X = torch.empty(M, ld, dtype=torch.bfloat16, device="cuda")[:, :K]
+    X.copy_(torch.randn(M, K, generator=g).bfloat16())
+    Q = torch.empty(M, ld, dtype=torch.int8, device="cuda")[:, :K]
+    S = torch.empty(M, device="cuda")
+    w = torch.ones(K, dtype=torch.bfloat16)
+    assert fg.s8_rmsnorm(M, K, 2, X, ld, None, 0, X, ld, w.cuda(), 1e-5, Q, ld, S) == 0
+    _, q, _, s = ref.rmsnorm(X.cpu(), None, w, 1e-5)
+    assert torch.equal(Q.cpu().long(), q)
+    assert fg.s8_quantize(0, M, K, 2, X, ld, Q, ld, S) == 0
+    q, s = ref.codes(X.cpu().double())
+    assert torch.equal(Q.cpu().long(), q) and torch.equal(S.cpu(), s)
+    QT, ST = torch.empty(K, M, dtype=torch.int8, device="cuda"), torch.empty(K, device="cuda")
+    assert fg.s8_quantize(1, K, M, 2, X, ld, QT, M, ST) == 0
+    qt, st = ref.codes(X.cpu().double().t())
+    assert torch.equal(QT.cpu().long(), qt) and torch.equal(ST.cpu(), st)
+    B = make_codes(g, N, K)
+    sB = torch.rand(N, generator=g)
+    C = torch.empty(M, ld, dtype=torch.float16, device="cuda")[:, :N]
+    z, bound = ref.gemm(Q.cpu(), S.cpu(), B, sB, 0.0, None, None, False, 1)
+    for cfg in (-1, CONFIGS.index("256x256_k1_s2"), CONFIGS.index("64x64_k2_s4"), CONFIGS.index("gemv_r2k4")):
+        C.fill_(float("nan"))
+        assert fg.fp32gemm_s8gemm_with_config(cfg, M, N, K, Q, ld, S, B.cuda(), K, sB.cuda(), 0.0, 1, C, ld) == 0
+        assert bool(((C.cpu().double() - z).abs() <= bound).all()), cfg
+    # the weight's rows that far apart: C is its own leading dimension wide
+    C2 = torch.empty(3, M, device="cuda")
+    A = make_codes(g, 3, K).cuda()
+    one = torch.ones(3, device="cuda")
+    z, bound = ref.gemm(A.cpu(), one.cpu(), Q.cpu(), S.cpu(), 0.0, None, None, False, 0)
+    for cfg in range(-1, len(CONFIGS)):
+        C2.fill_(float("nan"))
+        assert fg.fp32gemm_s8gemm_with_config(cfg, 3, M, K, A, K, one, Q, ld, S, 0.0, 0, C2, M) == 0
+        assert bool(((C2.cpu().double() - z).abs() <= bound).all()), cfg
+
+
+@gpu
+def test_same_bits_from_call_to_call():
+    require_gpu()
+    g = torch.Generator().manual_seed(3)
+    X = torch.randn(300, 5003, generator=g).cuda()
+    w = torch.rand(5003, generator=g).cuda()
+    runs = []
+    for _ in range(5):
+        Q, S = torch.empty(300, 5008, dtype=torch.int8, device="cuda")[:, :5003], torch.empty(300, device="cuda")
+        assert fg.s8_rmsnorm(300, 5003, 0, X, 5003, None, 0, None, 0, w, 1e-5, Q, 5008, S) == 0
+        C = torch.empty(300, 300, device="cuda")
+        assert fg.s8gemm(300, 300, 5003, Q, 5008, S, Q, 5008, S, 0.0, 0, C, 300) == 0
+        torch.matmul(X, X.t())
+        runs.append((Q, S, C))
+    for q, s, c in runs[1:]:
+        assert torch.equal(q, runs[0][0]) and torch.equal(s, runs[0][1]) and torch.equal(c, runs[0][2])
