@@ -298,33 +298,32 @@ template <class T, bool NORM, bool WHOLE> hipError_t launch_rows(const S8RowArgs
 }
 
 // Columns of X stored K x M, to rows of codes.  A workgroup takes 64 bytes of
-// each row of X over all of K, 1024 k at a time: four lanes read a row's 64
-// bytes, a thread four consecutive k, whose codes of a column make a word.
-// The words turn in LDS from k-major to column-major.  The first HELD times
-// 1024 k stay in registers between the columns' largest values and their
-// codes; the rest is read twice.
+// each row of X, 1024 k at a time: four lanes read a row's 64 bytes, a thread
+// four consecutive k, whose codes of a column make a word.  The words turn in
+// LDS from k-major to column-major.
 constexpr int CT = 1024, CK = 1024;
 
-template <class T, int HELD>
-__global__ void __launch_bounds__(CT) columns_kernel(S8RowArgs a) {
-  constexpr int VE = 16 / sizeof(T);  // columns of a thread
-  constexpr int CB = 4 * VE;          // of the workgroup
-  constexpr int PITCH = CK / 4 + 4;   // words of a column in LDS: 4 columns apart are 16 banks apart
+template <class T> struct Columns {
+  static constexpr int VE = 16 / sizeof(T);  // columns of a thread
+  static constexpr int CB = 4 * VE;          // of the workgroup
+  static constexpr int PITCH = CK / 4 + 4;   // words of a column in LDS: 4 columns apart are 16 banks apart
   typedef T vec __attribute__((ext_vector_type(VE)));
   typedef T anywhere __attribute__((ext_vector_type(VE), aligned(alignof(T))));
-  __shared__ uint32_t tops[CT / 64][CB];
-  __shared__ float scale[CB];
-  __shared__ __attribute__((aligned(16))) uint32_t turn[2][CB * PITCH];
-  const int tid = threadIdx.x;
-  // neighbouring columns, which share lines of X, to the same XCD
-  const int xcd = (int)blockIdx.x & 7, per = gridDim.x >> 3, extra = gridDim.x & 7;
-  const int lid = xcd * per + min(xcd, extra) + ((int)blockIdx.x >> 3);
-  const int col0 = lid * CB;
-  const int c = tid % 4 * VE, g = tid / 4;  // the thread's columns, and its word of 4 k
-  const int cols = a.M - col0 - c;          // of the thread's, valid ones
-  const T *x = static_cast<const T *>(a.X) + col0 + c;
 
-  auto load = [&](int k) -> vec {
+  const S8RowArgs &a;
+  int col0, c, g, cols;  // the workgroup's columns; the thread's, its word of 4 k, its columns in X
+  const T *x;
+
+  __device__ __forceinline__ Columns(const S8RowArgs &a_, int block, int blocks) : a(a_) {
+    // neighbouring columns, which share lines of X, to the same XCD
+    const int xcd = block & 7, lid = xcd * (blocks >> 3) + min(xcd, blocks & 7) + (block >> 3);
+    col0 = lid * CB;
+    c = threadIdx.x % 4 * VE;
+    g = threadIdx.x / 4;
+    cols = a.M - col0 - c;
+    x = static_cast<const T *>(a.X) + col0 + c;
+  }
+  __device__ __forceinline__ vec load(int k) const {
     vec v = {};
     if (k < a.K) {
       const T *p = x + (long long)k * a.ldx;
@@ -337,11 +336,12 @@ __global__ void __launch_bounds__(CT) columns_kernel(S8RowArgs a) {
       }
     }
     return v;
-  };
-  uint32_t top[VE];
+  }
+  __device__ __forceinline__ void load4(int k0, vec (&v)[4]) const {
 #pragma unroll
-  for (int e = 0; e < VE; ++e) top[e] = 0;
-  auto see = [&](const vec (&v)[4]) {
+    for (int u = 0; u < 4; ++u) v[u] = load(k0 + 4 * g + u);
+  }
+  __device__ __forceinline__ void see(const vec (&v)[4], uint32_t (&top)[VE]) const {
 #pragma unroll
     for (int u = 0; u < 4; ++u)
 #pragma unroll
@@ -349,44 +349,29 @@ __global__ void __launch_bounds__(CT) columns_kernel(S8RowArgs a) {
         const uint32_t b = abs_bits((float)v[u][e]);
         top[e] = b > top[e] ? b : top[e];
       }
-  };
-  vec held[HELD][4];
-#pragma unroll
-  for (int h = 0; h < HELD; ++h)
-#pragma unroll
-    for (int u = 0; u < 4; ++u) held[h][u] = load(h * CK + 4 * g + u);
-#pragma unroll
-  for (int h = 0; h < HELD; ++h) see(held[h]);
-  for (int k0 = HELD * CK; k0 < a.K; k0 += CK) {
-    vec v[4];
-#pragma unroll
-    for (int u = 0; u < 4; ++u) v[u] = load(k0 + 4 * g + u);
-    see(v);
   }
+  // The workgroup's largest bits of column `threadIdx.x` (below CB).
+  __device__ __forceinline__ uint32_t fold(uint32_t (&top)[VE], uint32_t (*tops)[CB]) const {
 #pragma unroll
-  for (int e = 0; e < VE; ++e) {
+    for (int e = 0; e < VE; ++e) {
 #pragma unroll
-    for (int d = 4; d < 64; d <<= 1) {
-      const uint32_t t = (uint32_t)__shfl_xor((int)top[e], d, 64);
-      top[e] = t > top[e] ? t : top[e];
+      for (int d = 4; d < 64; d <<= 1) {
+        const uint32_t t = (uint32_t)__shfl_xor((int)top[e], d, 64);
+        top[e] = t > top[e] ? t : top[e];
+      }
+      if (threadIdx.x % 64 < 4) tops[threadIdx.x / 64][c + e] = top[e];
     }
-    if (tid % 64 < 4) tops[tid / 64][c + e] = top[e];
-  }
-  __syncthreads();
-  if (tid < CB) {
+    __syncthreads();
     uint32_t t = 0;
+    if (threadIdx.x < CB) {
 #pragma unroll
-    for (int w = 0; w < CT / 64; ++w) t = tops[w][tid] > t ? tops[w][tid] : t;
-    scale[tid] = row_scale(t);
-    if (col0 + tid < a.M) a.scales[col0 + tid] = row_scale(t);
+      for (int w = 0; w < CT / 64; ++w) t = tops[w][threadIdx.x] > t ? tops[w][threadIdx.x] : t;
+    }
+    return t;
   }
-  __syncthreads();
-  float inv[VE];
-#pragma unroll
-  for (int e = 0; e < VE; ++e) inv[e] = quick_inv(scale[c + e]);
-
-  auto put = [&](const vec (&v)[4], int k0) {
-    uint32_t *words = turn[k0 / CK & 1];
+  // Codes of 1024 k from k0: scales by column in LDS, 1 / step in registers.
+  __device__ __forceinline__ void put(const vec (&v)[4], int k0, uint32_t *words, const float *scale,
+                                      const float (&inv)[VE]) const {
 #pragma unroll
     for (int e = 0; e < VE; ++e) {
       const float f[4] = {(float)v[0][e], (float)v[1][e], (float)v[2][e], (float)v[3][e]};
@@ -394,7 +379,7 @@ __global__ void __launch_bounds__(CT) columns_kernel(S8RowArgs a) {
     }
     __syncthreads();
     const int left = a.K - k0;
-    for (int f = tid; f < CB * (CK / 16); f += CT) {
+    for (int f = threadIdx.x; f < CB * (CK / 16); f += CT) {
       const int col = f / (CK / 16), k = f % (CK / 16) * 16;
       if (col0 + col >= a.M || k >= left) continue;
       int8_t *q = a.Q + (long long)(col0 + col) * a.ldq + k0 + k;
@@ -407,22 +392,107 @@ __global__ void __launch_bounds__(CT) columns_kernel(S8RowArgs a) {
         for (int e = 0; e < left - k; ++e) q[e] = (int8_t)(from[e / 4] >> 8 * (e % 4));
       }
     }
-    // the other half of `turn` is written next, and this one after the next barrier
-  };
+  }
+};
+
+// All of K in one workgroup.  The first HELD times 1024 k stay in registers
+// between the columns' largest values and their codes; the rest is read twice.
+template <class T, int HELD>
+__global__ void __launch_bounds__(CT) columns_kernel(S8RowArgs a) {
+  typedef Columns<T> C;
+  __shared__ uint32_t tops[CT / 64][C::CB];
+  __shared__ float scale[C::CB];
+  __shared__ __attribute__((aligned(16))) uint32_t turn[2][C::CB * C::PITCH];
+  const C o(a, blockIdx.x, gridDim.x);
+  uint32_t top[C::VE] = {};
+  typename C::vec held[HELD][4];
+#pragma unroll
+  for (int h = 0; h < HELD; ++h) o.load4(h * CK, held[h]);
+#pragma unroll
+  for (int h = 0; h < HELD; ++h) o.see(held[h], top);
+  for (int k0 = HELD * CK; k0 < a.K; k0 += CK) {
+    typename C::vec v[4];
+    o.load4(k0, v);
+    o.see(v, top);
+  }
+  const uint32_t t = o.fold(top, tops);
+  if (threadIdx.x < C::CB) {
+    scale[threadIdx.x] = row_scale(t);
+    if (o.col0 + (int)threadIdx.x < a.M) a.scales[o.col0 + threadIdx.x] = row_scale(t);
+  }
+  __syncthreads();
+  float inv[C::VE];
+#pragma unroll
+  for (int e = 0; e < C::VE; ++e) inv[e] = quick_inv(scale[o.c + e]);
+  // one half of `turn` is written while the other may still be read: two
+  // barriers lie between two writes of the same half
 #pragma unroll
   for (int h = 0; h < HELD; ++h)
-    if (h * CK < a.K) put(held[h], h * CK);
+    if (h * CK < a.K) o.put(held[h], h * CK, turn[h & 1], scale, inv);
   for (int k0 = HELD * CK; k0 < a.K; k0 += CK) {
-    vec v[4];
-#pragma unroll
-    for (int u = 0; u < 4; ++u) v[u] = load(k0 + 4 * g + u);
-    put(v, k0);
+    typename C::vec v[4];
+    o.load4(k0, v);
+    o.put(v, k0, turn[k0 / CK & 1], scale, inv);
   }
 }
 
+// K over workgroups (blockIdx.y takes 1024 k), for few columns: the columns'
+// largest bits by atomic maxima in `scales` (whole numbers: any order gives
+// the same), then the codes, then the scales in place of the bits.
+__global__ void columns_clear_kernel(float *scales, int M) {
+  const int i = blockIdx.x * blockDim.x + threadIdx.x;
+  if (i < M) scales[i] = 0.0f;
+}
+template <class T> __global__ void __launch_bounds__(CT) columns_top_kernel(S8RowArgs a) {
+  typedef Columns<T> C;
+  __shared__ uint32_t tops[CT / 64][C::CB];
+  const C o(a, blockIdx.x, gridDim.x);
+  uint32_t top[C::VE] = {};
+  typename C::vec v[4];
+  o.load4(blockIdx.y * CK, v);
+  o.see(v, top);
+  const uint32_t t = o.fold(top, tops);
+  if (threadIdx.x < C::CB && o.col0 + (int)threadIdx.x < a.M)
+    atomicMax(reinterpret_cast<uint32_t *>(a.scales) + o.col0 + threadIdx.x, t);
+}
+template <class T> __global__ void __launch_bounds__(CT) columns_code_kernel(S8RowArgs a) {
+  typedef Columns<T> C;
+  __shared__ float scale[C::CB];
+  __shared__ __attribute__((aligned(16))) uint32_t turn[C::CB * C::PITCH];
+  const C o(a, blockIdx.x, gridDim.x);
+  typename C::vec v[4];
+  o.load4(blockIdx.y * CK, v);
+  if (threadIdx.x < C::CB)
+    scale[threadIdx.x] = o.col0 + (int)threadIdx.x < a.M
+                             ? row_scale(reinterpret_cast<const uint32_t *>(a.scales)[o.col0 + threadIdx.x])
+                             : 0.0f;
+  __syncthreads();
+  float inv[C::VE];
+#pragma unroll
+  for (int e = 0; e < C::VE; ++e) inv[e] = quick_inv(scale[o.c + e]);
+  o.put(v, blockIdx.y * CK, turn, scale, inv);
+}
+__global__ void columns_scale_kernel(float *scales, int M) {
+  const int i = blockIdx.x * blockDim.x + threadIdx.x;
+  if (i < M) scales[i] = row_scale(reinterpret_cast<const uint32_t *>(scales)[i]);
+}
+
 template <class T> hipError_t launch_columns(const S8RowArgs &a, hipStream_t s) {
-  constexpr int CB = 4 * (16 / sizeof(T));
-  const int groups = (a.M + CB - 1) / CB;
+  constexpr int CB = Columns<T>::CB;
+  const int groups = (a.M - 1) / CB + 1, chunks = (a.K + CK - 1) / CK;
+  // With half the CUs or fewer busy, K over workgroups and four launches (14 to
+  // 20 us at least) are the quicker once K is long: fp32, 100 columns of 16384,
+  // 14.4 against 70.8 us, of 4096 13.8 against 15.8, 1000 of 3000 14.3 against
+  // 14.2; bf16, whose workgroups have twice the columns, 4096 of 4096 25.5
+  // against 28.6, of 2000 17.3 against 16.1.
+  if (groups <= 128 && chunks > (sizeof(T) == 4 ? 4 : 2)) {
+    const int small = (a.M - 1) / 256 + 1;
+    columns_clear_kernel<<<small, 256, 0, s>>>(a.scales, a.M);
+    columns_top_kernel<T><<<dim3(groups, chunks), CT, 0, s>>>(a);
+    columns_code_kernel<T><<<dim3(groups, chunks), CT, 0, s>>>(a);
+    columns_scale_kernel<<<small, 256, 0, s>>>(a.scales, a.M);
+    return hipGetLastError();
+  }
   // Registers for 4096 k of fp32 save the second reading, and cost the second
   // workgroup of a CU (11008 columns of 4096: 61.8 us, holding 1024 k 70.0);
   // up to K = 1024, and for 16-bit values, whose second reading is half as

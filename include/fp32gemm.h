@@ -310,7 +310,9 @@ int fp32gemm_splitk_splits(int M, int N, int K);
  * past 127 become 127, and with a zero scale all are 0.)  A row that holds an
  * infinity or a NaN gets the scale NaN and codes 0, so that the products of
  * that row, and of no other, are NaN.  A row of zeros has scale 0; K == 0
- * gives scale 0.  Bytes of Q past a row's K codes are left as they were.
+ * gives scale 0.  Bytes of Q past a row's K codes are left as they were.  Few
+ * columns of a long K run as four kernels in a row, with `scales` in use
+ * between them.
  * Argument positions for error codes: trans 1, M 2, K 3, type 4, X 5, ldx 6,
  * Q 7, ldq 8, scales 9, stream 10.
  */

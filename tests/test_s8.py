@@ -307,7 +307,8 @@ def test_quantize_rows(K, dtype):
 @gpu
 @pytest.mark.parametrize("dtype", list(ref.TYPES.values()), ids=str)
 @pytest.mark.parametrize("shape", [(1, 1), (1, 300), (300, 1), (31, 33), (32, 64), (65, 130), (200, 1000),
-                                   (4097, 70), (9000, 33)])
+                                   (4097, 70), (9000, 33), (4096, 600),
+                                   (2049, 200), (1025, 17), (20000, 1)])
 def test_quantize_columns(shape, dtype):
     require_gpu()
     g = torch.Generator().manual_seed(shape[0])
@@ -349,6 +350,9 @@ def test_quantize_rows_that_decide_by_a_bit_or_hold_no_number(dtype):
     X = odd_rows(dtype)
     check_quantize(X)
     check_quantize(X.t().contiguous(), columns=True)
+    longer = torch.nn.functional.pad(X, (0, 5000))  # K over workgroups
+    check_quantize(longer.t().contiguous(), columns=True)
+    check_quantize(torch.cat([longer] * 9 + [longer[:5]]).t().contiguous(), columns=True, offx=1, offq=3)
 
 
 @gpu
@@ -365,6 +369,7 @@ def test_quantize_values_next_to_halves():
     X = torch.from_numpy(np.stack(rows).astype(np.float32))
     check_quantize(X)
     check_quantize(X.t().contiguous(), columns=True)
+    check_quantize(torch.nn.functional.pad(X, (0, 9000)).t().contiguous(), columns=True)
     check_quantize(torch.nn.functional.pad(X, (0, 16000)))  # rows of the longer kernels
     check_quantize(torch.nn.functional.pad(X, (0, 20000)))
 
