@@ -21,6 +21,7 @@ import os
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libfp32gemm.so")
 _lib = None
+_torch = None  # set with _lib
 
 KIND_SGEMM = 0
 KIND_SGEMV = 1
@@ -88,7 +89,9 @@ def lib():
         # library binds to (same soname); loaded after the library, it would
         # be a second runtime in the process, and whichever of the two opens
         # the GPU second finds no device.  So torch goes first.
-        import torch  # noqa: F401
+        import torch
+        global _torch
+        _torch = torch
         L = ctypes.CDLL(LIB_PATH)
         L.sgemm.argtypes = _GEMM_ARGTYPES
         L.sgemm.restype = ctypes.c_int
@@ -148,18 +151,15 @@ def lib():
 
 def _addr(x):
     """Device address of a tensor / int / None."""
-    if x is None:
-        return None
-    if isinstance(x, int):
+    if x is None or isinstance(x, int):
         return x
     return x.data_ptr()
 
 
 def _stream(stream):
     if stream is None:
-        import torch
         # the handle alone: making a torch.cuda.Stream to ask for it costs 3 us
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return _torch._C._cuda_getCurrentRawStream(_torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -485,10 +485,12 @@ class _On:
 
 
 def _codes_out(M, K, out, scales, device):
-    """Codes (rows from multiples of 16 bytes, which s8gemm reads fastest) and scales, as given or new."""
+    """Codes and scales, as given or new.  New rows of codes start at multiples of 128 bytes, whole
+    cache lines, which s8gemm reads fastest, or of 16 where that would pad short rows by much."""
     import torch
     if out is None:
-        out = torch.empty((M, -(-K // 16) * 16), dtype=torch.int8, device=device)[:, :K]
+        to = 128 if K > 512 else 16
+        out = torch.empty((M, -(-K // to) * to), dtype=torch.int8, device=device)[:, :K]
     if tuple(out.shape) != (M, K):
         raise ValueError(f"out has shape {tuple(out.shape)}, expected {(M, K)}")
     _, ldq = _matrix(out, "out", torch.int8)
