@@ -526,8 +526,10 @@ __global__ void __launch_bounds__(T::NT) s8_kernel(S8Args a, int tiles_m, int ti
 }
 
 // 16-byte loads of whole chunks: rows that start at multiples of 16 bytes.
-// The chunk that K ends in is read whole: lda and ldb are then multiples of
-// 16 and at least K, so it lies inside its row.
+// The chunk that K ends in is read whole.  It lies inside its row's lda or ldb
+// bytes, multiples of 16 there; behind the last row, whose codes may end at K,
+// it is the aligned 16 bytes that hold the last code, so no page without one
+// is touched, and what it reads is multiplied by zeros.
 inline bool s8_dma_ok(const S8Args &a) {
   return (uintptr_t)a.A % 16 == 0 && (uintptr_t)a.B % 16 == 0 && a.lda % 16 == 0 && a.ldb % 16 == 0;
 }
