@@ -89,11 +89,11 @@ __global__ void __launch_bounds__(64 * kWaves) s8_gemv_kernel(S8Args a) {
   int sum = 0;
 #pragma unroll
   for (int q = 0; q < KW; ++q) sum += part[c / R * KW + q][i * R + c % R];
-  float v[1] = {__builtin_fmaf((float)sum * a.sA[m], a.sB[n], a.bias != nullptr ? a.bias[n] : 0.0f)};
+  const float v = s8_scaled<true>(sum, a.sA[m], a.sB[n], a.bias != nullptr ? a.bias[n] : 0.0f);
   const size_t at = (size_t)m * a.ldc + n;
-  if (a.type == kTypeF32) s8_finish_one(a, static_cast<float *>(a.C) + at, v[0]);
-  else if (a.type == kTypeF16) s8_finish_one(a, static_cast<_Float16 *>(a.C) + at, v[0]);
-  else s8_finish_one(a, static_cast<__bf16 *>(a.C) + at, v[0]);
+  if (a.type == kTypeF32) s8_finish_one(a, static_cast<float *>(a.C) + at, v);
+  else if (a.type == kTypeF16) s8_finish_one(a, static_cast<_Float16 *>(a.C) + at, v);
+  else s8_finish_one(a, static_cast<__bf16 *>(a.C) + at, v);
 }
 
 template <int MR, int R, int KW> hipError_t launch(const S8Args &a, hipStream_t s) {

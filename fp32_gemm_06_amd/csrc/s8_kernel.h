@@ -140,6 +140,22 @@ template <int N> __device__ __forceinline__ void s8_floats(const float *p, int n
   for (int e = 0; e < N; ++e) v[e] = w[e];
 }
 
+// sum sa sb + bias.  The first product may pass fp32's range where the whole
+// does not.  It cannot up to this sa, since a sum is at most 2^31.  Above it sa
+// is taken times 2^-32, which is exact, and the 2^32 comes back with the bias.
+// Nothing is lost at the lower end: sum sa is then zero or at least 2^64, and
+// its product with the smallest sb still normal.  The branch costs nothing that
+// shows (4096^3 fp32 out 64.0 us without it and 64.2, 256 x 4096 x 4096 11.4
+// both).
+constexpr float kWideScale = 0x1p96f;
+__device__ __forceinline__ bool s8_wide(float sa) { return __builtin_fabsf(sa) > kWideScale; }
+template <bool ANY_WIDE>
+__device__ __forceinline__ float s8_scaled(int sum, float sa, float sb, float bias) {
+  if constexpr (!ANY_WIDE) return __builtin_fmaf((float)sum * sa, sb, bias);
+  const float x = (float)sum * (s8_wide(sa) ? sa * 0x1p-32f : sa);
+  return s8_wide(sa) ? __builtin_fmaf(x * sb, 0x1p32f, bias) : __builtin_fmaf(x, sb, bias);
+}
+
 // A run of columns of C: scaled sums and bias in v, plus beta C, through the
 // activation, in 32 bits, rounded once to C's type.  `cols`: the run's columns
 // that are in C.  Wide accesses at any alignment of the element.
@@ -502,19 +518,30 @@ __global__ void __launch_bounds__(T::NT) s8_kernel(S8Args a, int tiles_m, int ti
     for (int t = 0; t < RUNS; ++t) s8_floats<RUN>(a.bias + n0 + run_col(t), cols - run_col(t), bias[t]);
   }
   const __amdgpu_buffer_rsrc_t rs_sa = make_rsrc(a.sA + m0);
+  float sa[T::TM];
+#pragma unroll
+  for (int i = 0; i < T::TM; ++i) {
+    const int m = wm * T::WM + i * 16 + lr;
+    sa[i] = s8_float(rs_sa, m < rows ? 4u * m : kOob);
+  }
   auto finish = [&](auto zero) {
     typedef decltype(zero) F;
     F *Cg = static_cast<F *>(a.C) + (size_t)m0 * a.ldc + n0;
 #pragma unroll
     for (int i = 0; i < T::TM; ++i) {
       const int m = wm * T::WM + i * 16 + lr;
-      const float sa = s8_float(rs_sa, m < rows ? 4u * m : kOob);
+      const bool any_wide = __any(s8_wide(sa[i]));  // rare, and one branch for the wave
 #pragma unroll
       for (int t = 0; t < RUNS; ++t) {
         const int col = run_col(t);
         float v[RUN];
+        if (any_wide) {
 #pragma unroll
-        for (int e = 0; e < RUN; ++e) v[e] = __builtin_fmaf((float)run_sum(i, t, e) * sa, sb[t][e], bias[t][e]);
+          for (int e = 0; e < RUN; ++e) v[e] = s8_scaled<true>(run_sum(i, t, e), sa[i], sb[t][e], bias[t][e]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < RUN; ++e) v[e] = s8_scaled<false>(run_sum(i, t, e), sa[i], sb[t][e], bias[t][e]);
+        }
         if (m < rows && col < cols)
           s8_finish_run<F, RUN>(a, Cg + (uint32_t)(m * a.ldc + col), cols - col, v);
       }

@@ -356,11 +356,13 @@ int s8_rmsnorm(int M, int K, int type, const void *X, int ldx, const void *R,
  *                + beta * C[i][j] + bias[j]),
  * A the M x K codes of the tokens (lda >= K), B the N x K codes of the weight
  * (ldb >= K), C M x N of `type`.  The sum is exact; it is rounded to fp32,
- * scaled and added to in fp32, and rounded once to C's type.  bias (N fp32
- * values) may be NULL; act is FP32GEMM_ACT_NONE or FP32GEMM_ACT_RELU (as in
- * sgemm_fused).  When beta == 0, C is not read.  K <= 131071, which keeps
- * every sum inside 32 bits; K == 0 reads neither codes nor scales.  M == 0 or
- * N == 0 does nothing.  Argument positions for error codes: M 1, N 2, K 3,
+ * scaled and added to in fp32, and rounded once to C's type.  Scales may be
+ * any fp32 values: scaleA[i] * sum past fp32's range does no harm where
+ * scaleA[i] * scaleB[j] * sum is inside it.  bias (N fp32 values) may be NULL;
+ * act is FP32GEMM_ACT_NONE or FP32GEMM_ACT_RELU (as in sgemm_fused).  When
+ * beta == 0, C is not read.  K <= 131071, which keeps every sum inside 32
+ * bits; K == 0 reads neither codes nor scales.  M == 0 or N == 0 does
+ * nothing.  Argument positions for error codes: M 1, N 2, K 3,
  * A 4, lda 5, scaleA 6, B 7, ldb 8, scaleB 9, beta 10, type 11, C 12, ldc 13,
  * bias 14, act 15, stream 16.
  */

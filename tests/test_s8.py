@@ -536,3 +536,76 @@ def test_same_bits_from_call_to_call():
         runs.append((Q, S, C))
     for q, s, c in runs[1:]:
         assert torch.equal(q, runs[0][0]) and torch.equal(s, runs[0][1]) and torch.equal(c, runs[0][2])
+
+# ---- scales at the ends of fp32's range ---------------------------------------------------
+
+def run_extreme_scales(cfg, type, aligned, beta, bias):
+    """(C, value in 64 bits, |value| bound, sum times scaleA) with scales from subnormal to the largest."""
+    g = torch.Generator().manual_seed(17)
+    top = float(np.float32(np.finfo(np.float32).max) / np.float32(127))  # the largest that s8_quantize makes
+    sA = torch.tensor([top, -top, 2.0 ** 96, 2.0 ** 97, 1e30, 1.0, 1e-30, 1e-40, 2.0 ** -149, 0.0, top, 3e38,
+                       3.5e33, 7e28, 8e28, 1e37, 2e20], dtype=torch.float32)
+    sB = torch.tensor([1e-4, 1.0, 1e-30, 1e-33, 1e-36, 1e-38, 1e-40, 2.0 ** -149, 0.0, 1e20, top, -1e-5, 3e38],
+                      dtype=torch.float32).repeat(6)
+    M, N, K = len(sA), len(sB), 201
+    A, B = make_codes(g, M, K), make_codes(g, N, K)
+    A[10] = 0  # sums of zero under the largest scales
+    ld = 208 if aligned else K
+    dA, _ = device(A, ld)
+    dB, _ = device(B, ld)
+    t = ref.TYPES[type]
+    C0 = torch.randn(M, N, generator=g).to(t)
+    bv = torch.randn(N, generator=g) if bias else None
+    C = C0.cuda() if beta else torch.full((M, N), float("nan"), dtype=t, device="cuda")
+    rc = fg.fp32gemm_s8gemm_with_config(cfg, M, N, K, dA, ld, sA.cuda(), dB, ld, sB.cuda(), beta, type, C, N,
+                                        bv.cuda() if bias else None)
+    assert rc == 0, fg.strerror(rc)
+    z, bound = ref.gemm(A, sA, B, sB, beta, C0, bv, False, type)
+    return C.cpu(), z, bound, (A.double() @ B.double().t()) * sA.double()[:, None]
+
+
+@gpu
+@pytest.mark.parametrize("type", [0, 1, 2])
+def test_gemm_scales_at_the_ends_of_their_range(type):
+    """sum scaleA may pass fp32's range where sum scaleA scaleB does not: every element whose value is
+    finite in C's type is within the bound, every other infinite with its sign, and a sum of zero is zero."""
+    require_gpu()
+    top = float(torch.finfo(ref.TYPES[type]).max)
+    for cfg in range(-1, len(CONFIGS)):
+        for aligned in (True, False):
+            for beta, bias in ((0.0, False), (0.5, True)):
+                C, z, bound, part = run_extreme_scales(cfg, type, aligned, beta, bias)
+                what = (cfg, aligned, beta)
+                inside, outside = z.abs() < 0.99 * top, z.abs() > 1.01 * top
+                # what the case is about, and what it is told from
+                assert int((inside & (part.abs() > 3.5e38) & (z.abs() > 0)).sum()) > 60
+                assert int(outside.sum()) > 100
+                err = (C.double() - z).abs()
+                assert bool((err <= bound)[inside].all()), (what, (inside & ~(err <= bound)).nonzero()[:4].tolist())
+                assert bool((torch.isinf(C) & (C.sign() == z.sign()))[outside].all()), what
+                if not beta:
+                    assert bool((C[10] == 0).all()) and bool((C[9] == 0).all()), what
+
+
+@gpu
+def test_gemm_same_bits_at_the_ends_of_the_scales_range():
+    require_gpu()
+    outs = [run_extreme_scales(cfg, 0, aligned, 0.5, True)[0]
+            for cfg in range(-1, len(CONFIGS)) for aligned in (True, False)]
+    for o in outs[1:]:
+        assert torch.equal(o, outs[0])
+
+
+@gpu
+def test_layer_of_rows_near_the_largest_float():
+    """Codes made from rows of 1e36, times a weight near 1e-4: every product is finite."""
+    require_gpu()
+    g = torch.Generator().manual_seed(23)
+    X = torch.randn(5, 300, generator=g) * 1e36
+    W = torch.randn(40, 300, generator=g) * 1e-4
+    for x, w in ((X, W), (W[:9], X)):
+        cx, sx = fg.quantize_s8(x.cuda())
+        cw, sw = fg.quantize_s8(w.cuda())
+        z, bound = ref.gemm(cx.cpu(), sx.cpu(), cw.cpu(), sw.cpu(), 0.0, None, None, False, 0)
+        y = fg.gemm_s8(cx, sx, cw.t(), sw).cpu().double()
+        assert bool(torch.isfinite(y).all()) and bool(((y - z).abs() <= bound).all())
