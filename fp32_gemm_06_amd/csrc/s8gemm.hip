@@ -6,8 +6,7 @@
 namespace fp32gemm {
 namespace {
 
-// Tiles of one launch: keeps the grid's threads below 2^32 (and its second
-// dimension, which the dot products use for rows, below 2^16).
+// Tiles of one launch: keeps the grid's threads below 2^32.
 constexpr long long kMaxLaunchTiles = 1 << 21;
 
 // A configuration, and its time on a shape in microseconds:
@@ -115,8 +114,8 @@ hipError_t launch_s8(int cfg, const S8Args &a, hipStream_t s) {
   const S8Config &c = kConfigs[cfg];
   const size_t size = a.type == kTypeF32 ? 4 : 2;
   const long long across = (a.N + c.BN - 1) / c.BN;
-  long long down = kMaxLaunchTiles / across;  // at least 2: N is at most 2^20
-  if (c.BM == kGemvRows && down > 65535) down = 65535;
+  long long down = kMaxLaunchTiles / across;  // at least 4: N is at most 2^20
+  if (c.BM == kGemvRows && down > 65535) down = 65535;  // rows are their grid's second dimension
   for (long long m0 = 0; m0 < a.M; m0 += down * c.BM) {
     S8Args b = a;
     b.M = (int)(a.M - m0 < down * c.BM ? a.M - m0 : down * c.BM);

@@ -609,3 +609,30 @@ def test_layer_of_rows_near_the_largest_float():
         z, bound = ref.gemm(cx.cpu(), sx.cpu(), cw.cpu(), sw.cpu(), 0.0, None, None, False, 0)
         y = fg.gemm_s8(cx, sx, cw.t(), sw).cpu().double()
         assert bool(torch.isfinite(y).all()) and bool(((y - z).abs() <= bound).all())
+
+
+@gpu
+def test_tiles_of_more_than_one_launch():
+    """A tile configuration past the tiles of one launch (2^21): rows 512 and up run in the second one.
+
+    Values of 65520 and more round to infinity in fp16; next to that border either side is right,
+    as far as the fp32 roundings of the epilogue (6 of them) can move a value.
+    """
+    require_gpu()
+    M, N, K = 530, 1 << 20, 16
+    cfg = CONFIGS.index("16x16_k4_s4")
+    g = torch.Generator().manual_seed(4)
+    A = make_codes(g, M, K).cuda()
+    sA = torch.rand(M, generator=g).cuda()
+    B = torch.randint(-128, 128, (N, K), dtype=torch.int8, device="cuda")
+    sB = torch.rand(N, device="cuda")
+    C = torch.full((M + 1, N), float("nan"), dtype=torch.float16, device="cuda")
+    assert fg.fp32gemm_s8gemm_with_config(cfg, M, N, K, A, K, sA, B, K, sB, 0.0, 1, C, N) == 0
+    assert bool(torch.isnan(C[M]).all())
+    for n0 in range(0, N, 1 << 17):
+        n = slice(n0, n0 + (1 << 17))
+        z, bound = ref.gemm(A, sA, B[n], sB[n], 0.0, None, None, False, 1)
+        got = C[:M, n].double()
+        past = torch.isinf(got) & (got.sign() == z.sign()) & (z.abs() * (1 + 6.001 * ref.U32) >= 65520)
+        near = z.abs() * (1 - 6.001 * ref.U32) < 65520
+        assert bool((((got - z).abs() <= bound) & near | past).all()), n0
