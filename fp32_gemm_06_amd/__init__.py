@@ -26,6 +26,7 @@ _torch = None  # set with _lib
 KIND_SGEMM = 0
 KIND_SGEMV = 1
 KIND_S8GEMM = 2
+_MAX_LD = 1 << 20  # the library's largest leading dimension
 ERR_CONFIG = -100
 ERR_SCRATCH = -101
 
@@ -553,6 +554,17 @@ def rmsnorm_s8(X, weight, eps=1e-6, residual=None, residual_out=None, out=None, 
     return out, scales, X if h is None else h
 
 
+def _codes_ld(t, name):
+    """Leading dimension of a matrix of codes.  A single row's is its stride, if that can be one: whether
+    it is a multiple of 16 decides between the loads of aligned and of other rows."""
+    import torch
+    _, ld = _matrix(t, name, torch.int8)
+    r, c = t.shape
+    if r == 1 and max(1, c) <= t.stride(0) <= _MAX_LD:
+        return t.stride(0)
+    return max(ld, c, 1)
+
+
 def gemm_s8(A, scale_a, B, scale_b, C=None, beta: float = 0.0, dtype=None, bias=None,
             act: int | str | None = None, config: int = -1, stream=None):
     """Torch wrapper of s8gemm: returns C = act(scale_a scale_b (A @ B) +
@@ -568,9 +580,9 @@ def gemm_s8(A, scale_a, B, scale_b, C=None, beta: float = 0.0, dtype=None, bias=
     K2, N = B.shape
     if K2 != K:
         raise ValueError(f"inner dimensions differ: {A.shape} @ {B.shape}")
-    _, lda = _matrix(A, "A", torch.int8)
+    lda = _codes_ld(A, "A")
     try:
-        _, ldb = _matrix(B.t(), "B", torch.int8)
+        ldb = _codes_ld(B.t(), "B")
     except ValueError:
         raise ValueError("B must be the transposed view of row-major N x K codes") from None
     _vector(scale_a, "scale_a", M, torch.float32)
@@ -594,8 +606,8 @@ def gemm_s8(A, scale_a, B, scale_b, C=None, beta: float = 0.0, dtype=None, bias=
             raise ValueError(f"C has shape {tuple(C.shape)}, expected {(M, N)}")
         type = _float_type(C, "C")
         _, ldc = _matrix(C, "C")
-        rc = fp32gemm_s8gemm_with_config(config, M, N, K, A, max(lda, K, 1), scale_a, B, max(ldb, K, 1),
-                                         scale_b, float(beta), type, C, max(ldc, N, 1), bias, int(act), s)
+        rc = fp32gemm_s8gemm_with_config(config, M, N, K, A, lda, scale_a, B, ldb, scale_b, float(beta),
+                                         type, C, max(ldc, N, 1), bias, int(act), s)
     if rc != 0:
         raise Fp32GemmError(rc if rc >= 0 or rc <= -100 else rc + 1)
     return C

@@ -236,3 +236,34 @@ def test_wrappers_refuse_host_tensors():
     c = torch.zeros(4, 32, dtype=torch.int8)
     with pytest.raises(ValueError):
         fg.gemm_s8(c, torch.ones(4), c.t(), torch.ones(4))
+
+
+@gpu
+def test_gemm_keeps_the_leading_dimension_of_one_row(monkeypatch):
+    """One token's codes (or a weight of one channel) come in a padded row: the call has to say so, or
+    a K that is no multiple of 16 takes the loads for rows without alignment."""
+    require_gpu()
+    seen = []
+    call = fg.fp32gemm_s8gemm_with_config
+
+    def spy(*args):
+        seen.append((args[5], args[8]))
+        return call(*args)
+
+    monkeypatch.setattr(fg, "fp32gemm_s8gemm_with_config", spy)
+    g = torch.Generator().manual_seed(6)
+    one, more = torch.randn(1, 1001, generator=g).cuda(), torch.randn(70, 1001, generator=g).cuda()
+    (c1, s1), (c2, s2) = fg.quantize_s8(one), fg.quantize_s8(more)
+    tile = fg.config_names(fg.KIND_S8GEMM).index("64x64_k1_s4")
+    for a, sa, b, sb in ((c1, s1, c2, s2), (c2, s2, c1, s1), (c2[9:10], s2[9:10], c2, s2)):
+        z, bound = ref.gemm(a.cpu(), sa.cpu(), b.cpu(), sb.cpu(), 0.0, None, None, False, 0)
+        for cfg in (-1, tile):
+            y = fg.gemm_s8(a, sa, b.t(), sb, config=cfg)
+            assert seen[-1] == (1024, 1024)
+            assert bool(((y.cpu().double() - z).abs() <= bound).all())
+    # a row that is stored by itself, a step that is less than a row, and one past the library's limit
+    for row in (c1.as_strided((1, 1001), (1001, 1)), c1.as_strided((1, 1001), (7, 1)),
+                torch.zeros(1, 1, dtype=torch.int8, device="cuda").as_strided((1, 1), (1 << 21, 1))):
+        w = torch.zeros(3, row.shape[1], dtype=torch.int8, device="cuda")
+        fg.gemm_s8(row, s1, w.t(), torch.ones(3, device="cuda"))
+        assert seen[-1][0] == row.shape[1]
