@@ -8,6 +8,7 @@ with device pointers given as ints or torch tensors, and return the C return
 code.  ``gemm``, ``gemm_s8``, ``quantize_s8`` and ``rmsnorm_s8`` are
 torch-tensor convenience wrappers that raise on error; the last three run on
 the tensors' device and on one of its streams, whichever device is current.
+No wrapper records a gradient: its inputs are constants to autograd.
 
 PyTorch serves only for device memory and streams.  The library must be built
 (``python -m fp32_gemm_06_amd.build``); there is no fallback of any kind when
@@ -485,6 +486,15 @@ class _On:
         return self._context.__exit__(*exc)
 
 
+def _written(*given):
+    """Autograd learns of the outputs that the caller gave: a backward pass that needs their old values
+    then refuses, as after any in-place operation."""
+    import torch
+    for t in given:
+        if t is not None and not t.is_inference():
+            torch.autograd.graph.increment_version(t)
+
+
 def _codes_out(M, K, out, scales, device):
     """Codes and scales, as given or new.  New rows of codes start at multiples of 128 bytes, whole
     cache lines, which s8gemm reads fastest, or of 16 where that would pad short rows by much."""
@@ -513,11 +523,13 @@ def quantize_s8(X, out=None, scales=None, stream=None):
     trans, ldx = _matrix(X, "X", allow_transposed=True)
     M, K = X.shape
     device = _one_device(("X", X), ("out", out), ("scales", scales))
+    given = (out, scales)
     with _On(device, stream) as s:
         out, ldq, scales = _codes_out(M, K, out, scales, device)
         rc = s8_quantize(trans, M, K, type, X, ldx, out, ldq, scales, s)
     if rc != 0:
         raise Fp32GemmError(rc)
+    _written(*given)
     return out, scales
 
 
@@ -537,6 +549,7 @@ def rmsnorm_s8(X, weight, eps=1e-6, residual=None, residual_out=None, out=None, 
     _vector(weight, "weight", K, X.dtype)
     device = _one_device(("X", X), ("weight", weight), ("residual", residual),
                          ("residual_out", residual_out), ("out", out), ("scales", scales))
+    given = (residual_out, out, scales)
     with _On(device, stream) as s:
         h = residual_out
         if h is None and residual is not None:
@@ -551,6 +564,7 @@ def rmsnorm_s8(X, weight, eps=1e-6, residual=None, residual_out=None, out=None, 
                         scales, s)
     if rc != 0:
         raise Fp32GemmError(rc)
+    _written(*given)
     return out, scales, X if h is None else h
 
 
@@ -597,6 +611,7 @@ def gemm_s8(A, scale_a, B, scale_b, C=None, beta: float = 0.0, dtype=None, bias=
         raise ValueError("beta != 0 needs C")
     device = _one_device(("A", A), ("scale_a", scale_a), ("B", B), ("scale_b", scale_b), ("bias", bias),
                          ("C", C))
+    given = C
     with _On(device, stream) as s:
         if C is None:
             C = torch.empty((M, N), dtype=dtype or torch.float32, device=device)
@@ -610,4 +625,5 @@ def gemm_s8(A, scale_a, B, scale_b, C=None, beta: float = 0.0, dtype=None, bias=
                                          type, C, max(ldc, N, 1), bias, int(act), s)
     if rc != 0:
         raise Fp32GemmError(rc if rc >= 0 or rc <= -100 else rc + 1)
+    _written(given)
     return C

@@ -267,3 +267,47 @@ def test_gemm_keeps_the_leading_dimension_of_one_row(monkeypatch):
         w = torch.zeros(3, row.shape[1], dtype=torch.int8, device="cuda")
         fg.gemm_s8(row, s1, w.t(), torch.ones(3, device="cuda"))
         assert seen[-1][0] == row.shape[1]
+
+
+@gpu
+def test_wrappers_tell_autograd_what_they_overwrite():
+    """A tensor that a backward pass still needs, given as an output: that pass has to refuse, as after
+    any in-place operation, and not to use the new values."""
+    require_gpu()
+    dev = "cuda"
+    w = torch.ones(32, device=dev)
+
+    def saved():
+        leaf = torch.randn(4, 32, device=dev, requires_grad=True)
+        h = leaf * 2
+        return h, (h * h).sum()
+
+    h, loss = saved()
+    fg.rmsnorm_s8(h, w, residual=torch.ones(4, 32, device=dev), residual_out=h)
+    with pytest.raises(RuntimeError, match="inplace"):
+        loss.backward()
+    h, loss = saved()
+    fg.rmsnorm_s8(torch.ones(4, 32, device=dev), w, residual=h, residual_out=h)
+    with pytest.raises(RuntimeError, match="inplace"):
+        loss.backward()
+    h, loss = saved()
+    q, s = fg.quantize_s8(torch.randn(4, 32, device=dev))
+    fg.gemm_s8(q, s, torch.zeros(32, 32, dtype=torch.int8, device=dev).t(), torch.ones(32, device=dev), C=h, beta=1.0)
+    with pytest.raises(RuntimeError, match="inplace"):
+        loss.backward()
+    # inputs are read only, and outputs made under no_grad or inference mode work as well
+    h, loss = saved()
+    fg.quantize_s8(h)
+    fg.rmsnorm_s8(h, w)
+    loss.backward()
+    before = (q._version, s._version)
+    fg.quantize_s8(torch.randn(4, 32, device=dev), out=q, scales=s)
+    assert q._version > before[0] and s._version > before[1]
+    before = q._version
+    with pytest.raises(fg.Fp32GemmError):
+        fg.rmsnorm_s8(torch.randn(4, 32, device=dev), w, eps=-1.0, out=q)
+    assert q._version == before  # nothing was written
+    with torch.inference_mode():
+        x = torch.randn(4, 32, device=dev)
+        fg.rmsnorm_s8(x, w, residual=x.clone(), residual_out=x)
+        fg.gemm_s8(q, s, q.t(), s, C=torch.zeros(4, 4, device=dev))
