@@ -59,18 +59,33 @@ const S8Config kConfigs[] = {
 #undef S8_TILE
 constexpr int kNumConfigs = sizeof(kConfigs) / sizeof(kConfigs[0]);
 
-// The dot products read W once for each kGemvRows rows of A, and stand to
-// choice up to twice that: from M = 9 on the tiles are always the quicker
-// (8 x 4096 x 4096: 6.9 us, tiles 6.1; 1: 4.9 against 5.4; 3 x 11008 x 4096:
-// 9.3 against 10.7).
-constexpr int kGemvRows = 4;
+// Where the fitted times decide between the dot products and the tiles, and
+// where they do not.  They come from N and K up to 11008 with W's codes in the
+// last-level cache, and what they say of few rows fails outside that: a round
+// of dot products costs nothing in them (gemv_r2's `each`), wide weights put one
+// row on 64 x 64 tiles.  So, measured with W from memory too:
+//   1 and 2 rows are dot products (1 x 32000 x 4096: 20.9 us, the best tiles
+//   30.6; 1 x 16384 x 4096 12.0 and 17.4; 1 x 28672 x 8192 36.4 and 43.6; over
+//   1981 fitted shapes 0.4% above the best, tiles alone 9%);
+//   3 and 4 are either, by the fitted times, which are not always right (4 x
+//   11008 x 4096 11.6 and 13.4; 4 x 28672 x 8192 51.3 and 43.9; 4 x 32000 x 4096
+//   26.8 and 30.7, and tiles are chosen);
+//   5 to 8 read W twice, and are either up to this N (8 x 131 x 10653 4.5 and
+//   6.6), tiles above (8 x 10931 x 443 10.2 and 5.2; 8 x 28672 x 8192 83.5 and
+//   44.3);
+//   from 9 rows on the tiles are always the quicker.
+constexpr int kGemvRows = 4, kGemvTwiceN = 2048;
+bool stands(bool dots, int M, int N) {
+  if (dots) return M <= kGemvRows || (M <= 2 * kGemvRows && N <= kGemvTwiceN);
+  return M > 2;
+}
 
 int pick(int M, int N, int K) {
   int best = -1;
   float least = 0.0f;
   for (int c = 0; c < kNumConfigs; ++c) {
     const S8Config &f = kConfigs[c];
-    if (f.BM == kGemvRows && M > 2 * kGemvRows) continue;
+    if (!stands(f.BM == kGemvRows, M, N)) continue;
     const float tiles = (float)((M - 1) / f.BM + 1) * (float)((N - 1) / f.BN + 1);
     const float rounds = ceilf(tiles / 256.0f), fill = tiles / (256.0f * rounds);
     const float t = f.fixed + f.each * rounds +

@@ -636,3 +636,18 @@ def test_tiles_of_more_than_one_launch():
         past = torch.isinf(got) & (got.sign() == z.sign()) & (z.abs() * (1 + 6.001 * ref.U32) >= 65520)
         near = z.abs() * (1 - 6.001 * ref.U32) < 65520
         assert bool((((got - z).abs() <= bound) & near | past).all()), n0
+
+
+def test_gemm_choice_for_few_rows():
+    """One and two rows are dot products whatever W's size, wide weights past the fitted sizes among them;
+    five to eight rows, which read W twice as dot products, are tiles where W is wide."""
+    sizes = [1, 64, 1000, 2048, 4096, 6400, 8448, 11008, 14336, 14592, 16384, 22784, 28672, 32000, 65536, 128256, 1 << 20]
+    dots = lambda M, N, K: CONFIGS[fg.fp32gemm_select_config(fg.KIND_S8GEMM, M, N, K)].startswith("gemv")
+    for N in sizes:
+        for K in (1, 128, 443, 1024, 4096, 8192, 11008, 28672, 131071):
+            assert dots(1, N, K) and dots(2, N, K), (N, K)
+            for M in (5, 6, 7, 8):
+                assert N <= 2048 or not dots(M, N, K), (M, N, K)
+            for M in (9, 64):
+                assert not dots(M, N, K), (M, N, K)
+    assert dots(8, 131, 10653) and dots(4, 11008, 4096)
