@@ -28,11 +28,15 @@ struct S8Config {
 // waves move more (256 x 128 tiles, 1536 x 4096 x 4096: 31.8 us with 16
 // waves, 35.7 with 8).  The five numbers are fitted to each configuration's
 // times on 6831 shapes (M 1 .. 4096, N and K 64 .. 11008, most of them drawn,
-// bf16 out) and 1722 large ones, and the shortest fitted time is chosen: 2.5%
-// above the best of the sixteen (geometric mean), 0.6% on the shapes that take
-// 20 us or more and 0.3% on the large ones.
+// bf16 out) and 1722 large ones, with three copies of the operands in turn, so
+// that a small W comes from the last-level cache.  The shortest fitted time is
+// chosen: 2.1% above the best of the sixteen (geometric mean; at most 50%),
+// 0.4% on the shapes that take 20 us or more and 0.3% on the large ones.
 // 64x64_k1_s4, the best one by itself, is 40% above.  On rows without
-// alignment (4618 shapes) the same choice is 4% and 2% above.
+// alignment (4618 shapes) the same choice is 3.5% and 1.2% above (at most 78%),
+// with W from memory (1 to 16 rows, N to 128256, K to 28672) 3% (at most 37%,
+// four rows of a wide W with a short K).  Beyond those sizes it is
+// extrapolated.
 #define S8_TILE(name, BM, BN, WM, WN, KS, NST, AHEAD, ...) \
   {name, BM, BN, __VA_ARGS__,                                               \
    s8_launch<S8Tile<BM, BN, WM, WN, KS, NST, AHEAD>, S8Tile<BM, BN, WM, WN, KS, NST, AHEAD>>}
@@ -66,7 +70,8 @@ constexpr int kNumConfigs = sizeof(kConfigs) / sizeof(kConfigs[0]);
 // row on 64 x 64 tiles.  So, measured with W from memory too:
 //   1 and 2 rows are dot products (1 x 32000 x 4096: 20.9 us, the best tiles
 //   30.6; 1 x 16384 x 4096 12.0 and 17.4; 1 x 28672 x 8192 36.4 and 43.6; over
-//   1981 fitted shapes 0.4% above the best, tiles alone 9%);
+//   the 1981 fitted shapes of one and two rows the quicker dot products are 0.3
+//   to 0.9% above the best, the quickest tiles 8 to 16%);
 //   3 and 4 are either, by the fitted times, which are not always right (4 x
 //   11008 x 4096 11.6 and 13.4; 4 x 28672 x 8192 51.3 and 43.9; 4 x 32000 x 4096
 //   26.8 and 30.7, and tiles are chosen);

@@ -5,6 +5,8 @@ reference's; a norm's scale is off by one rounding to fp32; a product by the
 fp32 roundings of its epilogue and the rounding to C's type, counted in
 s8_reference.gemm.
 """
+import os
+
 import numpy as np
 import pytest
 import torch
@@ -651,3 +653,21 @@ def test_gemm_choice_for_few_rows():
             for M in (9, 64):
                 assert not dots(M, N, K), (M, N, K)
     assert dots(8, 131, 10653) and dots(4, 11008, 4096)
+
+
+@pytest.mark.parametrize("name,mean,most", [("s8_aligned", 1.025, 1.55), ("s8_unaligned", 1.04, 1.85),
+                                            ("s8_large", 1.01, 1.2), ("s8_wide_cold", 1.04, 1.45)])
+def test_gemm_choice_against_recorded_times(name, mean, most):
+    """The chosen configuration's time over the best one's, in the recorded times of all of them."""
+    path = os.path.join(os.path.dirname(__file__), "..", "profiles", "sweeps", name + ".csv")
+    with open(path) as f:
+        lines = [line.split(",") for line in f.read().split("\n") if line]
+    assert lines[0][3:] == CONFIGS
+    ratios = []
+    for line in lines[1:]:
+        times = [float(t) if t else None for t in line[3:]]
+        chosen = times[fg.fp32gemm_select_config(fg.KIND_S8GEMM, *map(int, line[:3]))]
+        if chosen is not None:
+            ratios.append(chosen / min(t for t in times if t is not None))
+    assert len(ratios) > 0.9 * (len(lines) - 1)
+    assert np.exp(np.log(ratios).mean()) < mean and max(ratios) < most
