@@ -8,6 +8,8 @@ with device pointers given as ints or torch tensors, and return the C return
 code.  ``gemm``, ``gemm_s8``, ``quantize_s8`` and ``rmsnorm_s8`` are
 torch-tensor convenience wrappers that raise on error; the last three run on
 the tensors' device and on one of its streams, whichever device is current.
+With ``stream=`` they order nothing between it and the stream that made the
+inputs, nor keep those alive for it (``wait_stream``, ``record_stream``).
 No wrapper records a gradient: its inputs are constants to autograd.
 
 PyTorch serves only for device memory and streams.  The library must be built

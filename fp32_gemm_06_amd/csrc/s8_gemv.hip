@@ -8,11 +8,13 @@
 // pair.  The loads of UNROLL blocks are in flight together.  KW waves of a
 // workgroup share the same rows and split K.  The lanes' sums meet by
 // cross-lane additions, the waves' in LDS; they are integers, so the order
-// does not matter.  1 x 11008 x 4096: 8.3 us, W at 5.4 TB/s (16-row tiles 10.6);
-// 1 x 4096 x 4096 4.9 (5.4), most of it the launch; three or four rows, 9.3-9.6
-// and 5.4-5.8.  Two rows of W a wave: with one, A is read as often as W, with
-// four too few waves remain (4 x 11008 x 4096: 9.6, 9.6 and 14.0 us; 1 x 11007 x
-// 4095 without alignment 9.7, 9.9 and 10.4).
+// does not matter.  W from memory: 1 x 11008 x 4096 9.2 us, 4.9 TB/s (16-row
+// tiles 13.9); 1 x 4096 x 4096 4.9 (6.0), most of it the launch; 1 x 128256 x
+// 4096 84.7, 6.2 TB/s; four rows 11.8, 6.3 and 99.  From the last-level cache
+// the first two take 8.2 and 4.7, four rows 9.6 and 5.5.  Two rows of W a wave:
+// with one, A is read as often as W, with four too few waves remain (from the
+// cache, 4 x 11008 x 4096: 9.6, 9.6 and 14.0 us; 1 x 11007 x 4095 without
+// alignment 9.7, 9.9 and 10.4).
 #include "s8_kernel.h"
 
 namespace fp32gemm {

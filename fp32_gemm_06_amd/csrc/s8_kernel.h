@@ -47,9 +47,10 @@ struct S8Tile {
   static constexpr int STAGE = SLICE * KS;
   static constexpr int NIA = KS * BM / RL / WAVES;  // 1 KB loads per wave per stage
   static constexpr int NIB = KS * BN / RL / WAVES;
-  // Stages in registers on the path that loads through them: as many as fit
-  // beside the rest (one more each than 3 / 2 / 1 takes 2 to 5% off the small
-  // tiles and spills on the largest).
+  // Stages in registers on the path that loads through them (one more each
+  // than 3 / 2 / 1 takes 2 to 5% off the small tiles and spills on the
+  // largest).  Three leave 192x128 one workgroup a CU there (162 registers),
+  // which has two on the 128-bit path.
   static constexpr int REG = NIA + NIB <= 4 ? 4 : NIA + NIB <= 6 ? 3 : 1;
   // One wave a K group: it loads what it reads, and nothing is shared before the end.
   static constexpr bool OWN = WT == 1;
@@ -199,6 +200,7 @@ template <class F> __device__ __forceinline__ void s8_finish_one(const S8Args &a
 template <class T, bool DMA>
 __global__ void __launch_bounds__(T::NT) s8_kernel(S8Args a, int tiles_m, int tiles_n, int group_m) {
   constexpr int BM = T::BM, BN = T::BN, KS = T::KS;
+  // (the register path uses two of the NST stages)
   __shared__ __attribute__((aligned(16))) char lds[T::NST * T::STAGE];
   const int tid = threadIdx.x;
   const int lane = tid & 63;

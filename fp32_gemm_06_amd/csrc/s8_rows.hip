@@ -13,8 +13,10 @@
 // pass, and no value is normalised before it is coded.  The row stays in
 // registers between that pass and the codes, so memory is read once.  The
 // sum of squares is kept in 64 bits: squares of float32 values pass its range.
-// Bound by memory: 8192 x 4096 bf16 with residual 40.9 us, 5.74 TB/s; what
-// comes before one row's last byte is one wave's latency (1 x 4096: 3.3 us).
+// Bound by memory: 8192 x 4096 bf16 with residual 43.9 us, 5.35 TB/s (a copy of
+// 1 GiB 5.16).  One row is one workgroup's latency, from the loads through the
+// reduction to the codes (1 x 4096, eight waves: 3.1 us, launch and all, in a
+// captured run of calls).
 #include "s8_common.h"
 
 namespace fp32gemm {
@@ -278,8 +280,9 @@ template <class T, bool NORM, bool WHOLE> hipError_t launch_rows(const S8RowArgs
     a.scales += m0;
     // Whole waves of threads with NV chunks each.  With a row or less for each
     // CU its latency counts, and one chunk a thread is the quicker (bf16 norm,
-    // 128 x 4096: 3.7 against 4.9 us); with more rows two chunks in flight
-    // are (8192 x 4096: 40.9 against 47.9).  Four spill in fp32.
+    // 128 x 4096: 3.6 against 4.5 us); with many rows two chunks in flight
+    // are (8192 x 4096: 43.8 against 45.1).  In between one would still be the
+    // quicker by 5 to 10% (512 x 4096: 5.7 against 6.0).  Four spill in fp32.
     auto threads = [&](int nv) { return (chunks + 64 * nv - 1) / (64 * nv) * 64; };
     if (chunks <= 64)
       rows_kernel<T, NORM, 4, 1, WHOLE><<<(a.M + 3) / 4, 256, 0, s>>>(a);
@@ -480,11 +483,13 @@ __global__ void columns_scale_kernel(float *scales, int M) {
 template <class T> hipError_t launch_columns(const S8RowArgs &a, hipStream_t s) {
   constexpr int CB = Columns<T>::CB;
   const int groups = (a.M - 1) / CB + 1, chunks = (a.K + CK - 1) / CK;
-  // With half the CUs or fewer busy, K over workgroups and four launches (14 to
-  // 20 us at least) are the quicker once K is long: fp32, 100 columns of 16384,
-  // 14.4 against 70.8 us, of 4096 13.8 against 15.8, 1000 of 3000 14.3 against
-  // 14.2; bf16, whose workgroups have twice the columns, 4096 of 4096 25.5
-  // against 28.6, of 2000 17.3 against 16.1.
+  // With half the CUs or fewer busy, K over workgroups and four launches (12 us
+  // at least) are the quicker once K is long: fp32, 100 columns of 16384, 14.2
+  // against 69.7 us, 1000 of 5000 18.1 against 23.8, of 3000 14.4 against 15.0;
+  // bf16, whose workgroups have twice the columns, 4096 of 4096 25.5 against
+  // 29.6, of 2000 18.2 against 16.4.  The rule is coarse on both sides (fp32,
+  // 100 of 4096 would take 11.6 split and takes 15.9; 2048 of 5000 18.2 unsplit
+  // and takes 22.8).
   if (groups <= 128 && chunks > (sizeof(T) == 4 ? 4 : 2)) {
     const int small = (a.M - 1) / 256 + 1;
     columns_clear_kernel<<<small, 256, 0, s>>>(a.scales, a.M);
@@ -494,10 +499,12 @@ template <class T> hipError_t launch_columns(const S8RowArgs &a, hipStream_t s) 
     return hipGetLastError();
   }
   // Registers for 4096 k of fp32 save the second reading, and cost the second
-  // workgroup of a CU (11008 columns of 4096: 61.8 us, holding 1024 k 70.0);
+  // workgroup of a CU (11008 columns of 4096: 67.4 us, holding 1024 k 72.3);
   // up to K = 1024, and for 16-bit values, whose second reading is half as
-  // long, the two workgroups are worth more (16384 of 1024: 18.0 against
-  // 23.4; bf16, 11008 of 4096: 49.6 against 53.2).
+  // long, the two workgroups are worth more (16384 of 1024: 17.4 against
+  // 23.2; bf16, 11008 of 4096: 61.5 against 65.0, but 16384 of 4096 82.1
+  // against 77.8).  X from memory; from the last-level cache 48 and 61, and 49
+  // and 53.
   if constexpr (sizeof(T) == 4) {
     if (a.K > CK) {
       columns_kernel<T, 4><<<groups, CT, 0, s>>>(a);

@@ -20,10 +20,10 @@
  *    owned by the caller.  The library keeps no reference after the call's
  *    kernels finish.  C must not overlap A or B.
  *  - Arithmetic: fp32 throughout (fp32 MFMA or fp32 FMA); no conversion to a
- *    narrower format (the s8 routines below say what theirs is).  The order of the k-sum is unspecified, so results may
- *    differ from a sequential loop by rounding.  Repeated calls with the same
- *    arguments and configuration give bit-identical results (no atomics on
- *    floats).
+ *    narrower format (the s8 routines below say what theirs is).  The order
+ *    of the k-sum is unspecified, so results may differ from a sequential
+ *    loop by rounding.  Repeated calls with the same arguments and
+ *    configuration give bit-identical results (no atomics on floats).
  *  - Reads: when beta == 0, C is not read (NaN in C does not propagate).
  *    When alpha == 0 or K == 0, A and B are not read (they may be NULL) and
  *    C <- beta * C.  When M == 0 or N == 0 the call does nothing.
@@ -288,9 +288,9 @@ int fp32gemm_splitk_splits(int M, int N, int K);
  * Rows of codes that start at multiples of 16 bytes (base address and leading
  * dimension) take 128-bit loads; the up to 15 bytes that follow a row's K
  * codes, inside its leading dimension, may then be read, and their values do
- * not matter.  Rows from multiples of 128 bytes are whole cache lines (s8gemm
- * of 777 x 1280 x 4096: 12.9 us; with a leading dimension of 4112 16.4, of
- * 4099 24).
+ * not matter.  The path is chosen for both operands together.  Rows from
+ * multiples of 128 bytes are whole cache lines (s8gemm of 777 x 1280 x 4096,
+ * fp32 out: 13.8 us; with a leading dimension of 4112 16.3, of 4099 22.1).
  *
  * Beyond that the conventions at the top of this file hold: asynchronous, no
  * allocation, no workspace, results that are bit-identical from call to call,
@@ -341,7 +341,8 @@ int s8_quantize(int trans, int M, int K, int type, const void *X, int ldx,
  * 64 bits.  H may be X or R itself (the same address and leading dimension)
  * to update the residual stream in place; it must not overlap them otherwise.
  * R's and H's leading dimensions are not looked at when they are NULL.  Rows
- * with an infinity or a NaN, of zeros, or of no values, as in s8_quantize.
+ * with an infinity or a NaN among their v_ik (a sum past the type's range or a
+ * product past fp32's is one), of zeros, or of no values, as in s8_quantize.
  * Argument positions for error codes: M 1, K 2, type 3, X 4, ldx 5, R 6,
  * ldr 7, H 8, ldh 9, W 10, eps 11 (negative or not finite), Q 12, ldq 13,
  * scales 14, stream 15.
@@ -380,9 +381,10 @@ const char *fp32gemm_strerror(int code);
  * 参数自动调优": the tile parameters (block tile, K depth, wave tile) are
  * enumerated, each candidate is timed on the target GPU, and the fastest per
  * shape goes into a table, because the best choice differs between GPUs.
- * The tuner (fp32_gemm_06_amd/tune.py) drives the sweep through these calls.
+ * The tuner (fp32_gemm_06_amd/tune.py) drives the sweep of kinds 0 and 1
+ * through these calls.
  * kind 0 = the SGEMM kernel family, kind 1 = the GEMV family, kind 2 = the
- * 8-bit product (s8gemm).
+ * 8-bit product (s8gemm), whose choice is by fitted times and not a table.
  * Configurations are numbered 0 .. fp32gemm_num_configs(kind)-1 and named by
  * fp32gemm_config_name (NULL for an unknown id); an unknown kind gives 0
  * configurations, NULL names and FP32GEMM_ERR_CONFIG selections.
