@@ -1,12 +1,13 @@
-"""Python binding of libfp32gemm.so (fp32 SGEMM / small-M SGEMV, and an 8-bit
-linear layer, for MI355X).
+"""Python binding of libfp32gemm.so (fp32 SGEMM / small-M SGEMV, an 8-bit
+linear layer, and decode attention over a paged cache, for MI355X).
 
 Argument marshalling only: every step of the computation runs in the HIP
 kernels of the shared library.  The functions with the C names (``sgemm``,
 ``sgemv``, ``fp32gemm_*``) take the same arguments as the C entry points,
 with device pointers given as ints or torch tensors, and return the C return
-code.  ``gemm``, ``gemm_s8``, ``quantize_s8`` and ``rmsnorm_s8`` are
-torch-tensor convenience wrappers that raise on error; the last three run on
+code.  ``gemm``, ``gemm_s8``, ``quantize_s8``, ``rmsnorm_s8``, ``norm_rope``,
+``cache_write``, ``rope_write``, ``cache_read`` and ``attention`` are
+torch-tensor convenience wrappers that raise on error; all but the first run on
 the tensors' device and on one of its streams, whichever device is current.
 With ``stream=`` they order nothing between it and the stream that made the
 inputs, nor keep those alive for it (``wait_stream``, ``record_stream``).
@@ -66,6 +67,28 @@ _S8_QUANTIZE_ARGTYPES = [ctypes.c_int] * 4 + [ctypes.c_void_p, ctypes.c_int] * 2
 _S8_RMSNORM_ARGTYPES = [ctypes.c_int] * 3 + [ctypes.c_void_p, ctypes.c_int] * 3 + [
     ctypes.c_void_p, ctypes.c_float, ctypes.c_void_p, ctypes.c_int] + [ctypes.c_void_p] * 2
 
+TYPE_S8 = 3
+ROPE_HALVES = 0
+ROPE_PAIRS = 1
+
+
+class fp32gemm_kv_cache(ctypes.Structure):
+    """The paged cache as the C entry points take it."""
+    _fields_ = [(n, ctypes.c_int) for n in ("type", "pages", "page_size", "heads", "dim")] + [
+        (n, ctypes.c_void_p) for n in ("K", "V", "scaleK", "scaleV")]
+
+
+_int, _ptr = ctypes.c_int, ctypes.c_void_p
+_CACHE = ctypes.POINTER(fp32gemm_kv_cache)
+_QK_NORM_ROPE_ARGTYPES = [_int] * 3 + [_int, _ptr, _int, _ptr, _int, _ptr] * 2 + [
+    ctypes.c_float, _int, _int, _ptr, _ptr, _ptr]
+_QKV_ROPE_WRITE_ARGTYPES = [_int] * 3 + [_ptr, _int, _ptr, _int, _ptr] + [_ptr, _int, _ptr] + [
+    _ptr, _int, ctypes.c_float, _int, _int, _ptr, _ptr, _ptr, _CACHE, _ptr]
+_KV_WRITE_ARGTYPES = [_int, _int, _ptr, _int, _ptr, _int, _ptr, _CACHE, _ptr]
+_KV_READ_ARGTYPES = [_int, _ptr, _CACHE, _int, _ptr, _int, _ptr, _int, _ptr]
+_KV_ATTENTION_ARGTYPES = [_int] * 3 + [_ptr, _int, _CACHE, _ptr, _int, _ptr, _int, ctypes.c_float, _ptr, _int,
+                                       _ptr, _ptr, ctypes.c_size_t, _ptr]
+
 # Every symbol include/fp32gemm.h declares.
 EXPORTS = ("sgemm", "sgemv", "sgemm_ex", "sgemm_strided_batched", "sgemm_fused", "sgemm_splitk",
            "sgemm_splitk_noalloc", "sgemm_splitk_workspace_size", "fp32gemm_splitk_splits",
@@ -74,7 +97,8 @@ EXPORTS = ("sgemm", "sgemv", "sgemm_ex", "sgemm_strided_batched", "sgemm_fused",
            "fp32gemm_num_configs", "fp32gemm_config_name", "fp32gemm_select_config",
            "fp32gemm_config_max_rows", "fp32gemm_round_split", "fp32gemm_sgemm_with_config",
            "fp32gemm_sgemv_with_config", "s8gemm", "s8_quantize", "s8_rmsnorm",
-           "fp32gemm_s8gemm_with_config")
+           "fp32gemm_s8gemm_with_config", "qk_norm_rope", "qkv_rope_write", "kv_write", "kv_read",
+           "kv_attention", "kv_attention_workspace_size")
 
 
 class Fp32GemmError(RuntimeError):
@@ -149,6 +173,14 @@ def lib():
         L.s8_rmsnorm.restype = ctypes.c_int
         L.fp32gemm_s8gemm_with_config.argtypes = [ctypes.c_int] + _S8GEMM_ARGTYPES
         L.fp32gemm_s8gemm_with_config.restype = ctypes.c_int
+        for name, argtypes in (("qk_norm_rope", _QK_NORM_ROPE_ARGTYPES),
+                               ("qkv_rope_write", _QKV_ROPE_WRITE_ARGTYPES),
+                               ("kv_write", _KV_WRITE_ARGTYPES), ("kv_read", _KV_READ_ARGTYPES),
+                               ("kv_attention", _KV_ATTENTION_ARGTYPES)):
+            getattr(L, name).argtypes = argtypes
+            getattr(L, name).restype = ctypes.c_int
+        L.kv_attention_workspace_size.argtypes = [_int, _int, _CACHE]
+        L.kv_attention_workspace_size.restype = ctypes.c_size_t
         _lib = L
     return _lib
 
@@ -302,6 +334,51 @@ def fp32gemm_s8gemm_with_config(cfg, M, N, K, A, lda, scaleA, B, ldb, scaleB, be
     return lib().fp32gemm_s8gemm_with_config(cfg, M, N, K, _addr(A), lda, _addr(scaleA), _addr(B),
                                              ldb, _addr(scaleB), beta, type, _addr(C), ldc,
                                              _addr(bias), act, _stream(stream))
+
+
+def _cache(cache):
+    """A KVCache, an fp32gemm_kv_cache or None, as ctypes passes it."""
+    return cache._c if isinstance(cache, KVCache) else cache
+
+
+def qk_norm_rope(T, D, type, Hq, Q, ldq, Yq, ldyq, Wq, Hk, K, ldk, Yk, ldyk, Wk, eps, R, style, freq, pos,
+                 stream=None) -> int:
+    """Yq, Yk <- the heads of Q and K normalised (Wq, Wk; None: not) and turned by pos freq."""
+    return lib().qk_norm_rope(T, D, type, Hq, _addr(Q), ldq, _addr(Yq), ldyq, _addr(Wq), Hk, _addr(K), ldk,
+                              _addr(Yk), ldyk, _addr(Wk), eps, R, style, _addr(freq), _addr(pos),
+                              _stream(stream))
+
+
+def qkv_rope_write(T, type, Hq, Q, ldq, Yq, ldyq, Wq, K, ldk, Wk, V, ldv, eps, R, style, freq, pos, slots, cache,
+                   stream=None) -> int:
+    """qk_norm_rope with the keys, and the values as they are, written to the cache's slots."""
+    return lib().qkv_rope_write(T, type, Hq, _addr(Q), ldq, _addr(Yq), ldyq, _addr(Wq), _addr(K), ldk,
+                                _addr(Wk), _addr(V), ldv, eps, R, style, _addr(freq), _addr(pos),
+                                _addr(slots), _cache(cache), _stream(stream))
+
+
+def kv_write(T, type, K, ldk, V, ldv, slots, cache, stream=None) -> int:
+    """The cache's rows at slots <- the heads of K and V."""
+    return lib().kv_write(T, type, _addr(K), ldk, _addr(V), ldv, _addr(slots), _cache(cache), _stream(stream))
+
+
+def kv_read(T, slots, cache, type, K, ldk, V, ldv, stream=None) -> int:
+    """K, V <- the cache's rows at slots, as floats of ``type``."""
+    return lib().kv_read(T, _addr(slots), _cache(cache), type, _addr(K), ldk, _addr(V), ldv, _stream(stream))
+
+
+def kv_attention(B, type, Hq, Q, ldq, cache, table, ldt, lengths, window, scale, O, ldo, lse, workspace,
+                 workspace_bytes, stream=None) -> int:
+    """O (and lse, or None) <- attention of one token for each of B sequences
+    over the paged cache; the workspace (kv_attention_workspace_size bytes) is
+    the caller's and holds zeros before its first use."""
+    return lib().kv_attention(B, type, Hq, _addr(Q), ldq, _cache(cache), _addr(table), ldt, _addr(lengths),
+                              window, scale, _addr(O), ldo, _addr(lse), _addr(workspace), workspace_bytes,
+                              _stream(stream))
+
+
+def kv_attention_workspace_size(B, Hq, cache) -> int:
+    return lib().kv_attention_workspace_size(B, Hq, _cache(cache))
 
 
 def fp32gemm_strerror(code: int) -> str:
@@ -629,3 +706,295 @@ def gemm_s8(A, scale_a, B, scale_b, C=None, beta: float = 0.0, dtype=None, bias=
         raise Fp32GemmError(rc if rc >= 0 or rc <= -100 else rc + 1)
     _written(given)
     return C
+
+
+class KVCache:
+    """A paged cache of keys and values on tensors of the caller.
+
+    ``k`` and ``v`` are contiguous GPU tensors pages x heads x page size x
+    head size: int8 codes with float32 ``k_scale`` and ``v_scale`` (pages x
+    heads x page size), or floats without.  A token's slot is page * page size
+    + offset.  ``KVCache.empty`` makes the tensors, with zeros in them.
+    """
+
+    def __init__(self, k, v, k_scale=None, v_scale=None):
+        import torch
+        lib()
+        types = {torch.float32: TYPE_F32, torch.float16: TYPE_F16, torch.bfloat16: TYPE_BF16,
+                 torch.int8: TYPE_S8}
+        if k.dtype not in types or v.dtype != k.dtype:
+            raise TypeError("k and v must be int8, float32, float16 or bfloat16, both the same")
+        if k.dim() != 4 or k.shape != v.shape:
+            raise ValueError("k and v must be pages x heads x page size x head size, both the same")
+        codes = k.dtype == torch.int8
+        if codes != (k_scale is not None) or codes != (v_scale is not None):
+            raise ValueError("codes have scales, floats have none")
+        self.device = _one_device(("k", k), ("v", v), ("k_scale", k_scale), ("v_scale", v_scale))
+        for name, t in (("k", k), ("v", v), ("k_scale", k_scale), ("v_scale", v_scale)):
+            if t is None:
+                continue
+            if t.device.type != "cuda":
+                raise ValueError(f"{name} must be a GPU tensor")
+            if not t.is_contiguous():
+                raise ValueError(f"{name} must be contiguous")
+        for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+            if t is not None and (t.dtype != torch.float32 or t.shape != k.shape[:3]):
+                raise ValueError(f"{name} must be float32, pages x heads x page size")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.pages, self.heads, self.page_size, self.dim = k.shape
+        self.dtype = k.dtype
+        self._c = fp32gemm_kv_cache(types[k.dtype], self.pages, self.page_size, self.heads, self.dim,
+                                    *(None if t is None else t.data_ptr() for t in (k, v, k_scale, v_scale)))
+
+    @classmethod
+    def empty(cls, pages, page_size, heads, dim, dtype=None, device="cuda"):
+        """A cache of ``dtype`` (int8 by default) on new tensors."""
+        import torch
+        dtype = dtype or torch.int8
+        k, v = (torch.zeros((pages, heads, page_size, dim), dtype=dtype, device=device) for _ in range(2))
+        if dtype != torch.int8:
+            return cls(k, v)
+        return cls(k, v, *(torch.zeros((pages, heads, page_size), device=device) for _ in range(2)))
+
+    def _tensors(self):
+        return self.k, self.v, self.k_scale, self.v_scale
+
+
+def _heads(t, name, dtype, shape=None):
+    """Leading dimension of a tokens x heads x head size GPU tensor whose
+    tokens' heads lie one behind the other."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be tokens x heads x head size")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.device.type != "cuda":
+        raise ValueError(f"{name} must be a GPU tensor")
+    T, H, D = t.shape
+    if not t.numel():
+        return max(1, H * D)
+    if (D > 1 and t.stride(2) != 1) or (H > 1 and t.stride(1) != D):
+        raise ValueError(f"{name}'s heads must be packed, values next to each other")
+    ld = t.stride(0) if T > 1 else H * D
+    if ld < H * D:
+        raise ValueError(f"{name}'s tokens must not overlap")
+    return ld
+
+
+def _style(style):
+    if style in ("halves", ROPE_HALVES):
+        return ROPE_HALVES
+    if style in ("pairs", ROPE_PAIRS):
+        return ROPE_PAIRS
+    raise ValueError("style must be 'halves' or 'pairs'")
+
+
+def _turning(positions, freq, T, D):
+    """How many values of a head turn."""
+    import torch
+    if freq is None:
+        if positions is not None:
+            raise ValueError("positions need freq")
+        return 0
+    if positions is None:
+        raise ValueError("freq needs positions")
+    _vector(freq, "freq", freq.numel(), torch.float64)
+    _vector(positions, "positions", T, torch.int32)
+    if 2 * freq.numel() > D:
+        raise ValueError(f"freq has {freq.numel()} values, for a head of {D}")
+    return 2 * freq.numel()
+
+
+def norm_rope(q, k, positions=None, freq=None, q_weight=None, k_weight=None, eps=1e-6, style="halves",
+              out_q=None, out_k=None, stream=None):
+    """Torch wrapper of qk_norm_rope: (queries, keys), each head normalised by
+    its root mean square and multiplied by its weight (None: neither), then
+    turned by the angles ``positions[t] * freq[i]``.
+
+    ``q`` (tokens x heads x head size) and ``k`` may be views of a projection's
+    output; either may be None.  ``freq`` (float64) holds an angle's step for
+    each of the pairs that turn, the first values of a head: value i with i +
+    len(freq) (``style`` "halves") or 2 i with 2 i + 1 ("pairs").
+    ``positions`` are int32.  ``out_q`` and ``out_k`` may be ``q`` and ``k``.
+    """
+    import torch
+    one = q if q is not None else k
+    if one is None:
+        raise ValueError("q or k is needed")
+    type = _float_type(one, "q" if q is not None else "k")
+    if one.dim() != 3:
+        raise ValueError("q and k must be tokens x heads x head size")
+    T, _, D = one.shape
+    R, style = _turning(positions, freq, T, D), _style(style)
+    device = _one_device(("q", q), ("k", k), ("positions", positions), ("freq", freq), ("q_weight", q_weight),
+                         ("k_weight", k_weight), ("out_q", out_q), ("out_k", out_k))
+    given = (out_q, out_k)
+    sides = []
+    for name, x, w, y in (("q", q, q_weight, out_q), ("k", k, k_weight, out_k)):
+        if x is None:
+            if w is not None or y is not None:
+                raise ValueError(f"{name} is None, its weight or output is not")
+            sides.append([0, None, 1, None, 1, None])
+            continue
+        if x.dim() != 3 or x.shape[0] != T or x.shape[2] != D:
+            raise ValueError("q and k must be tokens x heads x head size, heads of one size")
+        ld = _heads(x, name, one.dtype)
+        if w is not None:
+            _vector(w, f"{name}_weight", D, one.dtype)
+        ldy = 0 if y is None else _heads(y, f"out_{name}", one.dtype, x.shape)
+        sides.append([x.shape[1], x, ld, y, ldy, w])
+    with _On(device, stream) as s:
+        for side in sides:
+            if side[1] is not None and side[3] is None:
+                side[3] = torch.empty(side[1].shape, dtype=one.dtype, device=device)
+                side[4] = max(1, side[0] * D)
+        rc = qk_norm_rope(T, D, type, *sides[0], *sides[1], float(eps), R, style, freq, positions, s)
+    if rc != 0:
+        raise Fp32GemmError(rc)
+    _written(*given)
+    return sides[0][3], sides[1][3]
+
+
+def _rows_for(cache, k, v):
+    """(tokens, type, leading dimensions) of keys and values for a cache."""
+    import torch
+    type = _float_type(k, "k")
+    if cache.dtype not in (torch.int8, k.dtype):
+        raise TypeError(f"the cache holds {cache.dtype}, k is {k.dtype}")
+    shape = (k.shape[0], cache.heads, cache.dim)
+    return shape[0], type, _heads(k, "k", k.dtype, shape), _heads(v, "v", k.dtype, shape)
+
+
+def cache_write(cache, k, v, slots, stream=None):
+    """Torch wrapper of kv_write: the keys and values of ``slots`` (int32, all
+    different; those outside the cache are skipped) in ``cache``, from ``k``
+    and ``v`` (tokens x heads x head size)."""
+    import torch
+    T, type, ldk, ldv = _rows_for(cache, k, v)
+    _vector(slots, "slots", T, torch.int32)
+    device = _one_device(("k", k), ("v", v), ("slots", slots), ("the cache", cache.k))
+    with _On(device, stream) as s:
+        rc = kv_write(T, type, k, ldk, v, ldv, slots, cache, s)
+    if rc != 0:
+        raise Fp32GemmError(rc)
+    _written(*cache._tensors())
+
+
+def rope_write(cache, q, k, v, slots, positions=None, freq=None, q_weight=None, k_weight=None, eps=1e-6,
+               style="halves", out_q=None, stream=None):
+    """Torch wrapper of qkv_rope_write: norm_rope of ``q`` and ``k`` with the
+    keys, and ``v`` as it is, going to ``slots`` of ``cache`` as in
+    cache_write.  Returns the queries (``out_q``, or a new tensor)."""
+    import torch
+    T, type, ldk, ldv = _rows_for(cache, k, v)
+    D = cache.dim
+    if q.dim() != 3:
+        raise ValueError("q must be tokens x heads x head size")
+    shape = (T, q.shape[1], D)
+    ldq = _heads(q, "q", k.dtype, shape)
+    R, style = _turning(positions, freq, T, D), _style(style)
+    _vector(slots, "slots", T, torch.int32)
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is not None:
+            _vector(w, name, D, k.dtype)
+    device = _one_device(("q", q), ("k", k), ("v", v), ("slots", slots), ("positions", positions), ("freq", freq),
+                         ("q_weight", q_weight), ("k_weight", k_weight), ("out_q", out_q), ("the cache", cache.k))
+    given = out_q
+    with _On(device, stream) as s:
+        if out_q is None:
+            out_q = torch.empty(shape, dtype=k.dtype, device=device)
+        ldy = _heads(out_q, "out_q", k.dtype, shape)
+        rc = qkv_rope_write(T, type, shape[1], q, ldq, out_q, ldy, q_weight, k, ldk, k_weight, v, ldv, float(eps), R,
+                            style, freq, positions, slots, cache, s)
+    if rc != 0:
+        raise Fp32GemmError(rc)
+    _written(given, *cache._tensors())
+    return out_q
+
+
+def cache_read(cache, slots, dtype=None, out_k=None, out_v=None, stream=None):
+    """Torch wrapper of kv_read: (keys, values) at ``slots`` (int32), tokens x
+    heads x head size of ``dtype`` (the cache's own, or float32 for codes).
+    Rows of slots outside the cache are left as they were, zero in new tensors."""
+    import torch
+    if slots.dim() != 1:
+        raise ValueError("slots must be a vector")
+    T = slots.shape[0]
+    _vector(slots, "slots", T, torch.int32)
+    given = (out_k, out_v)
+    if dtype is None:
+        dtype = next((t.dtype for t in given if t is not None),
+                     torch.float32 if cache.dtype == torch.int8 else cache.dtype)
+    if cache.dtype not in (torch.int8, dtype):
+        raise TypeError(f"the cache holds {cache.dtype}, asked for {dtype}")
+    device = _one_device(("slots", slots), ("the cache", cache.k), ("out_k", out_k), ("out_v", out_v))
+    shape = (T, cache.heads, cache.dim)
+    with _On(device, stream) as s:
+        out = [torch.zeros(shape, dtype=dtype, device=device) if t is None else t for t in given]
+        lds = [_heads(t, name, dtype, shape) for t, name in zip(out, ("out_k", "out_v"))]
+        rc = kv_read(T, slots, cache, _float_type(out[0], "out_k"), out[0], lds[0], out[1], lds[1], s)
+    if rc != 0:
+        raise Fp32GemmError(rc)
+    _written(*given)
+    return out[0], out[1]
+
+
+def attention_workspace(cache, heads):
+    """A workspace for attention of ``heads`` query heads over ``cache``: for
+    one call at a time, as often as wanted."""
+    import torch
+    size = kv_attention_workspace_size(1, heads, cache)
+    if size == 0:
+        raise ValueError(f"{heads} query heads do not go with the cache's {cache.heads} heads of {cache.dim}")
+    return torch.zeros(size, dtype=torch.uint8, device=cache.device)
+
+
+def attention(q, cache, table, lengths, scale=None, window=0, out=None, lse=None, workspace=None, stream=None):
+    """Torch wrapper of kv_attention: attention of one token for each sequence
+    over the paged cache, (sequences x heads x head size) as ``q``.
+
+    ``table`` (int32, sequences x pages) holds the pages that a sequence's
+    tokens lie on, ``lengths`` (int32) how many tokens it has, the new one
+    among them.  ``scale`` is 1 / sqrt(head size) by default; with ``window``
+    the last so many tokens are seen.  ``lse`` (float32, sequences x heads)
+    receives the scores' log-sum-exp.  ``workspace`` comes from
+    attention_workspace; without one the call makes its own and clears it.
+    """
+    import torch
+    if q.dim() != 3:
+        raise ValueError("q must be sequences x heads x head size")
+    type = _float_type(q, "q")
+    if cache.dtype not in (torch.int8, q.dtype):
+        raise TypeError(f"the cache holds {cache.dtype}, q is {q.dtype}")
+    B, Hq, _ = q.shape
+    ldq = _heads(q, "q", q.dtype, (B, Hq, cache.dim))
+    if table.dtype != torch.int32 or table.dim() != 2 or table.shape[0] != B:
+        raise ValueError("table must be an int32 matrix with a row for each sequence")
+    ldt = table.shape[1]
+    if not table.is_contiguous():
+        raise ValueError("table must be contiguous")
+    if table.device.type != "cuda":
+        raise ValueError("table must be a GPU tensor")
+    _vector(lengths, "lengths", B, torch.int32)
+    if lse is not None and (lse.dtype != torch.float32 or tuple(lse.shape) != (B, Hq) or not lse.is_contiguous()):
+        raise ValueError("lse must be a contiguous float32 matrix, sequences x heads")
+    if workspace is not None and (workspace.dtype != torch.uint8 or workspace.dim() != 1 or
+                                  not workspace.is_contiguous()):
+        raise ValueError("workspace must come from attention_workspace")
+    device = _one_device(("q", q), ("the cache", cache.k), ("table", table), ("lengths", lengths), ("out", out),
+                         ("lse", lse), ("workspace", workspace))
+    given = (out, lse)
+    with _On(device, stream) as s:
+        if out is None:
+            out = torch.empty(q.shape, dtype=q.dtype, device=device)
+        ldo = _heads(out, "out", q.dtype, q.shape)
+        if workspace is None:
+            workspace = attention_workspace(cache, Hq)
+        rc = kv_attention(B, type, Hq, q, ldq, cache, table, ldt, lengths, int(window),
+                          float(cache.dim ** -0.5 if scale is None else scale), out, ldo, lse, workspace,
+                          workspace.numel(), s)
+    if rc != 0:
+        raise Fp32GemmError(rc)
+    _written(*given)
+    return out

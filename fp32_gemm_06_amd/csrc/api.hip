@@ -6,7 +6,7 @@
 #include <mutex>
 
 #include "../../include/fp32gemm.h"
-#include "s8_common.h"
+#include "kv_common.h"
 
 using namespace fp32gemm;
 
@@ -259,6 +259,40 @@ int type_size(int type) { return type == kTypeF32 ? 4 : 2; }
 bool known_type(int type) { return type == kTypeF32 || type == kTypeF16 || type == kTypeBf16; }
 bool misaligned(const void *p, int size) { return (uintptr_t)p % (uintptr_t)size != 0; }
 
+// A cache as its operators take it (whether its type goes with the call's is
+// up to them); false when a field is bad.
+bool unpack_cache(const fp32gemm_kv_cache *c, KvCache *out) {
+  if (c == nullptr || (c->type != kTypeS8 && !known_type(c->type))) return false;
+  if (c->pages < 0 || c->page_size < 1 || c->heads < 1) return false;
+  if (c->dim < 16 || c->dim > 256 || c->dim % 16 != 0) return false;
+  if ((long long)c->pages * c->page_size > 0x7fffffff) return false;
+  if ((long long)c->pages * c->page_size * c->heads > 0x7fffffff) return false;
+  if (c->pages > 0) {
+    if (c->K == nullptr || c->V == nullptr || misaligned(c->K, 16) || misaligned(c->V, 16)) return false;
+    if (c->type == kTypeS8 && (c->scaleK == nullptr || c->scaleV == nullptr || misaligned(c->scaleK, 4) ||
+                               misaligned(c->scaleV, 4)))
+      return false;
+  }
+  *out = {c->type, c->pages, c->page_size, c->heads, c->dim, c->K, c->V, c->scaleK, c->scaleV};
+  return true;
+}
+
+// Matrix of heads: 0, or 1 for a bad address and 2 for a bad leading dimension.
+int bad_heads(const void *p, int ld, int T, int heads, int D, int type) {
+  if (heads == 0) return 0;
+  if ((long long)heads * D > ld || ld > kMaxLd) return 2;
+  return T > 0 && (p == nullptr || misaligned(p, type_size(type))) ? 1 : 0;
+}
+
+bool bad_eps(float eps) { return !(eps >= 0.0f) || eps > 3.4028235e38f; }
+
+// Workspace of kv_attention: the arrival counters, then the partial results.
+size_t attend_workspace(int Hq, const KvCache &c) {
+  const int G = Hq / c.heads;
+  return kAttendGroups * sizeof(unsigned) +
+         2 * kAttendGroups * attend_record(G < 16 ? G : 16, c.dim) * sizeof(float);
+}
+
 int s8gemm_call(int cfg, int base, int M, int N, int K, const signed char *A, int lda,
                 const float *scaleA, const signed char *B, int ldb, const float *scaleB, float beta,
                 int type, void *C, int ldc, const float *bias, int act, hipStream_t s) {
@@ -500,6 +534,164 @@ int fp32gemm_s8gemm_with_config(int cfg, int M, int N, int K, const signed char 
   if (cfg < -1 || cfg >= s8_num_configs()) return FP32GEMM_ERR_CONFIG;
   return s8gemm_call(cfg, 2, M, N, K, A, lda, scaleA, B, ldb, scaleB, beta, type, C, ldc, bias, act,
                      reinterpret_cast<hipStream_t>(stream));
+}
+
+int qk_norm_rope(int T, int D, int type, int Hq, const void *Q, int ldq, void *Yq, int ldyq,
+                 const void *Wq, int Hk, const void *K, int ldk, void *Yk, int ldyk, const void *Wk,
+                 float eps, int R, int style, const double *freq, const int *pos,
+                 fp32gemm_stream_t stream) {
+  if (T < 0) return -1;
+  if (D < 16 || D > 256 || D % 16 != 0) return -2;
+  if (!known_type(type)) return -3;
+  if (Hq < 0) return -4;
+  if (Hk < 0) return -10;
+  int e = bad_heads(Q, ldq, T, Hq, D, type);
+  if (e) return e == 1 ? -5 : -6;
+  e = bad_heads(Yq, ldyq, T, Hq, D, type);
+  if (e) return e == 1 ? -7 : -8;
+  e = bad_heads(K, ldk, T, Hk, D, type);
+  if (e) return e == 1 ? -11 : -12;
+  e = bad_heads(Yk, ldyk, T, Hk, D, type);
+  if (e) return e == 1 ? -13 : -14;
+  if (Hq > 0 && Q == Yq && ldq != ldyq && T > 0) return -8;
+  if (Hk > 0 && K == Yk && ldk != ldyk && T > 0) return -14;
+  if (misaligned(Wq, type_size(type))) return -9;
+  if (misaligned(Wk, type_size(type))) return -15;
+  if (bad_eps(eps)) return -16;
+  if (R < 0 || R > D || R % 2 != 0) return -17;
+  if (style != FP32GEMM_ROPE_HALVES && style != FP32GEMM_ROPE_PAIRS) return -18;
+  if (T == 0 || Hq + Hk == 0) return 0;
+  if (R > 0 && (freq == nullptr || misaligned(freq, 8))) return -19;
+  if (R > 0 && (pos == nullptr || misaligned(pos, 4))) return -20;
+  KvRowArgs a = {};
+  a.T = T, a.D = D, a.Hq = Hq, a.Hk = Hk, a.Hv = 0;
+  a.Q = Q, a.K = K, a.V = nullptr, a.ldq = ldq, a.ldk = ldk, a.ldv = 0;
+  a.Yq = Yq, a.Yk = Yk, a.ldyq = ldyq, a.ldyk = ldyk;
+  a.Wq = Hq > 0 ? Wq : nullptr, a.Wk = Hk > 0 ? Wk : nullptr, a.eps = eps;
+  a.R = R, a.style = style, a.freq = freq, a.pos = pos, a.slots = nullptr;
+  a.cache.type = -1;
+  return (int)launch_kv_rows(a, type, reinterpret_cast<hipStream_t>(stream));
+}
+
+int kv_write(int T, int type, const void *K, int ldk, const void *V, int ldv, const int *slots,
+             const fp32gemm_kv_cache *cache, fp32gemm_stream_t stream) {
+  if (T < 0) return -1;
+  if (!known_type(type)) return -2;
+  KvRowArgs a = {};
+  if (!unpack_cache(cache, &a.cache) || (a.cache.type != kTypeS8 && a.cache.type != type)) return -8;
+  int e = bad_heads(K, ldk, T, a.cache.heads, a.cache.dim, type);
+  if (e) return e == 1 ? -3 : -4;
+  e = bad_heads(V, ldv, T, a.cache.heads, a.cache.dim, type);
+  if (e) return e == 1 ? -5 : -6;
+  if (T > 0 && (slots == nullptr || misaligned(slots, 4))) return -7;
+  if (T == 0) return 0;
+  a.T = T, a.D = a.cache.dim, a.Hk = a.Hv = a.cache.heads;
+  a.K = K, a.V = V, a.ldk = ldk, a.ldv = ldv;
+  a.style = FP32GEMM_ROPE_HALVES, a.slots = slots;
+  return (int)launch_kv_rows(a, type, reinterpret_cast<hipStream_t>(stream));
+}
+
+int qkv_rope_write(int T, int type, int Hq, const void *Q, int ldq, void *Yq, int ldyq, const void *Wq,
+                   const void *K, int ldk, const void *Wk, const void *V, int ldv, float eps, int R,
+                   int style, const double *freq, const int *pos, const int *slots,
+                   const fp32gemm_kv_cache *cache, fp32gemm_stream_t stream) {
+  if (T < 0) return -1;
+  if (!known_type(type)) return -2;
+  if (Hq < 0) return -3;
+  KvRowArgs a = {};
+  if (!unpack_cache(cache, &a.cache) || (a.cache.type != kTypeS8 && a.cache.type != type)) return -20;
+  const int D = a.cache.dim, Hk = a.cache.heads;
+  int e = bad_heads(Q, ldq, T, Hq, D, type);
+  if (e) return e == 1 ? -4 : -5;
+  e = bad_heads(Yq, ldyq, T, Hq, D, type);
+  if (e) return e == 1 ? -6 : -7;
+  if (Hq > 0 && Q == Yq && ldq != ldyq && T > 0) return -7;
+  e = bad_heads(K, ldk, T, Hk, D, type);
+  if (e) return e == 1 ? -9 : -10;
+  e = bad_heads(V, ldv, T, Hk, D, type);
+  if (e) return e == 1 ? -12 : -13;
+  if (misaligned(Wq, type_size(type))) return -8;
+  if (misaligned(Wk, type_size(type))) return -11;
+  if (bad_eps(eps)) return -14;
+  if (R < 0 || R > D || R % 2 != 0) return -15;
+  if (style != FP32GEMM_ROPE_HALVES && style != FP32GEMM_ROPE_PAIRS) return -16;
+  if (T == 0) return 0;
+  if (R > 0 && (freq == nullptr || misaligned(freq, 8))) return -17;
+  if (R > 0 && (pos == nullptr || misaligned(pos, 4))) return -18;
+  if (slots == nullptr || misaligned(slots, 4)) return -19;
+  a.T = T, a.D = D, a.Hq = Hq, a.Hk = a.Hv = Hk;
+  a.Q = Q, a.K = K, a.V = V, a.ldq = ldq, a.ldk = ldk, a.ldv = ldv;
+  a.Yq = Yq, a.ldyq = ldyq;
+  a.Wq = Hq > 0 ? Wq : nullptr, a.Wk = Wk, a.eps = eps;
+  a.R = R, a.style = style, a.freq = freq, a.pos = pos, a.slots = slots;
+  return (int)launch_kv_rows(a, type, reinterpret_cast<hipStream_t>(stream));
+}
+
+int kv_read(int T, const int *slots, const fp32gemm_kv_cache *cache, int type, void *K, int ldk, void *V,
+            int ldv, fp32gemm_stream_t stream) {
+  if (T < 0) return -1;
+  KvReadArgs a = {};
+  if (!known_type(type)) return -4;
+  if (!unpack_cache(cache, &a.cache) || (a.cache.type != kTypeS8 && a.cache.type != type)) return -3;
+  if (T > 0 && (slots == nullptr || misaligned(slots, 4))) return -2;
+  int e = bad_heads(K, ldk, T, a.cache.heads, a.cache.dim, type);
+  if (e) return e == 1 ? -5 : -6;
+  e = bad_heads(V, ldv, T, a.cache.heads, a.cache.dim, type);
+  if (e) return e == 1 ? -7 : -8;
+  if (T == 0) return 0;
+  a.T = T, a.slots = slots, a.K = K, a.V = V, a.ldk = ldk, a.ldv = ldv;
+  return (int)launch_kv_read(a, type, reinterpret_cast<hipStream_t>(stream));
+}
+
+size_t kv_attention_workspace_size(int B, int Hq, const fp32gemm_kv_cache *cache) {
+  KvCache c;
+  if (B < 0 || !unpack_cache(cache, &c) || Hq < 1 || Hq % c.heads != 0) return 0;
+  return attend_workspace(Hq, c);
+}
+
+int kv_attention(int B, int type, int Hq, const void *Q, int ldq, const fp32gemm_kv_cache *cache,
+                 const int *table, int ldt, const int *lengths, int window, float scale, void *O, int ldo,
+                 float *lse, void *workspace, size_t workspace_bytes, fp32gemm_stream_t stream) {
+  if (B < 0) return -1;
+  if (!known_type(type)) return -2;
+  AttendArgs a = {};
+  if (!unpack_cache(cache, &a.cache) || (a.cache.type != kTypeS8 && a.cache.type != type)) return -6;
+  const KvCache &c = a.cache;
+  if (Hq < 1 || Hq % c.heads != 0) return -3;
+  int e = bad_heads(Q, ldq, B, Hq, c.dim, type);
+  if (e) return e == 1 ? -4 : -5;
+  if (B > 0 && ldt > 0 && (table == nullptr || misaligned(table, 4))) return -7;
+  if (ldt < 0 || (long long)ldt * c.page_size > 1 << 30) return -8;
+  const int G = Hq / c.heads, RG = (G + 15) / 16;
+  const int tokens = c.pages > 0 ? ldt * c.page_size : 0;
+  // more than any sequence can need: its tokens start up to 63 into a step
+  const double units = (double)B * c.heads * RG * (tokens / attend_step(c.type) + 2);
+  if (units >= 2147483647.0) return -8;
+  if (B > 0 && (lengths == nullptr || misaligned(lengths, 4))) return -9;
+  if (window < 0) return -10;
+  if (!(scale >= -0x1p127f && scale <= 0x1p127f)) return -11;
+  e = bad_heads(O, ldo, B, Hq, c.dim, type);
+  if (e) return e == 1 ? -12 : -13;
+  if (misaligned(lse, 4)) return -14;
+  if (B > 0 && (workspace == nullptr || misaligned(workspace, 16))) return -15;
+  if (B > 0 && workspace_bytes < attend_workspace(Hq, c)) return -16;
+  if (B == 0) return 0;
+  a.B = B, a.Hq = Hq, a.Hk = c.heads, a.G = G, a.RG = RG;
+  a.Q = Q, a.ldq = ldq, a.table = table, a.lengths = lengths, a.window = window;
+  a.ldt = c.pages > 0 ? ldt : 0;  // a cache without pages has no tokens
+  a.scale2 = (float)((double)scale * 1.4426950408889634);
+  a.O = O, a.ldo = ldo, a.lse = lse;
+  a.cnt = static_cast<unsigned *>(workspace);
+  a.part = reinterpret_cast<float *>(a.cnt + kAttendGroups);
+  a.groups = units < kAttendGroups ? (int)units : kAttendGroups;
+  // t / page_size for t < 2^31: with 2^(k-1) < page_size <= 2^k, magic =
+  // ceil(2^(31+k) / page_size) is below 2^32 and off by less than 2^k / page_size
+  int k = 0;
+  while ((1LL << k) < c.page_size) ++k;
+  a.magic = (uint32_t)(((1ULL << (31 + k)) + c.page_size - 1) / c.page_size);
+  a.shift = 31 + k;
+  const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  return (int)(c.type == kTypeS8 ? launch_attend_s8(a, type, s) : launch_attend_float(a, type, s));
 }
 
 const char *fp32gemm_strerror(int code) {

@@ -133,35 +133,6 @@ __device__ __forceinline__ void chunk_values(const Raw<T> &c, bool residual, T *
   }
 }
 
-// 1 / step, and NaN where the codes have to go the long way.
-__device__ __forceinline__ float quick_inv(float scale) {
-  const RowStep r = row_step(scale);
-  return r.lift == 1.0f && r.step > 0.0f ? r.inv : __builtin_nanf("");
-}
-
-// Four codes in a word.  Adding 1.5 2^23 leaves round(v inv), to even, in the
-// low bits, and its low byte is the code; v inv is within 8e-6 of v / step, so
-// only values that near to a half are done again by the residual (row_code),
-// as are the rows that are lifted or have no codes, for which inv is NaN.
-__device__ __forceinline__ uint32_t code_word(const float (&v)[4], float inv, float scale) {
-  constexpr float kMagic = 12582912.0f;
-  uint32_t u[4];
-  float off[4];
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const float f = __builtin_fmaf(v[e], inv, kMagic);
-    u[e] = __builtin_bit_cast(uint32_t, f);
-    off[e] = __builtin_fabsf(__builtin_fmaf(v[e], inv, kMagic - f));
-  }
-  const float far = __builtin_fmaxf(__builtin_fmaxf(off[0], off[1]), __builtin_fmaxf(off[2], off[3]));
-  if (!(far < 0.49999f)) {
-    const RowStep rs = row_step(scale);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) u[e] = (uint32_t)row_code(v[e], rs);
-  }
-  return __builtin_amdgcn_perm(u[1], u[0], 0x0c0c0400u) | __builtin_amdgcn_perm(u[3], u[2], 0x04000c0cu);
-}
-
 // Codes of one chunk of a row with this scale.
 template <bool WHOLE>
 __device__ __forceinline__ void chunk_codes(int8_t *qrow, int k, int K, const float (&v)[E], float inv,

@@ -1,5 +1,6 @@
 /*
- * fp32gemm — single-precision GEMM and small-M GEMV for AMD MI355X (gfx950).
+ * fp32gemm — single-precision GEMM and small-M GEMV for AMD MI355X (gfx950),
+ * an 8-bit linear layer, and decode attention over a paged cache.
  *
  * C ABI of libfp32gemm.so.  Plain pointers and sizes only; no HIP or torch
  * header is needed to call it (the stream is an opaque pointer that is
@@ -20,7 +21,7 @@
  *    owned by the caller.  The library keeps no reference after the call's
  *    kernels finish.  C must not overlap A or B.
  *  - Arithmetic: fp32 throughout (fp32 MFMA or fp32 FMA); no conversion to a
- *    narrower format (the s8 routines below say what theirs is).  The order
+ *    narrower format (the s8 and kv routines below say what theirs is).  The order
  *    of the k-sum is unspecified, so results may differ from a sequential
  *    loop by rounding.  Repeated calls with the same arguments and
  *    configuration give bit-identical results (no atomics on floats).
@@ -371,6 +372,149 @@ int s8gemm(int M, int N, int K, const signed char *A, int lda,
            const float *scaleA, const signed char *B, int ldb,
            const float *scaleB, float beta, int type, void *C, int ldc,
            const float *bias, int act, fp32gemm_stream_t stream);
+
+/*
+ * Between a decode step's projections: the norms and the position rotation of
+ * query and key heads, a paged cache of keys and values, and attention of each
+ * sequence's new token over it.
+ *
+ * Heads.  Row t of a matrix of heads holds token t's heads one behind the
+ * other: element (t, h, d) is X[t * ldx + h * dim + d], so that the queries,
+ * keys and values of a projection's output are three pointers into it with one
+ * leading dimension.  A head has `dim` values, a multiple of 16 up to 256.
+ * Floats are fp32, fp16 or bf16, one type in a call, at any address aligned to
+ * their type; leading dimensions are at most 2^20.
+ *
+ * The cache.  K and V are pages x heads x page_size x dim, packed and 16-byte
+ * aligned, owned by the caller.  Token offsets of one head lie behind each
+ * other, so a page of a head is one run of memory.  Its type is that of the
+ * call's floats, or FP32GEMM_TYPE_S8: codes as s8_quantize makes them, with a
+ * scale for each row of dim values (scaleK, scaleV: pages x heads x page_size).
+ * Scales are not looked at for other types.  Pages of a multiple of 16 tokens
+ * are read faster than others.  pages heads page_size < 2^31.  A token's slot
+ * is page * page_size + offset.
+ *
+ * The conventions at the top of this file hold: asynchronous, no allocation,
+ * bit-identical from call to call, argument p invalid = -p and nothing
+ * enqueued; a bad field of the cache counts as the cache argument.  The struct
+ * is read during the call only.
+ */
+#define FP32GEMM_TYPE_S8 3
+typedef struct {
+  int type, pages, page_size, heads, dim;
+  void *K, *V;
+  float *scaleK, *scaleV;
+} fp32gemm_kv_cache;
+
+/*
+ * Norm of each head of Q (T x Hq x D) and K (T x Hk x D), and the rotation by
+ * its token's position, in one pass:
+ *
+ *   n_d = x_d / sqrt(sum_d x_d^2 / D + eps) * W[d]     (n = x where W is NULL)
+ *   a', b' = a cos - b sin, b cos + a sin              of pos[t] * freq[i]
+ *
+ * for the R / 2 pairs (a, b) = (n_i, n_{i + R/2}) (FP32GEMM_ROPE_HALVES) or
+ * (n_{2i}, n_{2i+1}) (FP32GEMM_ROPE_PAIRS); values from R on keep n.  0 <= R <=
+ * D, even; with R == 0 freq and pos are not read.  freq holds R / 2 doubles
+ * (pos freq up to 2^50 in magnitude).  Computed in 64 bits, rounded to fp32 and
+ * from there to the type.  Yq may be Q itself and Yk K itself (the same address
+ * and leading dimension); outputs must not overlap inputs otherwise.  Hq or Hk
+ * may be 0.  Argument positions for error codes: T 1, D 2, type 3, Hq 4, Q 5,
+ * ldq 6, Yq 7, ldyq 8, Wq 9, Hk 10, K 11, ldk 12, Yk 13, ldyk 14, Wk 15,
+ * eps 16 (negative or not finite), R 17, style 18, freq 19, pos 20, stream 21.
+ */
+#define FP32GEMM_ROPE_HALVES 0
+#define FP32GEMM_ROPE_PAIRS 1
+int qk_norm_rope(int T, int D, int type, int Hq, const void *Q, int ldq,
+                 void *Yq, int ldyq, const void *Wq, int Hk, const void *K,
+                 int ldk, void *Yk, int ldyk, const void *Wk, float eps, int R,
+                 int style, const double *freq, const int *pos,
+                 fp32gemm_stream_t stream);
+
+/*
+ * The cache's rows of T tokens: K and V (T x heads x dim) go to slots[t].  A
+ * slot outside 0 .. pages page_size - 1 is skipped; those inside must differ
+ * from each other.  Codes and scales are those of s8_quantize for the row.  A
+ * row with an infinity or a NaN gets the scale NaN and codes 0.  Argument
+ * positions for error codes: T 1, type 2, K 3, ldk 4, V 5, ldv 6, slots 7,
+ * cache 8, stream 9.
+ */
+int kv_write(int T, int type, const void *K, int ldk, const void *V, int ldv,
+             const int *slots, const fp32gemm_kv_cache *cache,
+             fp32gemm_stream_t stream);
+
+/*
+ * qk_norm_rope with the keys and, as they are, the values going to the cache as
+ * in kv_write, in one pass.  A cache of codes holds those of the key rounded to
+ * fp32, not to the type.  A token whose slot is outside the cache still has its
+ * queries written.  Argument positions for error codes: T 1, type 2, Hq 3, Q 4,
+ * ldq 5, Yq 6, ldyq 7, Wq 8, K 9, ldk 10, Wk 11, V 12, ldv 13, eps 14, R 15,
+ * style 16, freq 17, pos 18, slots 19, cache 20, stream 21.
+ */
+int qkv_rope_write(int T, int type, int Hq, const void *Q, int ldq, void *Yq,
+                   int ldyq, const void *Wq, const void *K, int ldk,
+                   const void *Wk, const void *V, int ldv, float eps, int R,
+                   int style, const double *freq, const int *pos,
+                   const int *slots, const fp32gemm_kv_cache *cache,
+                   fp32gemm_stream_t stream);
+
+/*
+ * The cache's rows at T slots as floats, K and V T x heads x dim of `type` (a
+ * cache of codes in any of the float types: code * scale, rounded once to fp32
+ * and from there to the type).  Rows of slots outside the cache are left as
+ * they were; a slot may come more than once.  Argument positions for error
+ * codes: T 1, slots 2, cache 3, type 4, K 5, ldk 6, V 7, ldv 8, stream 9.
+ */
+int kv_read(int T, const int *slots, const fp32gemm_kv_cache *cache, int type,
+            void *K, int ldk, void *V, int ldv, fp32gemm_stream_t stream);
+
+/*
+ * Attention of one token for each of B sequences.  Query head h of sequence b
+ * (Q is B x Hq x dim, Hq a multiple of the cache's heads) sees key head
+ * h / (Hq / heads) of the tokens
+ *
+ *   max(0, n - window) <= t < n,  n = lengths[b]       (window 0: all t < n)
+ *
+ * which lie at offset t % page_size of page table[b * ldt + t / page_size]:
+ *
+ *   s_t = scale q . k_t,  O = sum_t exp(s_t) v_t / sum_t exp(s_t),
+ *   lse = log sum_t exp(s_t)      (B x Hq fp32, packed; NULL: not wanted)
+ *
+ * O is B x Hq x dim of `type`.  Lengths below 0 count as 0, above ldt page_size
+ * as that.  A table entry outside 0 .. pages - 1 is a page without tokens (one
+ * that the window has left, or that was given up); entries of pages that no
+ * seen token lies on are not looked at.  Where no token is left, or every score
+ * is minus infinity, O is 0 and lse minus infinity.  Values of unseen tokens,
+ * whatever they are, have no effect; a NaN or an infinity in the query, or in a
+ * key's scale, or in a seen token's values shows in the outputs that depend on
+ * it.  Sums are fp32; with codes the products are exact in integers of the
+ * query's row and the weights rounded to 23 bits (fp32) or 15 bits (fp16, bf16)
+ * of their largest; values below 2^-100 lose digits there.
+ *
+ * The lengths and the table are read on the GPU when the call runs, and work is
+ * spread by them; a captured call follows later lengths.  Results depend on the
+ * lengths and shapes of the whole call, not on timing.
+ *
+ * workspace: device memory of the caller, at least
+ * kv_attention_workspace_size(B, Hq, cache) bytes, 16-byte aligned, which must
+ * hold zeros before its first use; every call leaves its first 2048 bytes zero.
+ * It must not be used by another call, nor by two graphs' replays at once,
+ * until this one has completed.
+ *
+ * ldt page_size <= 2^30, and B times the key heads times the table's length in
+ * steps of 64 to 256 tokens < 2^31 (ldt is at fault otherwise).  Argument
+ * positions for error codes: B 1, type 2, Hq 3, Q 4, ldq 5, cache 6, table 7,
+ * ldt 8, lengths 9, window 10, scale 11 (NaN, or past 2^127), O 12, ldo 13, lse 14,
+ * workspace 15, workspace_bytes 16, stream 17.
+ */
+int kv_attention(int B, int type, int Hq, const void *Q, int ldq,
+                 const fp32gemm_kv_cache *cache, const int *table, int ldt,
+                 const int *lengths, int window, float scale, void *O, int ldo,
+                 float *lse, void *workspace, size_t workspace_bytes,
+                 fp32gemm_stream_t stream);
+
+/* Workspace bytes kv_attention needs; 0 for arguments it would refuse. */
+size_t kv_attention_workspace_size(int B, int Hq, const fp32gemm_kv_cache *cache);
 
 /* Human-readable text for a return code (static storage, never NULL). */
 const char *fp32gemm_strerror(int code);

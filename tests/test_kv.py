@@ -1,0 +1,580 @@
+"""Head norms with rotation, the paged cache and attention over it: the C entry points against the
+64-bit reference, and what they refuse."""
+import ctypes
+
+import pytest
+import torch
+
+import fp32_gemm_06_amd as fg
+import kv_reference as ref
+import s8_reference
+from gpu_util import require_gpu
+
+gpu = pytest.mark.gpu
+TYPES = list(ref.TYPES.values())
+TYPE_OF = {d: t for t, d in ref.TYPES.items()}
+FREQ = lambda n: 10000.0 ** (-torch.arange(n, dtype=torch.float64) / max(1, n))  # noqa: E731
+
+
+# ---- refusals, on the CPU ---------------------------------------------------------
+def cache_struct(**kw):
+    d = dict(type=fg.TYPE_S8, pages=4, page_size=16, heads=2, dim=64, K=256, V=256, scaleK=256, scaleV=256)
+    d.update(kw)
+    return fg.fp32gemm_kv_cache(*(d[n] for n, _ in fg.fp32gemm_kv_cache._fields_))
+
+
+def call(fn, names, values, kw):
+    a = dict(zip(names, values))
+    assert not set(kw) - set(a), kw
+    a.update(kw)
+    return fn(*(a[n] for n in names), stream=0)
+
+
+NORM = ("T D type Hq Q ldq Yq ldyq Wq Hk K ldk Yk ldyk Wk eps R style freq pos".split(),
+        [3, 64, 0, 4, 256, 512, 1024, 256, 256, 2, 256, 512, 1024, 128, 256, 1e-6, 64, 0, 256, 256])
+WRITE_ROPE = ("T type Hq Q ldq Yq ldyq Wq K ldk Wk V ldv eps R style freq pos slots cache".split(),
+              [3, 0, 4, 256, 512, 1024, 256, 256, 256, 512, 256, 256, 512, 1e-6, 64, 0, 256, 256, 256, None])
+WRITE = ("T type K ldk V ldv slots cache".split(), [3, 0, 256, 128, 256, 128, 256, None])
+READ = ("T slots cache type K ldk V ldv".split(), [3, 256, None, 0, 256, 128, 256, 128])
+ATTEND = ("B type Hq Q ldq cache table ldt lengths window scale O ldo lse workspace workspace_bytes".split(),
+          [3, 0, 4, 256, 256, None, 256, 2, 256, 0, 0.125, 256, 256, 256, 256, 1 << 30])
+
+
+def refused(fn, spec, kw, code):
+    names, values = spec
+    values = list(values)
+    if "cache" in names:
+        values[names.index("cache")] = cache_struct()
+    assert call(fn, names, values, kw) == code, kw
+
+
+NAN, INF = float("nan"), float("inf")
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(T=-1), -1), (dict(D=0), -2), (dict(D=24), -2), (dict(D=272), -2), (dict(type=3), -3), (dict(type=-1), -3),
+    (dict(Hq=-1), -4), (dict(Q=0), -5), (dict(Q=258), -5), (dict(Q=257, type=1), -5), (dict(ldq=255), -6),
+    (dict(ldq=(1 << 20) + 1), -6), (dict(Yq=0), -7), (dict(Yq=1026), -7), (dict(ldyq=255), -8),
+    (dict(Yq=256), -8), (dict(Wq=258), -9), (dict(Hk=-1), -10), (dict(K=0), -11), (dict(ldk=127), -12),
+    (dict(Yk=0), -13), (dict(ldyk=127), -14), (dict(Yk=256), -14), (dict(Wk=257), -15), (dict(eps=-1.0), -16),
+    (dict(eps=NAN), -16), (dict(eps=INF), -16), (dict(R=-2), -17), (dict(R=66), -17), (dict(R=7), -17),
+    (dict(style=2), -18), (dict(freq=0), -19), (dict(freq=260), -19), (dict(pos=0), -20), (dict(pos=258), -20)])
+def test_norm_rope_refuses(kw, code):
+    refused(fg.qk_norm_rope, NORM, kw, code)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(T=-1), -1), (dict(type=3), -2), (dict(Hq=-1), -3), (dict(Q=0), -4), (dict(ldq=255), -5), (dict(Yq=0), -6),
+    (dict(ldyq=255), -7), (dict(Yq=256), -7), (dict(Wq=258), -8), (dict(K=0), -9), (dict(ldk=127), -10),
+    (dict(Wk=258), -11), (dict(V=0), -12), (dict(ldv=127), -13), (dict(eps=-1.0), -14), (dict(R=65), -15),
+    (dict(R=66), -15), (dict(style=-1), -16), (dict(freq=0), -17), (dict(pos=0), -18), (dict(slots=0), -19),
+    (dict(slots=258), -19), (dict(cache=None), -20), (dict(cache=cache_struct(type=1)), -20)])
+def test_rope_write_refuses(kw, code):
+    refused(fg.qkv_rope_write, WRITE_ROPE, kw, code)
+
+
+BAD_CACHES = [dict(type=4), dict(type=-1), dict(pages=-1), dict(page_size=0), dict(heads=0), dict(dim=0), dict(dim=40),
+              dict(dim=272), dict(pages=1 << 20, page_size=1 << 12), dict(pages=1 << 16, page_size=1 << 10, heads=32),
+              dict(K=0), dict(V=0), dict(K=264), dict(V=264), dict(scaleK=0), dict(scaleV=0), dict(scaleK=258),
+              dict(scaleV=258)]
+
+
+@pytest.mark.parametrize("bad", BAD_CACHES, ids=str)
+def test_a_bad_cache_is_refused(bad):
+    c = cache_struct(**bad)
+    refused(fg.kv_write, WRITE, dict(cache=c), -8)
+    refused(fg.kv_read, READ, dict(cache=c), -3)
+    refused(fg.kv_attention, ATTEND, dict(cache=c), -6)
+    refused(fg.qkv_rope_write, WRITE_ROPE, dict(cache=c), -20)
+    assert fg.kv_attention_workspace_size(1, 32, c) == 0
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(T=-1), -1), (dict(type=5), -2), (dict(K=0), -3), (dict(K=258), -3), (dict(ldk=127), -4), (dict(V=0), -5),
+    (dict(ldv=127), -6), (dict(slots=0), -7), (dict(slots=257), -7), (dict(cache=cache_struct(type=2)), -8)])
+def test_write_refuses(kw, code):
+    refused(fg.kv_write, WRITE, kw, code)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(T=-1), -1), (dict(slots=0), -2), (dict(cache=cache_struct(type=2)), -3), (dict(type=3), -4), (dict(K=0), -5),
+    (dict(ldk=127), -6), (dict(V=0), -7), (dict(V=257), -7), (dict(ldv=127), -8)])
+def test_read_refuses(kw, code):
+    refused(fg.kv_read, READ, kw, code)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(B=-1), -1), (dict(type=3), -2), (dict(Hq=0), -3), (dict(Hq=3), -3), (dict(Q=0), -4), (dict(Q=258), -4),
+    (dict(ldq=255), -5), (dict(cache=cache_struct(type=1)), -6), (dict(table=0), -7), (dict(table=258), -7),
+    (dict(ldt=-1), -8), (dict(ldt=(1 << 26) + 1), -8), (dict(ldt=1 << 26, B=1 << 12), -8), (dict(lengths=0), -9),
+    (dict(window=-1), -10), (dict(scale=NAN), -11), (dict(scale=INF), -11), (dict(scale=-3e38), -11), (dict(O=0), -12),
+    (dict(ldo=255), -13), (dict(lse=258), -14), (dict(workspace=0), -15), (dict(workspace=264), -15),
+    (dict(workspace_bytes=4096), -16)])
+def test_attention_refuses(kw, code):
+    refused(fg.kv_attention, ATTEND, kw, code)
+
+
+def test_calls_of_nothing_need_no_gpu():
+    c = cache_struct()
+    refused(fg.qk_norm_rope, NORM, dict(T=0, Q=0, K=0, Yq=0, Yk=0, freq=0, pos=0), 0)
+    refused(fg.qk_norm_rope, NORM, dict(Hq=0, Hk=0, Q=0, ldq=0), 0)
+    refused(fg.qkv_rope_write, WRITE_ROPE, dict(T=0, slots=0), 0)
+    refused(fg.kv_write, WRITE, dict(T=0, slots=0), 0)
+    refused(fg.kv_read, READ, dict(T=0, slots=0), 0)
+    refused(fg.kv_attention, ATTEND, dict(B=0, table=0, lengths=0, workspace=0), 0)
+    assert fg.kv_attention_workspace_size(1, 3, c) == 0 and fg.kv_attention_workspace_size(-1, 4, c) == 0
+    assert fg.kv_attention_workspace_size(7, 4, c) > 2048
+    assert ctypes.sizeof(c) == 56
+
+
+# ---- norm and rotation ------------------------------------------------------------
+@gpu
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+@pytest.mark.parametrize("T,Hq,Hk,D,R,pairs,norm", [
+    (1, 1, 1, 16, 16, False, True), (1, 32, 8, 128, 128, False, True), (5, 3, 1, 64, 64, True, True),
+    (33, 5, 2, 80, 32, True, True), (17, 4, 4, 80, 20, False, True), (9, 7, 0, 96, 24, False, True),
+    (6, 0, 3, 192, 100, False, True), (40, 2, 1, 256, 256, False, True), (3, 2, 2, 256, 66, False, False),
+    (130, 1, 1, 128, 126, False, True), (4, 6, 2, 112, 2, False, True), (4, 6, 2, 48, 14, True, False),
+    (12, 2, 2, 32, 0, False, True), (300, 40, 8, 64, 64, False, True), (2, 1, 0, 128, 6, True, True)])
+def test_norm_rope(T, Hq, Hk, D, R, pairs, norm, dtype):
+    require_gpu()
+    g = torch.Generator().manual_seed(T + D)
+    x = torch.randn(T, (Hq + 2 * Hk) * D + 3, generator=g)
+    x[:, ::13] *= 20.0
+    x = x.to(dtype)
+    w = [(1 + 0.3 * torch.randn(D, generator=g)).to(dtype) if norm else None for _ in range(2)]
+    pos = torch.randint(0, 2 ** 20, (T,), generator=g).int()
+    pos[0] = -7
+    freq = FREQ(R // 2) if R else None
+    dx, dw, dpos = x.cuda(), [None if v is None else v.cuda() for v in w], pos.cuda()
+    dfreq = None if freq is None else freq.cuda()
+    ld = x.shape[1]
+    yq = torch.full((T, Hq * D + 5), 7.0, dtype=dtype, device="cuda")
+    yk = torch.full((T, Hk * D + 2), 7.0, dtype=dtype, device="cuda")
+    es = x.element_size()
+    rc = fg.qk_norm_rope(T, D, TYPE_OF[dtype], Hq, dx.data_ptr(), ld, yq, yq.shape[1], dw[0], Hk,
+                         dx.data_ptr() + Hq * D * es, ld, yk, yk.shape[1], dw[1], 1e-6, R,
+                         fg.ROPE_PAIRS if pairs else fg.ROPE_HALVES, dfreq, dpos)
+    assert rc == 0, fg.strerror(rc)
+    for y, H, at, weight in ((yq, Hq, 0, w[0]), (yk, Hk, Hq * D, w[1])):
+        want, bound, _ = ref.norm_rope(x[:, at:at + H * D].reshape(T, H, D), weight, 1e-6, pos, freq, pairs)
+        got = y.cpu()
+        assert bool((got[:, H * D:] == 7.0).all())
+        assert bool(((got[:, :H * D].reshape(T, H, D).double() - want).abs() <= bound).all())
+    # in place, the same bits
+    rc = fg.qk_norm_rope(T, D, TYPE_OF[dtype], Hq, dx.data_ptr(), ld, dx.data_ptr(), ld, dw[0], Hk,
+                         dx.data_ptr() + Hq * D * es, ld, dx.data_ptr() + Hq * D * es, ld, dw[1], 1e-6, R,
+                         fg.ROPE_PAIRS if pairs else fg.ROPE_HALVES, dfreq, dpos)
+    assert rc == 0
+    assert torch.equal(dx[:, :Hq * D], yq[:, :Hq * D]) and torch.equal(dx[:, Hq * D:(Hq + Hk) * D], yk[:, :Hk * D])
+    assert torch.equal(dx[:, (Hq + Hk) * D:].cpu(), x[:, (Hq + Hk) * D:])
+
+
+@gpu
+def test_far_positions_and_large_angles():
+    """Angles up to 2^50: the reduction by parts of pi / 2 against the host's."""
+    require_gpu()
+    T, D = 64, 32
+    freq = torch.tensor([0.0, 1.0, 0.5, 3.14159, 1e-9, 1234.567, 2.0 ** 19, 1e-300, -1.0, 7.0, 100.0, 1e4, 2.0 ** -30,
+                         1.5707963267948966, 0.7853981633974483, 6.283185307179586], dtype=torch.float64)
+    pos = torch.tensor([0, 1, 2, 3, -1, 2 ** 31 - 1, -2 ** 31, 10 ** 6, 10 ** 9] + list(range(100, 100 + T - 9))).int()
+    x = torch.randn(T, 1, D, generator=torch.Generator().manual_seed(0))
+    y, _ = fg.norm_rope(x.cuda(), None, pos.cuda(), freq.cuda())
+    want, bound, _ = ref.norm_rope(x, None, 0.0, pos, freq, False)
+    assert bool(((y.cpu().double() - want).abs() <= bound).all())
+
+
+@gpu
+def test_values_that_are_not_finite_stay_in_their_pair_or_row():
+    require_gpu()
+    x = torch.randn(4, 3, 64, generator=torch.Generator().manual_seed(1))
+    x[1, 1, 5], x[2, 0, 40], x[3, 2, 63] = NAN, INF, -INF   # pair (5, 21), beyond R, beyond R
+    pos, freq = torch.arange(4).int().cuda(), FREQ(16).cuda()
+    for pairs in (False, True):
+        y, _ = fg.norm_rope(x.cuda(), None, pos, freq, style="pairs" if pairs else "halves")
+        y = y.cpu()
+        bad = ~torch.isfinite(y)
+        assert bad[1, 1, 5] and bad[1, 1, 4 if pairs else 21] and bad.sum() == 4
+        assert y[2, 0, 40] == INF and y[3, 2, 63] == -INF
+    y, _ = fg.norm_rope(x.cuda(), None, pos, freq, q_weight=torch.ones(64).cuda())
+    rows = torch.isnan(y.cpu()).any(-1)
+    assert rows.sum() == 3 and rows[1, 1] and rows[2, 0] and rows[3, 2]
+
+
+# ---- the cache --------------------------------------------------------------------
+def make_cache(pages, heads, ps, D, dtype, fill=None):
+    cache = fg.KVCache.empty(pages, ps, heads, D, dtype)
+    if fill is not None:
+        for t in cache._tensors():
+            if t is not None:
+                t.fill_(fill)
+    return cache
+
+
+@gpu
+@pytest.mark.parametrize("dtype,kind", [(d, k) for d in TYPES for k in (torch.int8, d)], ids=str)
+@pytest.mark.parametrize("T,Hk,D,ps", [(1, 1, 16, 1), (7, 3, 64, 16), (65, 2, 80, 24), (200, 8, 128, 64), (9, 1, 256, 5),
+                                       (33, 5, 192, 7)])
+def test_write_and_read(T, Hk, D, ps, dtype, kind):
+    """Every slot written holds its row's codes and scale, or its values; no other byte changes; what is read is
+    what stands there."""
+    require_gpu()
+    g = torch.Generator().manual_seed(T * D)
+    pages = -(-T // ps) + 2
+    cache = make_cache(pages, Hk, ps, D, kind, 77)
+    x = torch.randn(T, 2 * Hk * D + 1, generator=g).to(dtype)
+    x[0, :D] = 0.0
+    slots = torch.randperm(pages * ps, generator=g)[:T].int()
+    skip = T > 3
+    if skip:
+        slots[1], slots[2], slots[3] = -1, pages * ps, 2 ** 31 - 1
+    dx, ds = x.cuda(), slots.cuda()
+    rc = fg.kv_write(T, TYPE_OF[dtype], dx.data_ptr(), x.shape[1], dx.data_ptr() + Hk * D * x.element_size(), x.shape[1],
+                     ds, cache)
+    assert rc == 0, fg.strerror(rc)
+    live = [t for t in range(T) if 0 <= int(slots[t]) < pages * ps]
+    want = make_cache(pages, Hk, ps, D, kind, 77)
+    page, at = (slots[live] // ps).long(), (slots[live] % ps).long()
+    for name, off in (("k", 0), ("v", Hk * D)):
+        rows = x[live, off:off + Hk * D].reshape(len(live), Hk, D)
+        if kind == torch.int8:
+            c, s = s8_reference.codes(rows.double().reshape(-1, D))
+            getattr(want, name)[page, :, at] = c.reshape(rows.shape).to(torch.int8).cuda()
+            getattr(want, name + "_scale")[page, :, at] = s.reshape(rows.shape[:2]).cuda()
+        else:
+            getattr(want, name)[page, :, at] = rows.cuda()
+    for a, b in zip(cache._tensors(), want._tensors()):
+        assert a is None or torch.equal(a, b)
+    # read: into wider rows, slots outside leave theirs
+    out = [torch.full((T, Hk * D + 4), 9.0, dtype=dtype, device="cuda") for _ in range(2)]
+    rc = fg.kv_read(T, ds, cache, TYPE_OF[dtype], out[0], Hk * D + 4, out[1], Hk * D + 4)
+    assert rc == 0, fg.strerror(rc)
+    for name, y in zip("kv", out):
+        y = y.cpu()
+        assert bool((y[:, Hk * D:] == 9.0).all())
+        c = getattr(want, name)[page, :, at].cpu()
+        v = c.float() * getattr(want, name + "_scale")[page, :, at].cpu()[..., None] if kind == torch.int8 else c
+        assert torch.equal(y[live, :Hk * D], v.to(dtype).reshape(len(live), -1))
+        if skip:
+            assert bool((y[1:4] == 9.0).all())
+
+
+@gpu
+@pytest.mark.parametrize("dtype,kind", [(d, k) for d in TYPES for k in (torch.int8, d)], ids=str)
+@pytest.mark.parametrize("T,Hq,Hk,D,R,pairs,norm", [(1, 32, 8, 128, 128, False, True), (70, 3, 1, 80, 20, False, True),
+                                                    (9, 0, 2, 64, 32, True, False), (18, 5, 5, 256, 256, False, True),
+                                                    (4, 2, 2, 16, 0, False, True)])
+def test_rope_write(T, Hq, Hk, D, R, pairs, norm, dtype, kind):
+    require_gpu()
+    g = torch.Generator().manual_seed(T + R)
+    ps, pages = 16, T // 16 + 3
+    x = torch.randn(T, Hq + 2 * Hk, D, generator=g).to(dtype)
+    w = [(1 + 0.3 * torch.randn(D, generator=g)).to(dtype).cuda() if norm else None for _ in range(2)]
+    pos, freq = torch.randint(0, 10 ** 6, (T,), generator=g).int(), FREQ(R // 2)
+    slots = torch.randperm(pages * ps, generator=g)[:T].int()
+    cache = make_cache(pages, Hk, ps, D, kind, 77)
+    q, k, v = x.cuda().split([Hq, Hk, Hk], 1)
+    style = "pairs" if pairs else "halves"
+    y = fg.rope_write(cache, q, k, v, slots.cuda(), pos.cuda(), freq.cuda(), *w, style=style)
+    page, at = (slots // ps).long(), (slots % ps).long()
+    hw = [None if t is None else t.cpu() for t in w]
+    want, bound, _ = ref.norm_rope(x[:, :Hq], hw[0], 1e-6, pos, freq, pairs)
+    assert bool(((y.cpu().double() - want).abs() <= bound).all())
+    want, bound, exact = ref.norm_rope(x[:, Hq:Hq + Hk], hw[1], 1e-6, pos, freq, pairs)
+    got = cache.k[page, :, at].cpu()
+    vals = x[:, Hq + Hk:]
+    if kind == torch.int8:
+        assert ref.codes_near(want, exact, got, cache.k_scale[page, :, at].cpu())
+        c, s = s8_reference.codes(vals.double().reshape(-1, D))
+        assert torch.equal(cache.v[page, :, at].cpu().long(), c.reshape(vals.shape))
+        assert torch.equal(cache.v_scale[page, :, at].cpu(), s.reshape(vals.shape[:2]))
+        left = torch.ones(pages, ps, dtype=torch.bool)
+        left[page, at] = False
+        assert bool((cache.k.cpu().permute(0, 2, 1, 3)[left] == 77).all())
+        assert bool((cache.v_scale.cpu().permute(0, 2, 1)[left] == 77).all())
+    else:
+        assert bool(((got.double() - want).abs() <= bound).all())
+        assert torch.equal(cache.v[page, :, at].cpu(), vals)
+    # the queries and keys are those of norm_rope; a key that is written is the one that is returned there
+    yq, yk = fg.norm_rope(q, k, pos.cuda(), freq.cuda(), *w, style=style)
+    assert torch.equal(yq, y)
+    if kind != torch.int8:
+        assert torch.equal(yk, cache.k[page, :, at].to("cuda"))
+
+
+@gpu
+def test_rows_that_are_not_finite_show():
+    require_gpu()
+    cache = make_cache(2, 2, 16, 64, torch.int8)
+    k, v = (torch.randn(3, 2, 64, device="cuda") for _ in range(2))
+    k[1, 0, 3], v[2, 1, 60] = NAN, INF
+    fg.cache_write(cache, k, v, torch.tensor([5, 9, 20], dtype=torch.int32, device="cuda"))
+    assert torch.isnan(cache.k_scale[0, 0, 9]) and bool((cache.k[0, 0, 9] == 0).all())
+    assert torch.isnan(cache.v_scale[1, 1, 4]) and bool((cache.v[1, 1, 4] == 0).all())
+    assert int(torch.isnan(cache.k_scale).sum()) == 1 and int(torch.isnan(cache.v_scale).sum()) == 1
+    a, b = fg.cache_read(cache, torch.tensor([9, 20, 5, 9], dtype=torch.int32, device="cuda"))
+    assert torch.isnan(a[0, 0]).all() and torch.isfinite(a[0, 1]).all() and torch.isnan(b[1, 1]).all()
+    assert torch.equal(torch.isnan(a[3]), torch.isnan(a[0]))
+
+
+# ---- attention --------------------------------------------------------------------
+def fill_cache(g, pages, Hk, ps, D, dtype, kind, spread=1.0):
+    """(k, v, k_scale, v_scale) on the CPU."""
+    if kind != torch.int8:
+        return [(spread * torch.randn(pages, Hk, ps, D, generator=g)).to(kind) for _ in range(2)] + [None, None]
+    kv, scales = [], []
+    for _ in range(2):
+        x = spread * torch.randn(pages, Hk, ps, D, generator=g) * torch.exp(torch.randn(pages, Hk, ps, 1, generator=g))
+        c, s = s8_reference.codes(x.double().reshape(-1, D))
+        kv.append(c.reshape(x.shape).to(torch.int8))
+        scales.append(s.reshape(x.shape[:3]))
+    return kv + scales
+
+
+def attend(q, kv, table, lengths, window=0, scale=None, ldo=0, pad=3):
+    """(o, lse) through the C name, into wider rows whose rest has to stay; the workspace has to be clean after."""
+    k, v, ks, vs = (None if t is None else t.cuda() for t in kv)
+    cache = fg.KVCache(k, v, ks, vs)
+    B, Hq, D = q.shape
+    dq = torch.zeros(B, Hq * D + pad, dtype=q.dtype)
+    dq[:, :Hq * D] = q.reshape(B, -1)
+    dq = dq.cuda()
+    out = torch.full((B, Hq * D + pad), 7.0, dtype=q.dtype, device="cuda")
+    lse = torch.full((B, Hq), 7.0, device="cuda")
+    size = fg.kv_attention_workspace_size(B, Hq, cache)
+    ws = torch.zeros(size, dtype=torch.uint8, device="cuda")
+    scale = D ** -0.5 if scale is None else scale
+    first = None
+    for _ in range(2):
+        out.fill_(7.0)
+        rc = fg.kv_attention(B, TYPE_OF[q.dtype], Hq, dq, Hq * D + pad, cache, table.int().cuda(), table.shape[1],
+                             lengths.int().cuda(), window, scale, out, Hq * D + pad, lse, ws, size)
+        assert rc == 0, fg.strerror(rc)
+        torch.cuda.synchronize()
+        assert int(ws[:2048].sum()) == 0
+        assert bool((out[:, Hq * D:] == 7.0).all())
+        o = (out[:, :Hq * D].reshape(B, Hq, D).cpu(), lse.cpu())
+        if first is not None:
+            assert torch.equal(torch.nan_to_num(first[0]), torch.nan_to_num(o[0]))
+            assert torch.equal(torch.nan_to_num(first[1]), torch.nan_to_num(o[1]))
+        first = o
+    return first
+
+
+def check(q, kv, table, lengths, window=0, scale=None):
+    o, lse = attend(q, kv, table, lengths, window, scale)
+    s = q.shape[2] ** -0.5 if scale is None else scale
+    wo, wl, bo, bl = ref.attention(q, *kv, table, lengths, window, s)
+    assert bool(((o.double() - wo).abs() <= bo).all()), float(((o.double() - wo).abs() / bo.clamp_min(1e-300)).max())
+    empty = torch.isinf(wl)
+    assert torch.equal(torch.isinf(lse), empty) and bool((o[empty] == 0).all())
+    assert bool(((lse.double() - wl).abs() <= bl)[~empty].all())
+
+
+def pages_for(g, lengths, ps, width=None, spare=2):
+    """(table, pages): every sequence's pages lie anywhere; entries behind them are no pages."""
+    need = [-(-max(0, int(n)) // ps) for n in lengths]
+    width = max(need + [1]) if width is None else width
+    pages = sum(need) + spare
+    perm, table, at = torch.randperm(pages, generator=g), torch.full((len(need), width), -5), 0
+    for b, n in enumerate(need):
+        n = min(n, width)
+        table[b, :n] = perm[at:at + n]
+        at += n
+    return table, pages
+
+
+PAIRS = [(d, k) for d in TYPES for k in (torch.int8, d)]
+
+
+@gpu
+@pytest.mark.parametrize("dtype,kind", PAIRS, ids=str)
+@pytest.mark.parametrize("Hk,G,D,ps", [(1, 1, 64, 16), (2, 4, 128, 64), (1, 3, 80, 24), (2, 17, 16, 1), (1, 16, 256, 16),
+                                       (3, 8, 96, 7), (1, 5, 192, 48)])
+def test_attention(Hk, G, D, ps, dtype, kind):
+    """Ragged lengths around the tiles' edges, an empty sequence among them."""
+    require_gpu()
+    g = torch.Generator().manual_seed(D + G)
+    lengths = torch.tensor([1, 0, 2, 15, 16, 17, 63, 64, 65, 127, 128, 129, 255, 257, 600])
+    table, pages = pages_for(g, lengths, ps)
+    kv = fill_cache(g, pages, Hk, ps, D, dtype, kind)
+    q = (2.0 * torch.randn(len(lengths), Hk * G, D, generator=g)).to(dtype)
+    check(q, kv, table, lengths)
+
+
+@gpu
+@pytest.mark.parametrize("dtype,kind", PAIRS, ids=str)
+@pytest.mark.parametrize("window", [1, 5, 64, 100, 10000])
+def test_window(window, dtype, kind):
+    require_gpu()
+    g = torch.Generator().manual_seed(window)
+    lengths = torch.tensor([0, 1, 70, 128, 333, 1000])
+    table, pages = pages_for(g, lengths, 16)
+    for b, n in enumerate(lengths.tolist()):    # pages that the window has left are given up
+        table[b, :max(0, n - window) // 16] = -1
+    kv = fill_cache(g, pages, 2, 16, 64, dtype, kind)
+    check(torch.randn(6, 6, 64, generator=g).to(dtype), kv, table, lengths, window)
+
+
+@gpu
+@pytest.mark.parametrize("dtype,kind", PAIRS, ids=str)
+@pytest.mark.parametrize("ps", [16, 5])
+def test_pages_that_are_none_and_values_behind_them(ps, dtype, kind):
+    """Entries outside the cache hold no tokens; what lies behind a sequence's end, before its window or on
+    other pages may be anything."""
+    require_gpu()
+    g = torch.Generator().manual_seed(ps)
+    lengths = torch.tensor([3, 100, 77, 40, 200, -3, 300])
+    table, pages = pages_for(g, lengths, ps)
+    table[1, 0], table[1, 3], table[2, 1] = -1, pages, 2 ** 31 - 1
+    table[3, :] = -1                              # no page at all
+    lengths[6] = 10 ** 9                          # as long as the table
+    kv = fill_cache(g, pages, 2, ps, 64, dtype, kind)
+    seen = torch.zeros(pages, ps, dtype=torch.bool)
+    for b, n in enumerate(lengths.tolist()):
+        for t in range(max(0, min(n, table.shape[1] * ps) - 90), min(n, table.shape[1] * ps)):
+            e = int(table[b, t // ps])
+            if 0 <= e < pages:
+                seen[e, t % ps] = True
+    dirty = [None if t is None else t.clone() for t in kv]
+    for t in dirty:
+        if t is not None and t.dtype != torch.int8:
+            t.permute(0, 2, 1, *range(3, t.dim()))[~seen] = NAN
+        elif t is not None:
+            t.permute(0, 2, 1, 3)[~seen] = -128
+    q = torch.randn(7, 4, 64, generator=g).to(dtype)
+    check(q, kv, table, lengths, 90)
+    a, b = attend(q, kv, table, lengths, 90), attend(q, dirty, table, lengths, 90)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+@gpu
+@pytest.mark.parametrize("dtype,kind", PAIRS, ids=str)
+def test_one_long_sequence_among_short_ones(dtype, kind):
+    """Heads that many workgroups share, and workgroups that have many heads."""
+    require_gpu()
+    g = torch.Generator().manual_seed(3)
+    lengths = torch.tensor([5, 20000, 1, 700, 0, 64] + [3] * 40)
+    table, pages = pages_for(g, lengths, 32)
+    kv = fill_cache(g, pages, 2, 32, 64, dtype, kind)
+    check((3 * torch.randn(len(lengths), 8, 64, generator=g)).to(dtype), kv, table, lengths)
+
+
+@gpu
+@pytest.mark.parametrize("dtype,kind", [(torch.float32, torch.int8), (torch.bfloat16, torch.bfloat16)], ids=str)
+@pytest.mark.parametrize("B", [255, 256, 257, 1500])
+def test_many_sequences(B, dtype, kind):
+    require_gpu()
+    g = torch.Generator().manual_seed(B)
+    lengths = torch.randint(0, 40, (B,), generator=g)
+    table, pages = pages_for(g, lengths, 16)
+    kv = fill_cache(g, pages, 1, 16, 16, dtype, kind)
+    check(torch.randn(B, 2, 16, generator=g).to(dtype), kv, table, lengths)
+
+
+@gpu
+@pytest.mark.parametrize("dtype,kind", PAIRS, ids=str)
+@pytest.mark.parametrize("case", ["large scores", "one token wins late", "equal scores", "zero scale", "negative scale",
+                                  "small values", "zero values"])
+def test_scores_and_values_at_the_ends(case, dtype, kind):
+    require_gpu()
+    g = torch.Generator().manual_seed(11)
+    lengths = torch.tensor([300, 65, 1])
+    table, pages = pages_for(g, lengths, 16)
+    kv = fill_cache(g, pages, 1, 16, 64, dtype, kind)
+    q = torch.randn(3, 4, 64, generator=g).to(dtype)
+    scale = None
+    if case == "large scores":
+        q = q * 16        # scores of hundreds: one token takes all
+    elif case == "one token wins late":
+        page, at = int(table[0, 290 // 16]), 290 % 16
+        if kind == torch.int8:
+            kv[0][page, 0, at] = torch.sign(q[0, 0].float()).to(torch.int8) * 127
+            kv[2][page, 0, at] = 0.5
+        else:
+            kv[0][page, 0, at] = torch.sign(q[0, 0]) * 60
+    elif case == "equal scores":
+        q = torch.zeros_like(q)
+    elif case == "zero scale":
+        scale = 0.0
+    elif case == "negative scale":
+        scale = -0.3
+    elif case == "small values":
+        q = q * 2.0 ** -12
+        if kind == torch.int8:
+            kv[3] *= 2.0 ** -60
+        else:
+            kv[1] *= 2.0 ** -10
+    else:
+        kv[1].zero_()
+        if kind == torch.int8:
+            kv[3].zero_()
+    check(q, kv, table, lengths, scale=scale)
+
+
+@gpu
+@pytest.mark.parametrize("dtype,kind", PAIRS, ids=str)
+def test_what_is_not_finite_shows_where_it_belongs(dtype, kind):
+    require_gpu()
+    g = torch.Generator().manual_seed(12)
+    lengths = torch.tensor([100, 100, 100, 100, 0])
+    table, pages = pages_for(g, torch.tensor([100, 100, 100, 100, 1]), 16)
+    kv = fill_cache(g, pages, 2, 16, 64, dtype, kind)
+    q = torch.randn(5, 4, 64, generator=g).to(dtype)
+    clean = attend(q, kv, table, lengths)
+    q[0, 1, 7], q[4, 2, 0] = NAN, NAN                      # one query head; an empty sequence
+    page, at = int(table[1, 50 // 16]), 50 % 16            # sequence 1, key head 0: a key
+    page2, at2 = int(table[2, 99 // 16]), 99 % 16          # sequence 2, key head 1: a value
+    if kind == torch.int8:
+        kv[2][page, 0, at], kv[3][page2, 1, at2] = NAN, NAN
+    else:
+        kv[0][page, 0, at, 3], kv[1][page2, 1, at2, 5] = NAN, NAN
+    q[3, 0, 0] = INF
+    o, lse = attend(q, kv, table, lengths)
+    bad = torch.isnan(o)
+    want = torch.zeros_like(bad)
+    want[0, 1] = want[3, 0] = True
+    want[1, :2] = True
+    want[2, 2:] = True if kind == torch.int8 else torch.arange(64) == 5
+    assert torch.equal(bad, want)
+    assert torch.equal(o[~want], clean[0][~want])
+    assert torch.isnan(lse[0, 1]) and torch.isnan(lse[1, :2]).all() and torch.isfinite(lse[2]).all()
+    assert bool((o[4] == 0).all()) and bool(torch.isneginf(lse[4]).all())
+
+
+@gpu
+def test_a_cache_past_4_gib():
+    """Rows whose byte offsets pass 32 bits: written, read and attended to."""
+    require_gpu()
+    pages, Hk, ps, D = 40, 2, 1 << 16, 256        # 5.4 GB of keys
+    cache = make_cache(pages, Hk, ps, D, torch.float32)
+    g = torch.Generator().manual_seed(5)
+    n = 50
+    k, v = (torch.randn(n, Hk, D, generator=g) for _ in range(2))
+    slots = (pages - 1) * ps + torch.arange(n)
+    fg.cache_write(cache, k.cuda(), v.cuda(), slots.int().cuda())
+    a, b = fg.cache_read(cache, slots.int().cuda())
+    assert torch.equal(a.cpu(), k) and torch.equal(b.cpu(), v)
+    assert torch.equal(cache.k[pages - 1, 1, :n].cpu(), k[:, 1])
+    q = torch.randn(1, 4, D, generator=g)
+    o = fg.attention(q.cuda(), cache, torch.tensor([[pages - 1]], dtype=torch.int32).cuda(),
+                     torch.tensor([n], dtype=torch.int32).cuda())
+    kk, vv = (t.permute(1, 0, 2)[None].contiguous() for t in (k, v))
+    kk, vv = kk.reshape(1, Hk, n, D), vv.reshape(1, Hk, n, D)
+    wo, _, bo, _ = ref.attention(q, kk, vv, None, None, torch.tensor([[0]]), torch.tensor([n]), 0, D ** -0.5)
+    assert bool(((o.cpu().double() - wo).abs() <= bo).all())
+
+
+@gpu
+def test_a_cache_without_pages():
+    require_gpu()
+    for kind in (torch.int8, torch.float32):
+        cache = make_cache(0, 2, 16, 64, kind)
+        table, lengths = torch.zeros(2, 3, dtype=torch.int32).cuda(), torch.tensor([0, 40], dtype=torch.int32).cuda()
+        lse = torch.ones(2, 4).cuda()
+        o = fg.attention(torch.randn(2, 4, 64).cuda(), cache, table, lengths, lse=lse)
+        assert bool((o == 0).all()) and bool(torch.isneginf(lse).all())
+        x = torch.randn(2, 2, 64).cuda()
+        fg.cache_write(cache, x, x, lengths)
+        a, b = fg.cache_read(cache, lengths)
+        assert bool((a == 0).all()) and bool((b == 0).all())
