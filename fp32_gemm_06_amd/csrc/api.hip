@@ -679,6 +679,7 @@ int kv_attention(int B, int type, int Hq, const void *Q, int ldq, const fp32gemm
   a.B = B, a.Hq = Hq, a.Hk = c.heads, a.G = G, a.RG = RG;
   a.Q = Q, a.ldq = ldq, a.table = table, a.lengths = lengths, a.window = window;
   a.ldt = c.pages > 0 ? ldt : 0;  // a cache without pages has no tokens
+  a.most = tokens;
   a.scale2 = (float)((double)scale * 1.4426950408889634);
   a.O = O, a.ldo = ldo, a.lse = lse;
   a.cnt = static_cast<unsigned *>(workspace);

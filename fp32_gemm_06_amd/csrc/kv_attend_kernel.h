@@ -29,10 +29,10 @@
 //
 //  codes (s8): both products in integers.  The query's row, and each tile's
 //    weights times V's scales, become fixed-point numbers relative to their
-//    own largest, in signed 8-bit digits: three (23 bits) for fp32 operands,
-//    two (15 bits) for 16-bit ones.  Two leave an error of 2^-16 of a row's
-//    largest q in each product, 3e-5 of a score of unit spread, and 2^-16 of
-//    a tile's largest weight: below a hundredth of the output's rounding.  No
+//    own largest, in signed 8-bit digits: three (23 bits) for the query, as
+//    the scores' sum is an fp32 result of its own; three for the weights of
+//    fp32 outputs, two (15 bits) for 16-bit ones, whose error of 2^-16 of a
+//    tile's largest weight is below a hundredth of the output's rounding.  No
 //    code of the cache is converted.
 //  16-bit floats: products of the type, sums in fp32.  A weight goes in as two
 //    numbers of the type (its rounding and what that left), 16 bits or more.
@@ -97,20 +97,33 @@ template <int DIG> __device__ __forceinline__ void digits4(const float (&v)[4], 
   }
 }
 
-// What a product's digits add up to.
-template <int DIG> __device__ __forceinline__ float digit_sum(const intx4 (&acc)[DIG], int r) {
-  if constexpr (DIG == 3)
-    return __builtin_fmaf(256.0f, (float)((acc[2][r] << 8) + acc[1][r]), (float)acc[0][r]);
-  else
-    return (float)((acc[1][r] << 8) + acc[0][r]);  // below 2^31: 256 products of 127 and 128, or 64
+// A product with fixed-point numbers: the digits' products one behind the other
+// in the same accumulator, moved up a digit in between (two digits stay below
+// 2^31: 256 products of 127 and 128, or 64), the third beside it.
+template <int DIG, int K> __device__ __forceinline__ floatx4 digit_product(const u32x4 (&x)[K], const u32x4 *w) {
+  intx4 hi = {0, 0, 0, 0}, lo = {0, 0, 0, 0};
+  auto add = [&](intx4 &acc, int digit) {
+#pragma unroll
+    for (int j = 0; j < K; ++j)
+      acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(intx4, x[j]),
+                                                  __builtin_bit_cast(intx4, w[digit * K + j]), acc, 0, 0, 0);
+  };
+  add(hi, DIG - 1);
+  hi <<= 8;
+  add(hi, DIG - 2);
+  if constexpr (DIG == 3) add(lo, 0);
+  floatx4 v;
+#pragma unroll
+  for (int r = 0; r < 4; ++r) v[r] = DIG == 3 ? __builtin_fmaf(256.0f, (float)hi[r], (float)lo[r]) : (float)hi[r];
+  return v;
 }
 
 template <class T, bool S8> struct Kind;
 template <class T> struct Kind<T, true> {
-  static constexpr int ES = 1, TOK = 64, DIG = sizeof(T) == 4 ? 3 : 2;
+  static constexpr int ES = 1, TOK = 64, DIG = sizeof(T) == 4 ? 3 : 2, QDIG = 3;
 };
-template <> struct Kind<float, false> { static constexpr int ES = 4, TOK = 16, DIG = 1; };
-template <class T> struct Kind<T, false> { static constexpr int ES = 2, TOK = 32, DIG = 2; };
+template <> struct Kind<float, false> { static constexpr int ES = 4, TOK = 16, DIG = 1, QDIG = 1; };
+template <class T> struct Kind<T, false> { static constexpr int ES = 2, TOK = 32, DIG = 2, QDIG = 1; };
 
 template <class T> __device__ __forceinline__ floatx4 mfma16(u32x4 a, u32x4 b, floatx4 c) {
   typedef T frag __attribute__((ext_vector_type(8)));
@@ -120,13 +133,43 @@ template <class T> __device__ __forceinline__ floatx4 mfma16(u32x4 a, u32x4 b, f
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(frag, a), __builtin_bit_cast(frag, b), c, 0, 0, 0);
 }
 
+// What a partial result with maximum m and sum l counts for under the maximum
+// of all; nothing where it saw no token.
+__device__ __forceinline__ float weight_of(float m, float l, float all) {
+  return m == kNegInf && l == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(m - (all == kNegInf ? 0.0f : all));
+}
+
+// Stores through this XCD's L2 and loads past it, as relaxed atomics of agent
+// scope are made (the sc1 bit), four words at a time.
+constexpr int kThrough = 16;
+__device__ __forceinline__ void store_through(floatx4 v, __amdgpu_buffer_rsrc_t r, uint32_t at) {
+  __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), r, at, 0, kThrough);
+}
+__device__ __forceinline__ void store_through(float v, __amdgpu_buffer_rsrc_t r, uint32_t at) {
+  __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, v), r, at, 0, kThrough);
+}
+__device__ __forceinline__ floatx4 load_through4(__amdgpu_buffer_rsrc_t r, uint32_t at) {
+  return __builtin_bit_cast(floatx4, __builtin_amdgcn_raw_buffer_load_b128(r, at, 0, kThrough));
+}
+__device__ __forceinline__ float load_through(__amdgpu_buffer_rsrc_t r, uint32_t at) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(r, at, 0, kThrough));
+}
+
+// One word at an address that is the same in all lanes, by the scalar unit.
+__device__ __forceinline__ int load_uniform(const int *p) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  typedef const __attribute__((address_space(4))) int constant_int;
+  return *(constant_int *)p;
+#else
+  return *p;
+#endif
+}
+
 // A sequence's units and where its tokens start: lo .. n are seen.
 template <int UNIT> struct Span {
   int lo, n, base, units;
-  __device__ __forceinline__ Span(const AttendArgs &a, int b) {
-    const int most = a.ldt * a.cache.page_size;  // fits: checked by the caller
-    n = a.lengths[b];
-    n = n < 0 ? 0 : n > most ? most : n;
+  __device__ __forceinline__ Span(const AttendArgs &a, int length) {
+    n = length < 0 ? 0 : length > a.most ? a.most : length;
     lo = a.window > 0 && n > a.window ? n - a.window : 0;
     base = lo & ~63;
     units = (n - base + UNIT - 1) / UNIT;
@@ -135,61 +178,56 @@ template <int UNIT> struct Span {
 };
 
 // B16: a page holds whole blocks of 16 tokens, so a block's address is the
-// wave's; else every token has its own.
-template <class T, bool S8, int DP, bool B16>
+// wave's; else every token has its own.  FULL: heads have DP values, not fewer.
+template <class T, bool S8, int DP, bool B16, bool FULL>
 __global__ void __launch_bounds__(256, DP > 128 ? 1 : 2) attend_kernel(AttendArgs a) {
   typedef Kind<T, S8> KD;
-  constexpr int ES = KD::ES, TOK = KD::TOK, DIG = KD::DIG, UNIT = 4 * TOK, BLK = TOK / 16;
+  constexpr int ES = KD::ES, TOK = KD::TOK, DIG = KD::DIG, QDIG = KD::QDIG, UNIT = 4 * TOK, BLK = TOK / 16;
   constexpr int CPL = DP >= 128 ? 8 : 4;       // columns of V of a lane, next to each other
   constexpr int HALVES = DP / (16 * CPL);      // of which there are 16 lanes
   constexpr int KF = DP * ES / 64;             // 16-byte pieces of a token's K in a lane
   constexpr int VW = CPL * ES / 4;             // words of a token's V piece
-  constexpr int NP = HALVES * CPL * 16 * 16;   // outputs of a wave: 16 heads x DP
-  static_assert(NP == 16 * DP, "");
+  constexpr int PITCH = DP + 4;                // of a head's outputs in LDS: 16 heads hit 64 banks
 
-  __shared__ __attribute__((aligned(16))) float merge[4 * NP > kAttendGroups * 16 ? 4 * NP : kAttendGroups * 16];
-  __shared__ float wm[4][16], wl[4][16], red[2][16][16];
-  __shared__ long long scan[4];
-  __shared__ long long at_prefix;
-  __shared__ int at_seq, last;
+  __shared__ __attribute__((aligned(16))) float merge[4][16 * PITCH];
+  __shared__ float wm[4][16], wl[4][16], part_m[16][16], part_l[16][16];
+  __shared__ int scan[4], at_prefix, at_seq, last;
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int n = lane & 15, g = lane >> 4;
-  const int rows = a.Hk * a.RG, D = a.cache.dim, ps = a.cache.page_size;
+  const int rows = a.Hk * a.RG, D = FULL ? DP : a.cache.dim, ps = a.cache.page_size;
 
   // ---- this workgroup's run of units -----------------------------------------
+  // (fewer than 2^31 units: checked by the caller)
   const int each = (a.B + 255) / 256;
-  long long mine = 0;
+  int mine = 0;
   for (int j = 0; j < each; ++j) {
     const int b = tid * each + j;
-    if (b < a.B) mine += (long long)Span<UNIT>(a, b).units * rows;
+    if (b < a.B) mine += Span<UNIT>(a, a.lengths[b]).units * rows;
   }
-  long long incl = mine;
+  int incl = mine;
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) {
-    const long long t = __shfl_up(incl, d, 64);
+    const int t = __shfl_up(incl, d, 64);
     if (lane >= d) incl += t;
   }
   if (lane == 63) scan[wave] = incl;
   __syncthreads();
-  long long total = 0, before = 0;
+  int total = 0;
 #pragma unroll
   for (int w = 0; w < 4; ++w) {
-    before += w < wave ? scan[w] : 0;
+    incl += w < wave ? scan[w] : 0;
     total += scan[w];
   }
-  // (the caller has checked that the units are fewer than 2^31)
-  const int U = (int)total, per = (U + a.groups - 1) / a.groups;
+  const int U = __builtin_amdgcn_readfirstlane(total), per = (U + a.groups - 1) / a.groups;
   const int u0 = (int)blockIdx.x * per;
   if (u0 >= U) return;
   const int u1 = min(U, u0 + per);
-  incl += before;
   if (incl - mine <= u0 && u0 < incl) {
-    long long p = incl - mine;
-    int b = tid * each;
+    int p = incl - mine, b = tid * each;
     for (;; ++b) {
-      const long long t = (long long)Span<UNIT>(a, b).units * rows;
+      const int t = Span<UNIT>(a, a.lengths[b]).units * rows;
       if (u0 < p + t) break;
       p += t;
     }
@@ -198,14 +236,14 @@ __global__ void __launch_bounds__(256, DP > 128 ? 1 : 2) attend_kernel(AttendArg
   }
   __syncthreads();
   int b = __builtin_amdgcn_readfirstlane(at_seq);
-  int prefix = __builtin_amdgcn_readfirstlane((int)at_prefix);
-  Span<UNIT> sp(a, b);
+  int prefix = __builtin_amdgcn_readfirstlane(at_prefix);
+  Span<UNIT> sp(a, load_uniform(a.lengths + b));
   const int first_row = prefix + (u0 - prefix) / sp.units * sp.units;  // unit where the first head starts
 
   for (int u = u0; u < u1;) {
     if (u >= prefix + sp.units * rows) {
       prefix += sp.units * rows;
-      sp = Span<UNIT>(a, ++b);
+      sp = Span<UNIT>(a, load_uniform(a.lengths + ++b));
       continue;
     }
     const int r = (u - prefix) / sp.units, i0 = u - prefix - r * sp.units;
@@ -216,7 +254,7 @@ __global__ void __launch_bounds__(256, DP > 128 ? 1 : 2) attend_kernel(AttendArg
 
     // ---- the query's operand -------------------------------------------------
     const T *q = static_cast<const T *>(a.Q) + (long long)b * a.ldq + (q0 + (n < G ? n : 0)) * D;
-    u32x4 qf[S8 ? DIG * KF : KF];
+    u32x4 qf[QDIG * KF];
     float qscale = a.scale2;
     if constexpr (S8) {
       typedef T eight __attribute__((ext_vector_type(8), aligned(alignof(T))));
@@ -238,18 +276,18 @@ __global__ void __launch_bounds__(256, DP > 128 ? 1 : 2) attend_kernel(AttendArg
       top = nanmax_groups(top);
       // rows below 2^-64 are taken times 2^80, which keeps 1 / top finite
       const float lift = top < 0x1p-64f ? 0x1p80f : 1.0f;
-      const float inv = top > 0.0f ? Fixed<DIG>::top / (top * lift) : 0.0f;
-      qscale *= top < __builtin_inff() ? top * (1.0f / Fixed<DIG>::top) : __builtin_nanf("");  // shows in every score
+      const float inv = top > 0.0f ? Fixed<QDIG>::top / (top * lift) : 0.0f;
+      qscale *= top < __builtin_inff() ? top * (1.0f / Fixed<QDIG>::top) : __builtin_nanf("");  // shows in every score
 #pragma unroll
       for (int j = 0; j < KF; ++j)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const float f[4] = {v[j][4 * e] * lift, v[j][4 * e + 1] * lift, v[j][4 * e + 2] * lift,
                               v[j][4 * e + 3] * lift};
-          uint32_t w[DIG];
-          digits4<DIG>(f, inv, w);
+          uint32_t w[QDIG];
+          digits4<QDIG>(f, inv, w);
 #pragma unroll
-          for (int k = 0; k < DIG; ++k) qf[k * KF + j][e] = w[k];
+          for (int k = 0; k < QDIG; ++k) qf[k * KF + j][e] = w[k];
         }
     } else {
       typedef u32x4 anywhere __attribute__((aligned(2)));
@@ -267,115 +305,118 @@ __global__ void __launch_bounds__(256, DP > 128 ? 1 : 2) attend_kernel(AttendArg
 #pragma unroll
     for (int c = 0; c < HALVES * CPL; ++c) o[c] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
 
-    for (int i = i0; i < i1; ++i) {
-      const int t0 = sp.base + i * UNIT + wave * TOK;
-      if (t0 >= sp.n) break;
-      // rows of the cache: of K's token 16 blk + n, of V's tokens 16 blk + 4 g + i
-      uint32_t krow[BLK], vrow[BLK][4];
-      uint32_t seen = 0;  // by blk: whether the block's (B16) or the token's page exists; bits 4 blk + i
+    // rows of the cache: of each block's first token (B16), and of token `lane`
+    // (modulo TOK); seen: which tokens (B16: blocks) lie on a page
+    struct Rows {
+      uint32_t base[BLK], own;
+      unsigned long long seen;
+    };
+    auto locate = [&](int t0) {
+      Rows w;
+      auto row_of = [&](uint32_t t, int page, uint32_t pi) {
+        return (uint32_t)((page >= 0 && page < a.cache.pages ? page : 0) * a.cache.heads + head) * ps + (t - pi * ps);
+      };
       if constexpr (B16) {
+        w.seen = 0;
 #pragma unroll
         for (int blk = 0; blk < BLK; ++blk) {
           const uint32_t t = t0 + 16 * blk;
           const int pi = (int)((uint64_t)t * a.magic >> a.shift);
-          const int page = pi < a.ldt ? a.table[(long long)b * a.ldt + pi] : -1;
-          const bool ok = page >= 0 && page < a.cache.pages;
-          const uint32_t base = ((ok ? page : 0) * a.cache.heads + head) * ps + (t - pi * ps);
-          seen |= ok ? 0xfu << 4 * blk : 0u;
-          krow[blk] = base + n;
-#pragma unroll
-          for (int k = 0; k < 4; ++k) vrow[blk][k] = base + 4 * g + k;
+          const int page = pi < a.ldt ? load_uniform(a.table + (long long)b * a.ldt + pi) : -1;
+          w.base[blk] = row_of(t, page, pi);
+          w.seen |= page >= 0 && page < a.cache.pages ? 0xffffull << 16 * blk : 0ull;
         }
+        if constexpr (S8)
+          w.own = (lane & 32 ? lane & 16 ? w.base[3] : w.base[2] : lane & 16 ? w.base[1] : w.base[0]) + n;
       } else {
-        // lane t < TOK looks its token's row up, the others ask it
         const uint32_t t = t0 + lane % TOK;
         const int pi = (int)((uint64_t)t * a.magic >> a.shift);
         const int page = pi < a.ldt ? a.table[(long long)b * a.ldt + pi] : -1;
-        const bool ok = page >= 0 && page < a.cache.pages;
-        const uint32_t row = ((ok ? page : 0) * a.cache.heads + head) * ps + (t - pi * ps);
-        const unsigned long long oks = __ballot(ok);
+        w.own = row_of(t, page, pi);
+        w.seen = __ballot(page >= 0 && page < a.cache.pages) & (~0ull >> (64 - TOK));
+      }
+      return w;
+    };
+    u32x4 kf[BLK][KF];
+    typedef uint32_t piece __attribute__((ext_vector_type(VW)));
+    piece vf[BLK][4][HALVES];
+    float ks = 0.0f, vs = 0.0f;  // of token `lane`
+    auto load_keys = [&](const Rows &w) {
 #pragma unroll
-        for (int blk = 0; blk < BLK; ++blk) {
-          krow[blk] = (uint32_t)__shfl((int)row, 16 * blk + n, 64);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            vrow[blk][k] = (uint32_t)__shfl((int)row, 16 * blk + 4 * g + k, 64);
-            seen |= (uint32_t)(oks >> (16 * blk + 4 * g + k) & 1) << (4 * blk + k);
-          }
+      for (int blk = 0; blk < BLK; ++blk) {
+        const char *base = static_cast<const char *>(a.cache.K);
+        uint32_t off = 0;
+        if constexpr (B16) {
+          base += (uint64_t)w.base[blk] * (D * ES);
+          off = n * (D * ES);
+        } else {
+          base += (uint64_t)(uint32_t)__shfl((int)w.own, 16 * blk + n, 64) * (D * ES);
         }
-      }
-      const uint32_t every = BLK == 8 ? ~0u : (1u << 4 * BLK) - 1;
-      const bool whole = t0 >= sp.lo && t0 + TOK <= sp.n && __all(seen == every);
-      if (!whole) {
-#pragma unroll
-        for (int blk = 0; blk < BLK; ++blk)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int t = t0 + 16 * blk + 4 * g + k;
-            if (t < sp.lo || t >= sp.n) seen &= ~(1u << (4 * blk + k));
-          }
-      }
-
-      u32x4 kf[BLK][KF];
-#pragma unroll
-      for (int blk = 0; blk < BLK; ++blk)
 #pragma unroll
         for (int j = 0; j < KF; ++j) {
-          const int d = j * 64 + g * 16;  // bytes
-          const char *p = static_cast<const char *>(a.cache.K) + (uint64_t)krow[blk] * (D * ES);
-          kf[blk][j] = *reinterpret_cast<const u32x4 *>(p + (d < D * ES ? d : 0));
+          const uint32_t d = j * 64 + g * 16;  // bytes
+          kf[blk][j] = *reinterpret_cast<const u32x4 *>(base + (off + (FULL || d < (uint32_t)(D * ES) ? d : 0u)));
         }
-      typedef uint32_t piece __attribute__((ext_vector_type(VW)));
-      piece vf[BLK][4][HALVES];
+      }
+      if constexpr (S8) ks = a.cache.scaleK[w.own];
+    };
+    auto load_values = [&](const Rows &w) {
 #pragma unroll
-      for (int blk = 0; blk < BLK; ++blk)
+      for (int blk = 0; blk < BLK; ++blk) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
+        for (int k = 0; k < 4; ++k) {
+          const char *base = static_cast<const char *>(a.cache.V);
+          uint32_t off = 0;
+          if constexpr (B16) {
+            base += (uint64_t)w.base[blk] * (D * ES);
+            off = (4 * g + k) * (D * ES);
+          } else {
+            base += (uint64_t)(uint32_t)__shfl((int)w.own, 16 * blk + 4 * g + k, 64) * (D * ES);
+          }
 #pragma unroll
           for (int hf = 0; hf < HALVES; ++hf) {
-            const int d = hf * 16 * CPL + n * CPL;
-            const char *p = static_cast<const char *>(a.cache.V) + (uint64_t)vrow[blk][k] * (D * ES);
-            vf[blk][k][hf] = *reinterpret_cast<const piece *>(p + (d < D ? d * ES : 0));
-          }
-      float ks[BLK][4], vs[BLK][4];
-      if constexpr (S8) {
-#pragma unroll
-        for (int blk = 0; blk < BLK; ++blk) {
-          if constexpr (B16) {
-            typedef floatx4 anywhere __attribute__((aligned(4)));
-            const floatx4 x = *reinterpret_cast<const anywhere *>(a.cache.scaleK + vrow[blk][0]);
-            const floatx4 y = *reinterpret_cast<const anywhere *>(a.cache.scaleV + vrow[blk][0]);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) ks[blk][k] = x[k], vs[blk][k] = y[k];
-          } else {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) ks[blk][k] = a.cache.scaleK[vrow[blk][k]], vs[blk][k] = a.cache.scaleV[vrow[blk][k]];
+            const uint32_t d = hf * 16 * CPL + n * CPL;
+            vf[blk][k][hf] = *reinterpret_cast<const piece *>(base + (off + (FULL || d < (uint32_t)D ? d * ES : 0u)));
           }
         }
       }
+      if constexpr (S8) vs = a.cache.scaleV[w.own];
+    };
+
+    // A tile's keys are asked for when the one before has given its scores, its
+    // values when the one before is added up: one tile's bytes are always on
+    // the way while a wave computes, in the registers that it has just read.
+    int t0 = sp.base + i0 * UNIT + wave * TOK;
+    const int tend = min(sp.n, sp.base + i1 * UNIT);
+    Rows at;
+    if (t0 < tend) {
+      at = locate(t0);
+      load_keys(at);
+      load_values(at);
+    }
+    for (; t0 < tend; t0 += UNIT) {
+      const bool more = t0 + UNIT < tend;
+      // which tokens are seen, by their place in the tile
+      unsigned long long seen = at.seen;
+      if (t0 < sp.lo) seen &= ~0ull << (sp.lo - t0);  // fewer than 64 before the window: base is that near
+      if (t0 + 63 >= sp.n) seen &= ~0ull >> (63 - (sp.n - 1 - t0));
+      const bool whole = seen == ~0ull >> (64 - TOK);
+      if (more) at = locate(t0 + UNIT);
 
       // scores, in powers of two
       float s[BLK][4];
 #pragma unroll
       for (int blk = 0; blk < BLK; ++blk) {
         if constexpr (S8) {
-          intx4 acc[DIG];
+          const floatx4 v = digit_product<QDIG, KF>(kf[blk], qf);
 #pragma unroll
-          for (int k = 0; k < DIG; ++k) {
-            acc[k] = intx4{0, 0, 0, 0};
-#pragma unroll
-            for (int j = 0; j < KF; ++j)
-              acc[k] = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(intx4, kf[blk][j]),
-                                                             __builtin_bit_cast(intx4, qf[k * KF + j]), acc[k], 0, 0, 0);
-          }
-#pragma unroll
-          for (int k = 0; k < 4; ++k) s[blk][k] = digit_sum<DIG>(acc, k) * (ks[blk][k] * qscale);
+          for (int k = 0; k < 4; ++k) s[blk][k] = v[k] * (__shfl(ks, 16 * blk + 4 * g + k, 64) * qscale);
         } else {
           floatx4 acc = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
           for (int j = 0; j < KF; ++j) {
             u32x4 x = kf[blk][j];
-            if (D != DP && j * 64 + g * 16 >= D * ES) x = u32x4{0, 0, 0, 0};
+            if (!FULL && j * 64 + g * 16 >= D * ES) x = u32x4{0, 0, 0, 0};
             if constexpr (ES == 2) {
               acc = mfma16<T>(x, qf[j], acc);
             } else {
@@ -389,12 +430,22 @@ __global__ void __launch_bounds__(256, DP > 128 ? 1 : 2) attend_kernel(AttendArg
           for (int k = 0; k < 4; ++k) s[blk][k] = acc[k] * qscale;
         }
       }
+      __builtin_amdgcn_sched_barrier(0);
+      if (more) load_keys(at);
+      __builtin_amdgcn_sched_barrier(0);
       if (!whole) {
 #pragma unroll
         for (int blk = 0; blk < BLK; ++blk)
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            if (!(seen >> (4 * blk + k) & 1)) s[blk][k] = kNegInf;
+          for (int k = 0; k < 4; ++k) {
+            const bool in = (uint32_t)(seen >> 16 * blk) >> (4 * g + k) & 1;
+            s[blk][k] = in ? s[blk][k] : kNegInf;
+            if constexpr (!S8) {
+#pragma unroll
+              for (int hf = 0; hf < HALVES; ++hf)
+                if (!in) vf[blk][k][hf] = piece{};
+            }
+          }
       }
 
       // running maximum and sum; a NaN does not become the maximum, it shows in the sum
@@ -429,7 +480,8 @@ __global__ void __launch_bounds__(256, DP > 128 ? 1 : 2) attend_kernel(AttendArg
         for (int blk = 0; blk < BLK; ++blk)
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            p[blk][k] = seen >> (4 * blk + k) & 1 ? p[blk][k] * vs[blk][k] : 0.0f;
+            p[blk][k] *= __shfl(vs, 16 * blk + 4 * g + k, 64);
+            if (!whole && !((uint32_t)(seen >> 16 * blk) >> (4 * g + k) & 1)) p[blk][k] = 0.0f;
             big = nan_max(big, __builtin_fabsf(p[blk][k]));
           }
         big = nanmax_groups(big);
@@ -464,26 +516,15 @@ __global__ void __launch_bounds__(256, DP > 128 ? 1 : 2) attend_kernel(AttendArg
             }
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-              intx4 acc[DIG];
-#pragma unroll
-              for (int k = 0; k < DIG; ++k)
-                acc[k] = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(intx4, col[c]),
-                                                               __builtin_bit_cast(intx4, pd[k]), intx4{0, 0, 0, 0}, 0, 0, 0);
+              const u32x4 one[1] = {col[c]};
+              const floatx4 v = digit_product<DIG, 1>(one, pd);
               floatx4 &out = o[hf * CPL + 4 * x + c];
 #pragma unroll
-              for (int k = 0; k < 4; ++k) out[k] = __builtin_fmaf(factor, digit_sum<DIG>(acc, k), out[k]);
+              for (int k = 0; k < 4; ++k) out[k] = __builtin_fmaf(factor, v[k], out[k]);
             }
+            __builtin_amdgcn_sched_barrier(0);  // else all columns' sums are in registers at once
           }
       } else {
-        if (!whole) {
-#pragma unroll
-          for (int blk = 0; blk < BLK; ++blk)
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-#pragma unroll
-              for (int hf = 0; hf < HALVES; ++hf)
-                if (!(seen >> (4 * blk + k) & 1)) vf[blk][k][hf] = piece{};
-        }
         if constexpr (ES == 2) {
           u32x4 ph, pl;
 #pragma unroll
@@ -521,11 +562,14 @@ __global__ void __launch_bounds__(256, DP > 128 ? 1 : 2) attend_kernel(AttendArg
                     __builtin_bit_cast(float, (uint32_t)vf[0][k][hf][c]), p[0][k], o[hf * CPL + c], 0, 0, 0);
         }
       }
+      __builtin_amdgcn_sched_barrier(0);
+      if (more) load_values(at);
+      __builtin_amdgcn_sched_barrier(0);
     }
 
     // ---- the four waves' results, joined ----------------------------------------
     l = sum_groups(l);
-    __syncthreads();  // merge, wm, wl and red are free again
+    __syncthreads();  // merge, wm and wl are free again
     if (g == 0) wm[wave][n] = m, wl[wave][n] = l;
     if (n < G) {
 #pragma unroll
@@ -536,18 +580,26 @@ __global__ void __launch_bounds__(256, DP > 128 ? 1 : 2) attend_kernel(AttendArg
           for (int c = 0; c < CPL; c += 4) {
             const int d = hf * 16 * CPL + (4 * g + k) * CPL + c;
             const int x = hf * CPL + c;
-            *reinterpret_cast<floatx4 *>(&merge[wave * NP + n * DP + d]) =
+            *reinterpret_cast<floatx4 *>(&merge[wave][n * PITCH + d]) =
                 floatx4{o[x][k], o[x + 1][k], o[x + 2][k], o[x + 3][k]};
           }
     }
     __syncthreads();
     const bool alone = i0 == 0 && i1 == sp.units;
     const int row_start = prefix + r * sp.units;
-    const int wa = row_start / per, wb = (row_start + sp.units - 1) / per;  // workgroups of this head
-    const size_t record = (size_t)min(16, a.G) * (D + 2);
-    float *part = a.part + (size_t)(2 * blockIdx.x + (row_start == first_row ? 0 : 1)) * record;
-    auto put = [&](int row, int d, float value) {
-      static_cast<T *>(a.O)[(long long)b * a.ldo + (q0 + row) * D + d] = (T)value;
+    // the head's workgroups, and where their parts of it are: a workgroup's
+    // first head is in its first place, its last one, if another, in its second
+    const int wa = row_start / per, ns = (row_start + sp.units - 1) / per - wa + 1;
+    const uint32_t record = (uint32_t)attend_record(min(16, a.G), D) * 4;
+    const __amdgpu_buffer_rsrc_t parts = __builtin_amdgcn_make_buffer_rsrc(
+        a.part, (short)0, (int)(2 * kAttendGroups * record), kRsrcWord3);
+    const int vecs = G * D / 4;  // a part: outputs, maxima, sums
+    auto put = [&](int e, floatx4 v) {
+      const int row = 4 * e / D, d = 4 * e - row * D;
+      typedef T four __attribute__((ext_vector_type(4), aligned(alignof(T))));
+      typedef T plain __attribute__((ext_vector_type(4)));
+      *reinterpret_cast<four *>(static_cast<T *>(a.O) + (long long)b * a.ldo + (q0 + row) * D + d) =
+          plain{(T)v[0], (T)v[1], (T)v[2], (T)v[3]};
     };
     constexpr float bias = __is_same(T, _Float16) && !S8 ? (float)kScoreBias16 : 0.0f;
     auto put_lse = [&](int row, float mm, float ll) {
@@ -555,25 +607,29 @@ __global__ void __launch_bounds__(256, DP > 128 ? 1 : 2) attend_kernel(AttendArg
         a.lse[(long long)b * a.Hq + q0 + row] =
             ll == 0.0f ? kNegInf : (mm - bias + __builtin_amdgcn_logf(ll)) * 0.69314718056f;
     };
-    for (int e = tid; e < G * D; e += 256) {
-      const int row = e / D, d = e - row * D;
-      float mm = kNegInf, ll = 0.0f, sum = 0.0f;
+    const uint32_t mine_at = (uint32_t)(2 * blockIdx.x + (row_start == first_row ? 0 : 1)) * record;
+    for (int e = tid; e < vecs; e += 256) {
+      const int row = 4 * e / D, d = 4 * e - row * D;
+      float mm = kNegInf, ll = 0.0f;
+      floatx4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
       for (int w = 0; w < 4; ++w) mm = __builtin_fmaxf(mm, wm[w][row]);
 #pragma unroll
       for (int w = 0; w < 4; ++w) {
-        const float f = wm[w][row] == kNegInf && wl[w][row] == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(wm[w][row] - (mm == kNegInf ? 0.0f : mm));
+        const float f = weight_of(wm[w][row], wl[w][row], mm);
+        const floatx4 v = *reinterpret_cast<const floatx4 *>(&merge[w][row * PITCH + d]);
         ll = __builtin_fmaf(f, wl[w][row], ll);
-        sum = __builtin_fmaf(f, merge[w * NP + row * DP + d], sum);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) sum[k] = __builtin_fmaf(f, v[k], sum[k]);
       }
       if (alone) {
-        put(row, d, ll == 0.0f ? 0.0f : sum / ll);
+        put(e, ll == 0.0f ? floatx4{0.0f, 0.0f, 0.0f, 0.0f} : sum / ll);
         if (d == 0) put_lse(row, mm, ll);
       } else {
-        __hip_atomic_store(part + row * D + d, sum, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        store_through(sum, parts, mine_at + 16 * e);
         if (d == 0) {
-          __hip_atomic_store(part + G * D + row, mm, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-          __hip_atomic_store(part + G * D + G + row, ll, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+          store_through(mm, parts, mine_at + 16 * vecs + 4 * row);
+          store_through(ll, parts, mine_at + 16 * vecs + 4 * (G + row));
         }
       }
     }
@@ -581,57 +637,65 @@ __global__ void __launch_bounds__(256, DP > 128 ? 1 : 2) attend_kernel(AttendArg
       asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
       __syncthreads();
       if (tid == 0)
-        last = __hip_atomic_fetch_add(&a.cnt[wa], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == (unsigned)(wb - wa);
+        last = __hip_atomic_fetch_add(&a.cnt[wa], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == (unsigned)(ns - 1);
       __syncthreads();
       if (last) {
         asm volatile("" ::: "memory");
-        const int ns = wb - wa + 1;
-        // workgroup wa has this head in its first place only if its run starts here
-        auto src = [&](int w) {
-          return a.part + (size_t)(2 * (wa + w) + (w == 0 && wa * per != row_start ? 1 : 0)) * record;
-        };
-        // weights of the parts, in LDS
+        // 16 parts at a time: four outputs a thread of each, on the way while
+        // the parts' weights are found (thread: part tid / 16, head tid % 16).
+        // Parts behind the last read as zero, past the end of the buffer.
+        const uint32_t at0 = (uint32_t)(2 * wa) * record;
+        const uint32_t extra = wa * per == row_start ? 0 : record;  // of part 0
         const int row = tid & 15, sub = tid >> 4;
-        float mm = kNegInf;
-        if (row < G)
-          for (int w = sub; w < ns; w += 16)
-            mm = __builtin_fmaxf(mm, __hip_atomic_load(src(w) + G * D + row, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
-        red[0][sub][row] = mm;
-        __syncthreads();
-        for (int w = 0; w < 16; ++w) mm = __builtin_fmaxf(mm, red[0][w][row]);
-        float ll = 0.0f;
-        if (row < G)
-          for (int w = sub; w < ns; w += 16) {
-            const float pm = __hip_atomic_load(src(w) + G * D + row, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-            const float pl = __hip_atomic_load(src(w) + G * D + G + row, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-            const float f = pm == kNegInf && pl == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(pm - (mm == kNegInf ? 0.0f : mm));
-            merge[w * 16 + row] = f;
-            ll = __builtin_fmaf(f, pl, ll);
-          }
-        red[1][sub][row] = ll;
-        __syncthreads();
-        for (int e = tid; e < G * D; e += 256) {
-          const int rr = e / D, d = e - rr * D;
-          float sum = 0.0f, all = 0.0f;
-          for (int w = 0; w < 16; ++w) all += red[1][w][rr];
-          int w = 0;
-          for (; w + 8 <= ns; w += 8) {
-            float v[8];
+#pragma unroll 1
+        for (int e0 = 0; e0 < vecs; e0 += 256) {
+          const int e = e0 + tid, rr = min(4 * e / D, 15);
+          floatx4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+          float top = kNegInf, all = 0.0f;  // of head `row`
+#pragma unroll 1
+          for (int w0 = 0; w0 < ns; w0 += 16) {
+            const uint32_t from = at0 + (uint32_t)(2 * w0) * record;
+            const bool in = row < G && w0 + sub < ns;
+            const uint32_t p = from + 2 * sub * record + (w0 + sub == 0 ? extra : 0) + 16 * vecs + 4 * row;
+            float pm = load_through(parts, in ? p : kOob);
+            const float pl = load_through(parts, in ? p + 4 * G : kOob);
+            floatx4 v[16];
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-              v[k] = __hip_atomic_load(src(w + k) + e, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            for (int w = 0; w < 16; ++w)
+              v[w] = load_through4(parts, e < vecs && w0 + w < ns ? from + 2 * w * record + (w0 + w == 0 ? extra : 0) + 16 * e
+                                                                  : kOob);
+            pm = in ? pm : kNegInf;
+            __syncthreads();
+            part_m[sub][row] = pm;
+            part_l[sub][row] = pl;
+            __syncthreads();
+            float mm = top, sum = 0.0f;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) sum = __builtin_fmaf(merge[(w + k) * 16 + rr], v[k], sum);
+            for (int w = 0; w < 16; ++w) mm = __builtin_fmaxf(mm, part_m[w][row]);
+#pragma unroll
+            for (int w = 0; w < 16; ++w)
+              sum = __builtin_fmaf(weight_of(part_m[w][row], part_l[w][row], mm), part_l[w][row], sum);
+            const float old = weight_of(top, all, mm);
+            all = __builtin_fmaf(all, old, sum);
+            top = mm;
+            __syncthreads();
+            part_m[sub][row] = weight_of(pm, pl, mm);
+            if (sub == 0) part_l[0][row] = old;
+            __syncthreads();
+            acc *= part_l[0][rr];
+#pragma unroll
+            for (int w = 0; w < 16; ++w)
+#pragma unroll
+              for (int k = 0; k < 4; ++k) acc[k] = __builtin_fmaf(part_m[w][rr], v[w][k], acc[k]);
           }
-          for (; w < ns; ++w)
-            sum = __builtin_fmaf(merge[w * 16 + rr],
-                                 __hip_atomic_load(src(w) + e, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT), sum);
-          put(rr, d, all == 0.0f ? 0.0f : sum / all);
-          if (d == 0) {
-            float top = kNegInf;
-            for (int k = 0; k < 16; ++k) top = __builtin_fmaxf(top, red[0][k][rr]);
-            put_lse(rr, top, all);
+          __syncthreads();
+          if (sub == 0) {
+            part_l[0][row] = all;
+            if (row < G && e0 == 0) put_lse(row, top, all);
           }
+          __syncthreads();
+          const float sum = part_l[0][rr];
+          if (e < vecs) put(e, sum == 0.0f ? floatx4{0.0f, 0.0f, 0.0f, 0.0f} : acc / sum);
         }
         if (tid == 0) __hip_atomic_store(&a.cnt[wa], 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
       }
@@ -640,11 +704,18 @@ __global__ void __launch_bounds__(256, DP > 128 ? 1 : 2) attend_kernel(AttendArg
   }
 }
 
-template <class T, bool S8, int DP> hipError_t launch_attend_dim(const AttendArgs &a, hipStream_t s) {
-  if (a.cache.page_size % 16 == 0)
-    attend_kernel<T, S8, DP, true><<<a.groups, 256, 0, s>>>(a);
-  else
-    attend_kernel<T, S8, DP, false><<<a.groups, 256, 0, s>>>(a);
+template <class T, bool S8, int DP> hipError_t launch_attend_dim(const AttendArgs &all, hipStream_t s) {
+  AttendArgs a = all;
+  // two workgroups a CU, one where heads past 128 values take the registers of both
+  if (DP > 128 && a.groups > 256) a.groups = 256;
+  const bool blocks = a.cache.page_size % 16 == 0;
+  if (a.cache.dim == DP) {
+    if (blocks) attend_kernel<T, S8, DP, true, true><<<a.groups, 256, 0, s>>>(a);
+    else attend_kernel<T, S8, DP, false, true><<<a.groups, 256, 0, s>>>(a);
+  } else {
+    if (blocks) attend_kernel<T, S8, DP, true, false><<<a.groups, 256, 0, s>>>(a);
+    else attend_kernel<T, S8, DP, false, false><<<a.groups, 256, 0, s>>>(a);
+  }
   return hipGetLastError();
 }
 template <class T, bool S8> hipError_t launch_attend(const AttendArgs &a, hipStream_t s) {

@@ -55,6 +55,7 @@ struct AttendArgs {
   const int *table;
   int ldt;
   const int *lengths;
+  int most;               // tokens that a table's row has pages for
   int window;
   float scale2;           // the scale times log2(e)
   void *O;
@@ -68,8 +69,9 @@ struct AttendArgs {
 constexpr int kAttendGroups = 512;  // most workgroups of a launch
 hipError_t launch_attend_s8(const AttendArgs &a, int type, hipStream_t s);
 hipError_t launch_attend_float(const AttendArgs &a, int type, hipStream_t s);
-// Floats of a partial result: rows query heads with dim values, maximum and sum.
-inline size_t attend_record(int rows, int dim) { return (size_t)rows * (dim + 2); }
+// Floats of a partial result: rows query heads with dim values, maximum and
+// sum, from a multiple of 16 bytes.
+__host__ __device__ inline size_t attend_record(int rows, int dim) { return ((size_t)rows * (dim + 2) + 3) / 4 * 4; }
 // Tokens of a workgroup's step.
 inline int attend_step(int cache_type) { return cache_type == kTypeS8 ? 256 : cache_type == kTypeF32 ? 64 : 128; }
 

@@ -488,8 +488,9 @@ int kv_read(int T, const int *slots, const fp32gemm_kv_cache *cache, int type,
  * whatever they are, have no effect; a NaN or an infinity in the query, or in a
  * key's scale, or in a seen token's values shows in the outputs that depend on
  * it.  Sums are fp32; with codes the products are exact in integers of the
- * query's row and the weights rounded to 23 bits (fp32) or 15 bits (fp16, bf16)
- * of their largest; values below 2^-100 lose digits there.
+ * query's row, rounded to 23 bits of its largest, and of the weights, rounded
+ * to 23 bits (fp32) or 15 (fp16, bf16) of theirs; weighted steps of V below
+ * 2^-100 lose digits there.
  *
  * The lengths and the table are read on the GPU when the call runs, and work is
  * spread by them; a captured call follows later lengths.  Results depend on the

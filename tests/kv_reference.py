@@ -95,7 +95,7 @@ def attention(q, k, v, ks, vs, table, lengths, window, scale):
         out = w @ V
         tiles = t // TILE[kind]
         if kind == torch.int8:
-            lsb = qq.abs().amax(-1) / TOP[digits] * (1.01 if digits == 3 else 0.52)   # per value of q
+            lsb = qq.abs().amax(-1) / TOP[3] * 1.01   # per value of q
             es = abs(scale) * lsb[..., None] * K.abs().sum(-1)[:, None, :].amax(-1, keepdim=True) + 16 * U32 * a
         else:
             es = (2 * D + 16) * U32 * a
