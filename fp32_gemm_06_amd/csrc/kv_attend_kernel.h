@@ -118,6 +118,8 @@ template <int DIG, int K> __device__ __forceinline__ floatx4 digit_product(const
   return v;
 }
 
+template <bool V> struct Flag { static constexpr bool value = V; };
+
 template <class T, bool S8> struct Kind;
 template <class T> struct Kind<T, true> {
   static constexpr int ES = 1, TOK = 64, DIG = sizeof(T) == 4 ? 3 : 2, QDIG = 3;
@@ -141,7 +143,7 @@ __device__ __forceinline__ float weight_of(float m, float l, float all) {
 
 // Stores through this XCD's L2 and loads past it, as relaxed atomics of agent
 // scope are made (the sc1 bit), four words at a time.
-constexpr int kThrough = 16;
+constexpr int kThrough = 16, kNontemporal = 2;
 __device__ __forceinline__ void store_through(floatx4 v, __amdgpu_buffer_rsrc_t r, uint32_t at) {
   __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), r, at, 0, kThrough);
 }
@@ -153,6 +155,35 @@ __device__ __forceinline__ floatx4 load_through4(__amdgpu_buffer_rsrc_t r, uint3
 }
 __device__ __forceinline__ float load_through(__amdgpu_buffer_rsrc_t r, uint32_t at) {
   return __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(r, at, 0, kThrough));
+}
+
+// 16 bytes a lane from memory into LDS, at dst + 16 lane, not kept in the
+// caches.  The compiler counts a buffer's loads when it waits for one of them;
+// behind the other form it waits for all loads.
+__device__ __forceinline__ void load_lds16(__amdgpu_buffer_rsrc_t r, uint32_t off, char *dst) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  typedef __attribute__((address_space(3))) void lds_void;
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void *)dst, 16, off, 0, 0, kNontemporal);
+#else
+  (void)r; (void)off; (void)dst;
+#endif
+}
+__device__ __forceinline__ void load_lds16(const char *src, char *dst) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  typedef __attribute__((address_space(1))) const void global_void;
+  typedef __attribute__((address_space(3))) void lds_void;
+  __builtin_amdgcn_global_load_lds((global_void *)src, (lds_void *)dst, 16, 0, kNontemporal);
+#else
+  (void)src; (void)dst;
+#endif
+}
+
+// Where in its row of CP pieces a piece of K lies (exclusive-ored with this).
+// A cycle of ds_read_b128 takes rows 0-3 and 12-15 at an even piece and rows
+// 4-11 at the one behind it (or the other way round), and 16 pieces fill the
+// banks.
+template <int CP> __device__ __forceinline__ int key_turn(int row) {
+  return CP == 4 ? (row & 8 ? 3 : 0) : CP == 8 ? row & 7 : row & 15;
 }
 
 // One word at an address that is the same in all lanes, by the scalar unit.
@@ -187,9 +218,14 @@ __global__ void __launch_bounds__(256, DP > 128 ? 1 : 2) attend_kernel(AttendArg
   constexpr int HALVES = DP / (16 * CPL);      // of which there are 16 lanes
   constexpr int KF = DP * ES / 64;             // 16-byte pieces of a token's K in a lane
   constexpr int VW = CPL * ES / 4;             // words of a token's V piece
+  constexpr int CP = 4 * KF;                   // 16-byte pieces of a row of K in LDS
   constexpr int PITCH = DP + 4;                // of a head's outputs in LDS: 16 heads hit 64 banks
 
-  __shared__ __attribute__((aligned(16))) float merge[4][16 * PITCH];
+  // each wave's tile of K, and behind the loop the waves' outputs
+  constexpr int KT = TOK * DP * ES;  // bytes of a tile
+  constexpr int SHARED = 4 * KT > 4 * 16 * PITCH * 4 ? 4 * KT : 4 * 16 * PITCH * 4;
+  __shared__ __attribute__((aligned(16))) char shared[SHARED];
+  float(*const merge)[16 * PITCH] = reinterpret_cast<float(*)[16 * PITCH]>(shared);
   __shared__ float wm[4][16], wl[4][16], part_m[16][16], part_l[16][16];
   __shared__ int scan[4], at_prefix, at_seq, last;
 
@@ -313,52 +349,54 @@ __global__ void __launch_bounds__(256, DP > 128 ? 1 : 2) attend_kernel(AttendArg
     };
     auto locate = [&](int t0) {
       Rows w;
-      auto row_of = [&](uint32_t t, int page, uint32_t pi) {
-        return (uint32_t)((page >= 0 && page < a.cache.pages ? page : 0) * a.cache.heads + head) * ps + (t - pi * ps);
+      // the row of token t, and whether its page exists (else a row that does)
+      auto row_of = [&](uint32_t t, auto load, bool &ok) {
+        const int pi = (int)((uint64_t)t * a.magic >> a.shift);
+        const int page = load(a.table + ((long long)b * a.ldt + min(pi, a.ldt - 1)));
+        ok = pi < a.ldt && page >= 0 && page < a.cache.pages;
+        return (uint32_t)((ok ? page : 0) * a.cache.heads + head) * ps + (t - pi * ps);
       };
+      bool ok;
       if constexpr (B16) {
         w.seen = 0;
 #pragma unroll
         for (int blk = 0; blk < BLK; ++blk) {
-          const uint32_t t = t0 + 16 * blk;
-          const int pi = (int)((uint64_t)t * a.magic >> a.shift);
-          const int page = pi < a.ldt ? load_uniform(a.table + (long long)b * a.ldt + pi) : -1;
-          w.base[blk] = row_of(t, page, pi);
-          w.seen |= page >= 0 && page < a.cache.pages ? 0xffffull << 16 * blk : 0ull;
+          w.base[blk] = row_of(t0 + 16 * blk, load_uniform, ok);
+          w.seen |= ok ? 0xffffull << 16 * blk : 0ull;
         }
         if constexpr (S8)
           w.own = (lane & 32 ? lane & 16 ? w.base[3] : w.base[2] : lane & 16 ? w.base[1] : w.base[0]) + n;
       } else {
-        const uint32_t t = t0 + lane % TOK;
-        const int pi = (int)((uint64_t)t * a.magic >> a.shift);
-        const int page = pi < a.ldt ? a.table[(long long)b * a.ldt + pi] : -1;
-        w.own = row_of(t, page, pi);
-        w.seen = __ballot(page >= 0 && page < a.cache.pages) & (~0ull >> (64 - TOK));
+        w.own = row_of(t0 + lane % TOK, [](const int *p) { return *p; }, ok);
+        w.seen = __ballot(ok) & (~0ull >> (64 - TOK));
       }
       return w;
     };
-    u32x4 kf[BLK][KF];
+    char *const kt = shared + wave * KT;
     typedef uint32_t piece __attribute__((ext_vector_type(VW)));
     piece vf[BLK][4][HALVES];
     float ks = 0.0f, vs = 0.0f;  // of token `lane`
+    // K's tile, straight into LDS: an instruction takes 64 pieces of 16 bytes,
+    // whole rows next to each other in the page (loaded as the products want
+    // them, 16 rows at a time, lines are asked for in halves: 5% slower).
+    // Piece c of row r is at place c ^ turn(r), so that the 16 rows that a
+    // ds_read_b128 takes in a cycle are in different banks.
     auto load_keys = [&](const Rows &w) {
 #pragma unroll
-      for (int blk = 0; blk < BLK; ++blk) {
-        const char *base = static_cast<const char *>(a.cache.K);
-        uint32_t off = 0;
-        if constexpr (B16) {
-          base += (uint64_t)w.base[blk] * (D * ES);
-          off = n * (D * ES);
-        } else {
-          base += (uint64_t)(uint32_t)__shfl((int)w.own, 16 * blk + n, 64) * (D * ES);
-        }
-#pragma unroll
-        for (int j = 0; j < KF; ++j) {
-          const uint32_t d = j * 64 + g * 16;  // bytes
-          kf[blk][j] = *reinterpret_cast<const u32x4 *>(base + (off + (FULL || d < (uint32_t)(D * ES) ? d : 0u)));
-        }
+      for (int i = 0; i < BLK * KF; ++i) {
+        const int row = (i * 64 + lane) / CP, blk = i / KF;  // of the tile
+        const uint32_t c = (lane % CP) ^ key_turn<CP>(row % 16);
+        const uint32_t at = FULL || 16 * c < (uint32_t)(D * ES) ? 16 * c : 0u;
+        const char *keys = static_cast<const char *>(a.cache.K);
+        if constexpr (B16)
+          load_lds16(make_rsrc(keys + (uint64_t)w.base[blk] * (D * ES)), (row % 16) * (D * ES) + at, kt + i * 1024);
+        else
+          load_lds16(keys + (uint64_t)(uint32_t)__shfl((int)w.own, row, 64) * (D * ES) + at, kt + i * 1024);
       }
       if constexpr (S8) ks = a.cache.scaleK[w.own];
+    };
+    auto key = [&](int blk, int j) {
+      return *reinterpret_cast<const u32x4 *>(kt + (16 * blk + n) * (CP * 16) + 16 * ((4 * j + g) ^ key_turn<CP>(n)));
     };
     auto load_values = [&](const Rows &w) {
 #pragma unroll
@@ -376,7 +414,8 @@ __global__ void __launch_bounds__(256, DP > 128 ? 1 : 2) attend_kernel(AttendArg
 #pragma unroll
           for (int hf = 0; hf < HALVES; ++hf) {
             const uint32_t d = hf * 16 * CPL + n * CPL;
-            vf[blk][k][hf] = *reinterpret_cast<const piece *>(base + (off + (FULL || d < (uint32_t)D ? d * ES : 0u)));
+            vf[blk][k][hf] = __builtin_nontemporal_load(
+                reinterpret_cast<const piece *>(base + (off + (FULL || d < (uint32_t)D ? d * ES : 0u))));
           }
         }
       }
@@ -394,28 +433,31 @@ __global__ void __launch_bounds__(256, DP > 128 ? 1 : 2) attend_kernel(AttendArg
       load_keys(at);
       load_values(at);
     }
-    for (; t0 < tend; t0 += UNIT) {
-      const bool more = t0 + UNIT < tend;
+    auto tile = [&](auto goes_on) {
+      constexpr bool more = decltype(goes_on)::value;
       // which tokens are seen, by their place in the tile
       unsigned long long seen = at.seen;
       if (t0 < sp.lo) seen &= ~0ull << (sp.lo - t0);  // fewer than 64 before the window: base is that near
       if (t0 + 63 >= sp.n) seen &= ~0ull >> (63 - (sp.n - 1 - t0));
       const bool whole = seen == ~0ull >> (64 - TOK);
-      if (more) at = locate(t0 + UNIT);
+      if constexpr (more) at = locate(t0 + UNIT);
 
       // scores, in powers of two
       float s[BLK][4];
 #pragma unroll
       for (int blk = 0; blk < BLK; ++blk) {
         if constexpr (S8) {
-          const floatx4 v = digit_product<QDIG, KF>(kf[blk], qf);
+          u32x4 kf[KF];
+#pragma unroll
+          for (int j = 0; j < KF; ++j) kf[j] = key(blk, j);
+          const floatx4 v = digit_product<QDIG, KF>(kf, qf);
 #pragma unroll
           for (int k = 0; k < 4; ++k) s[blk][k] = v[k] * (__shfl(ks, 16 * blk + 4 * g + k, 64) * qscale);
         } else {
           floatx4 acc = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
           for (int j = 0; j < KF; ++j) {
-            u32x4 x = kf[blk][j];
+            u32x4 x = key(blk, j);
             if (!FULL && j * 64 + g * 16 >= D * ES) x = u32x4{0, 0, 0, 0};
             if constexpr (ES == 2) {
               acc = mfma16<T>(x, qf[j], acc);
@@ -431,7 +473,7 @@ __global__ void __launch_bounds__(256, DP > 128 ? 1 : 2) attend_kernel(AttendArg
         }
       }
       __builtin_amdgcn_sched_barrier(0);
-      if (more) load_keys(at);
+      if constexpr (more) load_keys(at);
       __builtin_amdgcn_sched_barrier(0);
       if (!whole) {
 #pragma unroll
@@ -563,8 +605,15 @@ __global__ void __launch_bounds__(256, DP > 128 ? 1 : 2) attend_kernel(AttendArg
         }
       }
       __builtin_amdgcn_sched_barrier(0);
-      if (more) load_values(at);
+      if constexpr (more) load_values(at);
       __builtin_amdgcn_sched_barrier(0);
+    };
+    // The last tile asks for no other one.  It has code of its own: with a
+    // branch around each of the two loads the compiler would wait for all of
+    // them where K's tile is needed.
+    if (t0 < tend) {
+      for (; t0 + UNIT < tend; t0 += UNIT) tile(Flag<true>{});
+      tile(Flag<false>{});
     }
 
     // ---- the four waves' results, joined ----------------------------------------
