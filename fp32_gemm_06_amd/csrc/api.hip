@@ -568,6 +568,7 @@ int qk_norm_rope(int T, int D, int type, int Hq, const void *Q, int ldq, void *Y
   a.Q = Q, a.K = K, a.V = nullptr, a.ldq = ldq, a.ldk = ldk, a.ldv = 0;
   a.Yq = Yq, a.Yk = Yk, a.ldyq = ldyq, a.ldyk = ldyk;
   a.Wq = Hq > 0 ? Wq : nullptr, a.Wk = Hk > 0 ? Wk : nullptr, a.eps = eps;
+  a.inv_dim = 1.0 / D;
   a.R = R, a.style = style, a.freq = freq, a.pos = pos, a.slots = nullptr;
   a.cache.type = -1;
   return (int)launch_kv_rows(a, type, reinterpret_cast<hipStream_t>(stream));
@@ -622,7 +623,7 @@ int qkv_rope_write(int T, int type, int Hq, const void *Q, int ldq, void *Yq, in
   a.T = T, a.D = D, a.Hq = Hq, a.Hk = a.Hv = Hk;
   a.Q = Q, a.K = K, a.V = V, a.ldq = ldq, a.ldk = ldk, a.ldv = ldv;
   a.Yq = Yq, a.ldyq = ldyq;
-  a.Wq = Hq > 0 ? Wq : nullptr, a.Wk = Wk, a.eps = eps;
+  a.Wq = Hq > 0 ? Wq : nullptr, a.Wk = Wk, a.eps = eps, a.inv_dim = 1.0 / D;
   a.R = R, a.style = style, a.freq = freq, a.pos = pos, a.slots = slots;
   return (int)launch_kv_rows(a, type, reinterpret_cast<hipStream_t>(stream));
 }

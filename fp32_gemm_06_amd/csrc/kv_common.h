@@ -28,6 +28,7 @@ struct KvRowArgs {
   int ldyq, ldyk;
   const void *Wq, *Wk;    // NULL: no norm
   float eps;
+  double inv_dim;         // 1 / D
   int R, style;           // R values of a head turn; 0: none
   const double *freq;
   const int *pos;

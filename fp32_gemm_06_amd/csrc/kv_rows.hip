@@ -15,9 +15,10 @@
 // of squares is added in, but for values within 1e-15 of a half.  On this card
 // 64-bit fused multiplications run at the rate of 32-bit ones.
 //
-// A group of L lanes has a row, each lane four pairs of it, so the rotation
-// needs no other lane; sine and cosine of the workgroup's tokens are computed
-// once, into LDS, for all their heads.
+// A wave has some rows of one token and one kind (queries, keys or values), a
+// group of L lanes a row at a time, each lane four pairs of it: the rotation
+// needs no other lane, and sines, cosines and weights stay in registers from
+// row to row.  No wave waits for another.
 #include "kv_common.h"
 
 namespace fp32gemm {
@@ -31,14 +32,14 @@ template <class T> struct Four {
 };
 
 // Elements [0, n) of p, zero behind them; and back.
-template <class T, bool WHOLE> __device__ __forceinline__ void load4(const T *p, int n, float *v) {
+template <class T, bool WHOLE, class V> __device__ __forceinline__ void load4(const T *p, int n, V *v) {
   if (WHOLE || n == 4) {
     const typename Four<T>::type c = *reinterpret_cast<const typename Four<T>::anywhere *>(p);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = (float)c[e];
+    for (int e = 0; e < 4; ++e) v[e] = (V)c[e];
   } else {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = e < n ? (float)p[e] : 0.0f;
+    for (int e = 0; e < 4; ++e) v[e] = e < n ? (V)p[e] : (V)0.0f;
   }
 }
 template <class T, bool WHOLE> __device__ __forceinline__ void store4(T *p, int n, const float *v) {
@@ -97,18 +98,46 @@ __device__ __forceinline__ void rotate(double &a, double &b, const SinCos &t) {
   a = u;
 }
 
-template <int L> __device__ __forceinline__ double row_sum(double v) {
-#pragma unroll
-  for (int d = L / 2; d > 0; d >>= 1) v += __shfl_xor(v, d, 64);
+// The value of another lane of the row: in step S the other of the pair, the
+// other pair of the quad, and from there on a lane of the other half of 8, 16,
+// 32 and 64 lanes, whose lanes all hold the same by then.
+template <int S> __device__ __forceinline__ uint32_t across(uint32_t v) {
+  constexpr int kDpp[4] = {0xb1, 0x4e, 0x141, 0x140};
+  if constexpr (S < 4) {
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, kDpp[S < 4 ? S : 0], 0xf, 0xf, false);
+  } else {
+    const auto p = S == 4 ? __builtin_amdgcn_permlane16_swap(v, v, false, false)
+                          : __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    return (threadIdx.x & (S == 4 ? 16 : 32)) ? p[0] : p[1];
+  }
+}
+template <int S> __device__ __forceinline__ double across(double v) {
+  const unsigned long long b = __builtin_bit_cast(unsigned long long, v);
+  const uint32_t lo = across<S>((uint32_t)b), hi = across<S>((uint32_t)(b >> 32));
+  return __builtin_bit_cast(double, (unsigned long long)hi << 32 | lo);
+}
+__device__ __forceinline__ double both(double a, double b) { return a + b; }
+__device__ __forceinline__ uint32_t both(uint32_t a, uint32_t b) { return a > b ? a : b; }
+// Sum (of doubles) or maximum (of words) over a row's L lanes, in all of them.
+template <int L, class V> __device__ __forceinline__ V over_row(V v) {
+  v = both(v, across<0>(v));
+  v = both(v, across<1>(v));
+  v = both(v, across<2>(v));
+  if constexpr (L > 8) v = both(v, across<3>(v));
+  if constexpr (L > 16) v = both(v, across<4>(v));
+  if constexpr (L > 32) v = both(v, across<5>(v));
   return v;
 }
-template <int L> __device__ __forceinline__ uint32_t row_max(uint32_t v) {
+
+// 1 / sqrt(x): the hardware's estimate (23 bits) and two Newton steps.
+__device__ __forceinline__ double rsqrt64(double x) {
+  double y = __builtin_amdgcn_rsq(x);
 #pragma unroll
-  for (int d = L / 2; d > 0; d >>= 1) {
-    const uint32_t t = (uint32_t)__shfl_xor((int)v, d, 64);
-    v = t > v ? t : v;
+  for (int i = 0; i < 2; ++i) {
+    const double h = 0.5 * y;
+    y = __builtin_fma(h, __builtin_fma(-x * y, y, 1.0), y);
   }
-  return v;
+  return y;
 }
 
 // Where a slot's row starts, in rows; -1 for slots outside the cache.
@@ -119,61 +148,36 @@ __device__ __forceinline__ long long cache_row(const KvCache &c, int slot, int h
 }
 
 // CACHE: 0 none, 1 in the operands' type, 2 codes.  WHOLE: every lane's four
-// pairs exist, or none of them.
+// pairs exist, or none of them.  A step is 64 / L rows of one kind; a token's
+// steps are its queries', keys' and values', and a wave takes `steps` of them
+// behind each other.
 template <class T, int L, bool WHOLE, int CACHE>
-__global__ void __launch_bounds__(NT) kv_rows_kernel(KvRowArgs a) {
-  constexpr int RP = NT / L;  // rows of a workgroup
-  __shared__ SinCos turn[4 * NT];  // a workgroup's tokens times R / 2: at most RP (4 L)
-  const int RT = a.Hq + a.Hk + a.Hv;
-  const int rows = a.T * RT, first = blockIdx.x * RP;
+__global__ void __launch_bounds__(NT) kv_rows_kernel(KvRowArgs a, int steps) {
+  constexpr int RPS = 64 / L;  // rows of a step
+  __shared__ SinCos turns_of[NT / 64][4 * L];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int sq = (a.Hq + RPS - 1) / RPS, sk = (a.Hk + RPS - 1) / RPS, sv = (a.Hv + RPS - 1) / RPS;
+  const int pieces = (sq + sk + sv + steps - 1) / steps;
+  const int unit = blockIdx.x * (NT / 64) + wave;
+  const int t = unit / pieces, s0 = (unit - t * pieces) * steps;
+  if (t >= a.T) return;  // a wave by itself: nothing is shared
+  int s1 = min(s0 + steps, sq + sk + sv);
+  long long row0 = 0;
+  if (CACHE > 0 && s1 > sq) {
+    row0 = cache_row(a.cache, a.slots[t], 0);
+    if (row0 < 0) s1 = min(s1, sq);
+  }
   const int half = a.R / 2;
-  const int t0 = first / RT;
-  if (half > 0) {
-    const int t1 = min(first + RP, rows) - 1;
-    const int entries = (t1 / RT - t0 + 1) * half;
-    for (int e = threadIdx.x; e < entries; e += NT) {
-      const int t = e / half;
-      turn[e] = sin_cos((double)a.pos[t0 + t] * a.freq[e - t * half]);
-    }
-  }
 
-  const int i = first + (int)threadIdx.x / L, c = threadIdx.x % L;
-  const bool live = i < rows;
-  const int t = live ? i / RT : t0;
-  int h = live ? i - t * RT : 0;
-  // the row, its norm, and where it goes
-  const T *x, *w;
-  T *y = nullptr;
-  long long row = -1;
-  bool value = false;
-  if (h < a.Hq) {
-    x = static_cast<const T *>(a.Q) + (long long)t * a.ldq + h * a.D;
-    w = static_cast<const T *>(a.Wq);
-    y = static_cast<T *>(a.Yq) + (long long)t * a.ldyq + h * a.D;
-  } else {
-    h -= a.Hq;
-    value = h >= a.Hk;
-    h -= value ? a.Hk : 0;
-    x = value ? static_cast<const T *>(a.V) + (long long)t * a.ldv + h * a.D
-              : static_cast<const T *>(a.K) + (long long)t * a.ldk + h * a.D;
-    w = value ? nullptr : static_cast<const T *>(a.Wk);
-    if constexpr (CACHE == 0) {
-      y = static_cast<T *>(a.Yk) + (long long)t * a.ldyk + h * a.D;
-    } else if (live) {
-      row = cache_row(a.cache, a.slots[t], h);
-      if constexpr (CACHE == 1)
-        if (row >= 0) y = static_cast<T *>(value ? a.cache.V : a.cache.K) + row * a.D;
-    }
-  }
-  const bool codes = CACHE == 2 && y == nullptr;
-  // the lane's pairs
+  // the lane's four pairs of a row
+  const int c = lane % L, group = lane / L;
   int pa, pb, n;
   bool turns;
   if (a.style == 0) {
     const int c1 = (half + 3) / 4;
     turns = c < c1;
-    const int cc = turns ? c : c - c1, hh = turns ? half : (a.D - a.R) / 2;
-    pa = (turns ? 0 : a.R) + 4 * cc;
+    const int cc = turns ? c : c - c1, hh = turns ? half : a.D / 2 - half;
+    pa = (turns ? 0 : 2 * half) + 4 * cc;
     pb = pa + hh;
     n = min(4, hh - 4 * cc);
   } else {
@@ -182,75 +186,115 @@ __global__ void __launch_bounds__(NT) kv_rows_kernel(KvRowArgs a) {
     pb = pa + 4;
     n = 8 * c < a.D ? 4 : 0;
   }
-  turns = turns && !value;
-  const bool has = live && n > 0 && (y != nullptr || (codes && row >= 0));
+  SinCos turn[4];
+  if (half > 0 && s0 < sq + sk) {
+    SinCos *mine = turns_of[wave];
+    const double position = (double)a.pos[t];
+    for (int e = lane; e < half; e += 64) mine[e] = sin_cos(position * a.freq[e]);
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");  // the wave's own LDS is in order
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      turn[e] = turns && 4 * c + e < half ? mine[4 * c + e] : SinCos{0.0, 1.0};
+  }
 
-  float f[8] = {}, g[8];
-  if (has) {
-    load4<T, WHOLE>(x + pa, n, f);
-    load4<T, WHOLE>(x + pb, n, f + 4);
-  }
-  if (w != nullptr && has) {
-    load4<T, WHOLE>(w + pa, n, g);
-    load4<T, WHOLE>(w + pb, n, g + 4);
-  }
-  double v[8];
-#pragma unroll
-  for (int e = 0; e < 8; ++e) v[e] = (double)f[e];
-  if (a.Wq != nullptr || a.Wk != nullptr) {
-    double ss = 0.0;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) ss = __builtin_fma(v[e], v[e], ss);
-    ss = row_sum<L>(ss);
-    if (w != nullptr && has) {
-      const double rstd = 1.0 / __builtin_sqrt(ss / a.D + (double)a.eps);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] *= rstd * (double)g[e];
+  // a step's row, asked for a step before it is used
+  struct Row {
+    T v[8];
+  };
+  auto load = [&](int s) {
+    const bool query = s < sq, value = s >= sq + sk;
+    const int h = (s - (query ? 0 : value ? sq + sk : sq)) * RPS + group;
+    const T *x = static_cast<const T *>(query ? a.Q : value ? a.V : a.K) +
+                 (long long)t * (query ? a.ldq : value ? a.ldv : a.ldk) + h * a.D;
+    Row r = {};
+    if (s < s1 && h < (query ? a.Hq : value ? a.Hv : a.Hk) && n > 0) {
+      load4<T, WHOLE>(x + pa, n, r.v);
+      load4<T, WHOLE>(x + pb, n, r.v + 4);
     }
-  }
-  if (half > 0) {
-    __syncthreads();
-    if (turns && has) {
-      const SinCos *sc = turn + (t - t0) * half + 4 * c;
-if (a.style == 0) {
+    return r;
+  };
+  int kind = -1;  // of the weights in g
+  float g[8];
+  Row next = load(s0);
+  for (int s = s0; s < s1; ++s) {
+    const bool query = s < sq, value = s >= sq + sk;
+    const int now = query ? 0 : value ? 2 : 1;
+    const int h = (s - (query ? 0 : value ? sq + sk : sq)) * RPS + group;
+    const T *w = static_cast<const T *>(query ? a.Wq : value ? nullptr : a.Wk);
+    const bool has = h < (query ? a.Hq : value ? a.Hv : a.Hk) && n > 0;
+    float f[8];
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (WHOLE || e < n) rotate(v[e], v[e + 4], sc[e]);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (4 * c + e < half) rotate(v[2 * e], v[2 * e + 1], sc[e]);
+    for (int e = 0; e < 8; ++e) f[e] = (float)next.v[e];
+    next = load(s + 1);
+    if (now != kind) {
+      kind = now;
+      if (w != nullptr && n > 0) {
+        load4<T, WHOLE>(w + pa, n, g);
+        load4<T, WHOLE>(w + pb, n, g + 4);
       }
     }
-  }
+    if (!value && (w != nullptr || half > 0)) {
+      double v[8];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) f[e] = (float)v[e];
-  if constexpr (CACHE == 2) {
-    uint32_t top = 0;
+      for (int e = 0; e < 8; ++e) v[e] = (double)f[e];
+      if (w != nullptr) {
+        double ss = 0.0;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) top = max(top, abs_bits(f[e]));
-    top = row_max<L>(top);
-    if (codes && has) {
-      const float scale = row_scale(top), inv = quick_inv(scale);
-      int8_t *q = static_cast<int8_t *>(value ? a.cache.V : a.cache.K) + row * a.D;
+        for (int e = 0; e < 8; ++e) ss = __builtin_fma(v[e], v[e], ss);
+        const double rstd = rsqrt64(__builtin_fma(over_row<L>(ss), a.inv_dim, (double)a.eps));
+        if (n > 0) {
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const float u[4] = {f[4 * k], f[4 * k + 1], f[4 * k + 2], f[4 * k + 3]};
-        const uint32_t word = code_word(u, inv, scale);
-        int8_t *p = q + (k ? pb : pa);
-        if (WHOLE || n == 4) {
-          typedef uint32_t anywhere __attribute__((aligned(1)));
-          *reinterpret_cast<anywhere *>(p) = word;
-        } else {
-          for (int e = 0; e < n; ++e) p[e] = (int8_t)(word >> 8 * e);
+          for (int e = 0; e < 8; ++e) v[e] *= rstd * (double)g[e];
         }
       }
-      if (c == 0) (value ? a.cache.scaleV : a.cache.scaleK)[row] = scale;
+      if (turns) {
+        if (a.style == 0) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) rotate(v[e], v[e + 4], turn[e]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (4 * c + e < half) rotate(v[2 * e], v[2 * e + 1], turn[e]);
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[e] = (float)v[e];
     }
-  }
-  if (has && y != nullptr) {
-    store4<T, WHOLE>(y + pa, n, f);
-    store4<T, WHOLE>(y + pb, n, f + 4);
+    if (CACHE == 2 && !query) {
+      uint32_t top = 0;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) top = max(top, abs_bits(f[e]));
+      top = over_row<L>(top);
+      if (has) {
+        const float scale = row_scale(top), inv = quick_inv(scale);
+        const long long row = row0 + (long long)h * a.cache.page_size;
+        int8_t *q = static_cast<int8_t *>(value ? a.cache.V : a.cache.K) + row * a.D;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const float u[4] = {f[4 * k], f[4 * k + 1], f[4 * k + 2], f[4 * k + 3]};
+          const uint32_t word = code_word(u, inv, scale);
+          int8_t *p = q + (k ? pb : pa);
+          if (WHOLE || n == 4) {
+            typedef uint32_t anywhere __attribute__((aligned(1)));
+            *reinterpret_cast<anywhere *>(p) = word;
+          } else {
+            for (int e = 0; e < n; ++e) p[e] = (int8_t)(word >> 8 * e);
+          }
+        }
+        if (c == 0) (value ? a.cache.scaleV : a.cache.scaleK)[row] = scale;
+      }
+    } else if (has) {
+      T *y;
+      if (query)
+        y = static_cast<T *>(a.Yq) + (long long)t * a.ldyq + h * a.D;
+      else if (CACHE == 0)
+        y = static_cast<T *>(a.Yk) + (long long)t * a.ldyk + h * a.D;
+      else
+        y = static_cast<T *>(value ? a.cache.V : a.cache.K) + (row0 + (long long)h * a.cache.page_size) * a.D;
+      store4<T, WHOLE>(y + pa, n, f);
+      store4<T, WHOLE>(y + pb, n, f + 4);
+    }
   }
 }
 
@@ -261,13 +305,24 @@ int lanes_of(const KvRowArgs &a) {
 }
 
 template <class T, int L, bool WHOLE> hipError_t launch_lanes(const KvRowArgs &a, hipStream_t s) {
-  const int rows = a.T * (a.Hq + a.Hk + a.Hv), grid = (rows + NT / L - 1) / (NT / L);
+  auto steps_of = [](int heads) { return (heads + 64 / L - 1) / (64 / L); };
+  const int all = steps_of(a.Hq) + steps_of(a.Hk) + steps_of(a.Hv);
+  // Several steps a wave share the token's sines; one at a time fills the GPU
+  // with fewer tokens.  bf16, 32 + 8 heads of 128, steps of 1 / 2 / 5 / 10: 128
+  // tokens 4.3 / 4.8 / 6.8 / 10.2 us, 1024 11.1 / 9.1 / 10.4 / 13.3, 8192 61 /
+  // 46 / 39.6 / 43.  A token's pieces are made alike.
+  int steps = (int)(((long long)a.T * all + 3000) / 6000);
+  steps = steps < 1 ? 1 : steps > 6 ? 6 : steps;
+  const int pieces = (all + steps - 1) / steps;
+  steps = (all + pieces - 1) / pieces;
+  const long long units = (long long)a.T * ((all + steps - 1) / steps);
+  const int grid = (int)((units + NT / 64 - 1) / (NT / 64));
   if (a.cache.type < 0)
-    kv_rows_kernel<T, L, WHOLE, 0><<<grid, NT, 0, s>>>(a);
+    kv_rows_kernel<T, L, WHOLE, 0><<<grid, NT, 0, s>>>(a, steps);
   else if (a.cache.type == kTypeS8)
-    kv_rows_kernel<T, L, WHOLE, 2><<<grid, NT, 0, s>>>(a);
+    kv_rows_kernel<T, L, WHOLE, 2><<<grid, NT, 0, s>>>(a, steps);
   else
-    kv_rows_kernel<T, L, WHOLE, 1><<<grid, NT, 0, s>>>(a);
+    kv_rows_kernel<T, L, WHOLE, 1><<<grid, NT, 0, s>>>(a, steps);
   return hipGetLastError();
 }
 
