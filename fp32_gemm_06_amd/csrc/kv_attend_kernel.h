@@ -157,9 +157,14 @@ __device__ __forceinline__ float load_through(__amdgpu_buffer_rsrc_t r, uint32_t
   return __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(r, at, 0, kThrough));
 }
 
+// Waits until all but the last N of the wave's memory accesses are done.
+template <int N> __device__ __forceinline__ void wait_loads() {
+  static_assert(N <= 63, "six bits");
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+
 // 16 bytes a lane from memory into LDS, at dst + 16 lane, not kept in the
-// caches.  The compiler counts a buffer's loads when it waits for one of them;
-// behind the other form it waits for all loads.
+// caches.  (Behind the other form the compiler waits for all loads at once.)
 __device__ __forceinline__ void load_lds16(__amdgpu_buffer_rsrc_t r, uint32_t off, char *dst) {
 #if defined(__HIP_DEVICE_COMPILE__)
   typedef __attribute__((address_space(3))) void lds_void;
@@ -196,6 +201,20 @@ __device__ __forceinline__ int load_uniform(const int *p) {
 #endif
 }
 
+// The sum of the lanes up to one's own.
+template <int CTRL, int ROWS> __device__ __forceinline__ int lane_below(int v) {
+  return __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xf, false);
+}
+__device__ __forceinline__ int sum_to_lane(int v) {
+  v += lane_below<0x111, 0xf>(v);  // from 1, 2, 4, 8 lanes below in a row of 16
+  v += lane_below<0x112, 0xf>(v);
+  v += lane_below<0x114, 0xf>(v);
+  v += lane_below<0x118, 0xf>(v);
+  v += lane_below<0x142, 0xa>(v);  // lane 15 of a row to the next row
+  v += lane_below<0x143, 0xc>(v);  // lane 31 to the upper half
+  return v;
+}
+
 // A sequence's units and where its tokens start: lo .. n are seen.
 template <int UNIT> struct Span {
   int lo, n, base, units;
@@ -221,12 +240,12 @@ __global__ void __launch_bounds__(256, DP > 128 ? 1 : 2) attend_kernel(AttendArg
   constexpr int CP = 4 * KF;                   // 16-byte pieces of a row of K in LDS
   constexpr int PITCH = DP + 4;                // of a head's outputs in LDS: 16 heads hit 64 banks
 
-  // each wave's tile of K, and behind the loop the waves' outputs
+  // each wave's tile of K; the waves' outputs when they are joined, beside it,
+  // since the next head's first tile is on its way by then
   constexpr int KT = TOK * DP * ES;  // bytes of a tile
-  constexpr int SHARED = 4 * KT > 4 * 16 * PITCH * 4 ? 4 * KT : 4 * 16 * PITCH * 4;
-  __shared__ __attribute__((aligned(16))) char shared[SHARED];
-  float(*const merge)[16 * PITCH] = reinterpret_cast<float(*)[16 * PITCH]>(shared);
-  __shared__ float wm[4][16], wl[4][16], part_m[16][16], part_l[16][16];
+  __shared__ __attribute__((aligned(16))) char keys_of[4][KT];
+  __shared__ __attribute__((aligned(16))) float merge[4][16 * PITCH];
+  __shared__ float wm[4][16], wl[4][16], part_f[17][16], total_of[16];
   __shared__ int scan[4], at_prefix, at_seq, last;
 
   const int tid = threadIdx.x, lane = tid & 63;
@@ -236,78 +255,181 @@ __global__ void __launch_bounds__(256, DP > 128 ? 1 : 2) attend_kernel(AttendArg
 
   // ---- this workgroup's run of units -----------------------------------------
   // (fewer than 2^31 units: checked by the caller)
-  const int each = (a.B + 255) / 256;
-  int mine = 0;
-  for (int j = 0; j < each; ++j) {
-    const int b = tid * each + j;
-    if (b < a.B) mine += Span<UNIT>(a, a.lengths[b]).units * rows;
-  }
-  int incl = mine;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int t = __shfl_up(incl, d, 64);
-    if (lane >= d) incl += t;
-  }
-  if (lane == 63) scan[wave] = incl;
-  __syncthreads();
-  int total = 0;
-#pragma unroll
-  for (int w = 0; w < 4; ++w) {
-    incl += w < wave ? scan[w] : 0;
-    total += scan[w];
-  }
-  const int U = __builtin_amdgcn_readfirstlane(total), per = (U + a.groups - 1) / a.groups;
-  const int u0 = (int)blockIdx.x * per;
-  if (u0 >= U) return;
-  const int u1 = min(U, u0 + per);
-  if (incl - mine <= u0 && u0 < incl) {
-    int p = incl - mine, b = tid * each;
-    for (;; ++b) {
-      const int t = Span<UNIT>(a, a.lengths[b]).units * rows;
-      if (u0 < p + t) break;
-      p += t;
+  int U, per, u0, u1, b, prefix, length;
+  if (a.B <= 64) {  // a sequence a lane, and no wave waits for another
+    const int len = lane < a.B ? a.lengths[lane] : 0;
+    const int mine = lane < a.B ? Span<UNIT>(a, len).units * rows : 0;
+    const int incl = sum_to_lane(mine);
+    U = __builtin_amdgcn_readlane(incl, 63);
+    per = (U + a.groups - 1) / a.groups;
+    u0 = (int)blockIdx.x * per;
+    if (u0 >= U) return;
+    b = __builtin_popcountll(__ballot(incl <= u0));
+    prefix = __builtin_amdgcn_readlane(incl - mine, b);
+    length = __builtin_amdgcn_readlane(len, b);
+  } else {
+    const int each = (a.B + 255) / 256;
+    int mine = 0;
+    for (int j = 0; j < each; ++j) {
+      const int x = tid * each + j;
+      if (x < a.B) mine += Span<UNIT>(a, a.lengths[x]).units * rows;
     }
-    at_prefix = p;
-    at_seq = b;
+    int incl = sum_to_lane(mine);
+    if (lane == 63) scan[wave] = incl;
+    __syncthreads();
+    int total = 0;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      incl += w < wave ? scan[w] : 0;
+      total += scan[w];
+    }
+    U = __builtin_amdgcn_readfirstlane(total);
+    per = (U + a.groups - 1) / a.groups;
+    u0 = (int)blockIdx.x * per;
+    if (u0 >= U) return;
+    if (incl - mine <= u0 && u0 < incl) {
+      int p = incl - mine, x = tid * each;
+      for (;; ++x) {
+        const int t = Span<UNIT>(a, a.lengths[x]).units * rows;
+        if (u0 < p + t) break;
+        p += t;
+      }
+      at_prefix = p;
+      at_seq = x;
+    }
+    __syncthreads();
+    b = __builtin_amdgcn_readfirstlane(at_seq);
+    prefix = __builtin_amdgcn_readfirstlane(at_prefix);
+    length = load_uniform(a.lengths + b);
   }
-  __syncthreads();
-  int b = __builtin_amdgcn_readfirstlane(at_seq);
-  int prefix = __builtin_amdgcn_readfirstlane(at_prefix);
-  Span<UNIT> sp(a, load_uniform(a.lengths + b));
-  const int first_row = prefix + (u0 - prefix) / sp.units * sp.units;  // unit where the first head starts
+  u1 = min(U, u0 + per);
 
-  for (int u = u0; u < u1;) {
-    if (u >= prefix + sp.units * rows) {
+  // One head's part of the run: units [i0, i1) of the head's, which begin at
+  // unit `start` of all.
+  struct Segment {
+    Span<UNIT> sp;
+    int b, prefix, start, i0, i1, head, q0, G;
+  };
+  auto segment = [&](int u, int b, int prefix, Span<UNIT> sp) {
+    while (u >= prefix + sp.units * rows) {
       prefix += sp.units * rows;
       sp = Span<UNIT>(a, load_uniform(a.lengths + ++b));
-      continue;
     }
-    const int r = (u - prefix) / sp.units, i0 = u - prefix - r * sp.units;
-    const int i1 = min(sp.units, i0 + u1 - u);
-    const int head = r / a.RG, h0 = (r - head * a.RG) * 16;
-    const int G = min(16, a.G - h0);  // query heads here
-    const int q0 = head * a.G + h0;   // the first of them
+    const int r = (u - prefix) / sp.units, head = r / a.RG, h0 = (r - head * a.RG) * 16;
+    const int start = prefix + r * sp.units, i0 = u - start;
+    return Segment{sp, b, prefix, start, i0, min(sp.units, i0 + u1 - u), head, head * a.G + h0, min(16, a.G - h0)};
+  };
+  Segment sg = segment(u0, b, prefix, Span<UNIT>(a, length));
+  const int first_row = sg.start;
 
-    // ---- the query's operand -------------------------------------------------
-    const T *q = static_cast<const T *>(a.Q) + (long long)b * a.ldq + (q0 + (n < G ? n : 0)) * D;
-    u32x4 qf[QDIG * KF];
-    float qscale = a.scale2;
+  // rows of the cache: of each block's first token (B16), and of token `lane`
+  // (modulo TOK); seen: which tokens (B16: blocks) lie on a page
+  struct Rows {
+    uint32_t base[BLK], own;
+    unsigned long long seen;
+  };
+  auto locate = [&](const Segment &sg, int t0) {
+    Rows w;
+    // the row of token t, and whether its page exists (else a row that does)
+    auto row_of = [&](uint32_t t, auto load, bool &ok) {
+      const int pi = (int)((uint64_t)t * a.magic >> a.shift);
+      const int page = load(a.table + ((long long)sg.b * a.ldt + min(pi, a.ldt - 1)));
+      ok = pi < a.ldt && page >= 0 && page < a.cache.pages;
+      return (uint32_t)((ok ? page : 0) * a.cache.heads + sg.head) * ps + (t - pi * ps);
+    };
+    bool ok;
+    if constexpr (B16) {
+      w.seen = 0;
+#pragma unroll
+      for (int blk = 0; blk < BLK; ++blk) {
+        w.base[blk] = row_of(t0 + 16 * blk, load_uniform, ok);
+        w.seen |= ok ? 0xffffull << 16 * blk : 0ull;
+      }
+      if constexpr (S8)
+        w.own = (lane & 32 ? lane & 16 ? w.base[3] : w.base[2] : lane & 16 ? w.base[1] : w.base[0]) + n;
+    } else {
+      w.own = row_of(t0 + lane % TOK, [](const int *p) { return *p; }, ok);
+      w.seen = __ballot(ok) & (~0ull >> (64 - TOK));
+    }
+    return w;
+  };
+  char *const kt = keys_of[wave];
+  typedef uint32_t piece __attribute__((ext_vector_type(VW)));
+  piece vf[BLK][4][HALVES];
+  float ks = 0.0f, vs = 0.0f;  // of token `lane`
+  // K's tile, straight into LDS: an instruction takes 64 pieces of 16 bytes,
+  // whole rows next to each other in the page (loaded as the products want
+  // them, 16 rows at a time, lines are asked for in halves: 5% slower).
+  // Piece c of row r is at place c ^ turn(r), so that the 16 rows that a
+  // ds_read_b128 takes in a cycle are in different banks.
+  auto load_keys = [&](const Rows &w) {
+#pragma unroll
+    for (int i = 0; i < BLK * KF; ++i) {
+      const int row = (i * 64 + lane) / CP, blk = i / KF;  // of the tile
+      const uint32_t c = (lane % CP) ^ key_turn<CP>(row % 16);
+      const uint32_t at = FULL || 16 * c < (uint32_t)(D * ES) ? 16 * c : 0u;
+      const char *keys = static_cast<const char *>(a.cache.K);
+      if constexpr (B16)
+        load_lds16(make_rsrc(keys + (uint64_t)w.base[blk] * (D * ES)), (row % 16) * (D * ES) + at, kt + i * 1024);
+      else
+        load_lds16(keys + (uint64_t)(uint32_t)__shfl((int)w.own, row, 64) * (D * ES) + at, kt + i * 1024);
+    }
+    if constexpr (S8) ks = a.cache.scaleK[w.own];
+  };
+  auto key = [&](int blk, int j) {
+    return *reinterpret_cast<const u32x4 *>(kt + (16 * blk + n) * (CP * 16) + 16 * ((4 * j + g) ^ key_turn<CP>(n)));
+  };
+  auto load_values = [&](const Rows &w) {
+    const char *values = static_cast<const char *>(a.cache.V);
+    uint32_t col[HALVES];
+#pragma unroll
+    for (int hf = 0; hf < HALVES; ++hf) {
+      const uint32_t d = hf * 16 * CPL + n * CPL;
+      col[hf] = FULL || d < (uint32_t)D ? d * ES : 0u;
+    }
+#pragma unroll
+    for (int blk = 0; blk < BLK; ++blk) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const char *row;
+        if constexpr (B16)
+          row = values + (uint64_t)w.base[blk] * (D * ES) + (uint32_t)(4 * g * (D * ES)) + k * (D * ES);
+        else
+          row = values + (uint64_t)(uint32_t)__shfl((int)w.own, 16 * blk + 4 * g + k, 64) * (D * ES);
+#pragma unroll
+        for (int hf = 0; hf < HALVES; ++hf)
+          vf[blk][k][hf] = __builtin_nontemporal_load(reinterpret_cast<const piece *>(row + col[hf]));
+      }
+    }
+    if constexpr (S8) vs = a.cache.scaleV[w.own];
+  };
+
+  // The query's values as they are in memory, then its operand: 16 values of
+  // piece j for codes, 16 bytes else.
+  typedef uint32_t raw __attribute__((ext_vector_type(S8 ? 4 * sizeof(T) : 4)));
+  typedef raw raw_anywhere __attribute__((aligned(2)));
+  raw qr[KF];
+  auto load_query = [&](const Segment &sg) {
+    const T *q = static_cast<const T *>(a.Q) + (long long)sg.b * a.ldq + (sg.q0 + (n < sg.G ? n : 0)) * D;
+#pragma unroll
+    for (int j = 0; j < KF; ++j) {
+      const int d = j * (64 / ES) + g * (16 / ES);
+      qr[j] = *reinterpret_cast<const raw_anywhere *>(q + (d < D ? d : 0));
+      if (n >= sg.G || d >= D) qr[j] = raw{};
+    }
+  };
+  u32x4 qf[QDIG * KF];
+  float qscale;
+  auto turn_query = [&]() {
+    qscale = a.scale2;
     if constexpr (S8) {
-      typedef T eight __attribute__((ext_vector_type(8), aligned(alignof(T))));
-      float v[KF][16];
+      typedef T sixteen __attribute__((ext_vector_type(16)));
       float top = 0.0f;
 #pragma unroll
       for (int j = 0; j < KF; ++j) {
-        const int d = j * 64 + g * 16;
+        const sixteen x = __builtin_bit_cast(sixteen, qr[j]);
 #pragma unroll
-        for (int e = 0; e < 16; e += 8) {
-          eight x = *reinterpret_cast<const eight *>(q + (d < D ? d + e : 0));
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            v[j][e + k] = n < G && d < D ? (float)x[k] : 0.0f;
-            top = nan_max(top, __builtin_fabsf(v[j][e + k]));
-          }
-        }
+        for (int e = 0; e < 16; ++e) top = nan_max(top, __builtin_fabsf((float)x[e]));
       }
       top = nanmax_groups(top);
       // rows below 2^-64 are taken times 2^80, which keeps 1 / top finite
@@ -315,25 +437,43 @@ __global__ void __launch_bounds__(256, DP > 128 ? 1 : 2) attend_kernel(AttendArg
       const float inv = top > 0.0f ? Fixed<QDIG>::top / (top * lift) : 0.0f;
       qscale *= top < __builtin_inff() ? top * (1.0f / Fixed<QDIG>::top) : __builtin_nanf("");  // shows in every score
 #pragma unroll
-      for (int j = 0; j < KF; ++j)
+      for (int j = 0; j < KF; ++j) {
+        const sixteen x = __builtin_bit_cast(sixteen, qr[j]);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const float f[4] = {v[j][4 * e] * lift, v[j][4 * e + 1] * lift, v[j][4 * e + 2] * lift,
-                              v[j][4 * e + 3] * lift};
+          const float f[4] = {(float)x[4 * e] * lift, (float)x[4 * e + 1] * lift, (float)x[4 * e + 2] * lift,
+                              (float)x[4 * e + 3] * lift};
           uint32_t w[QDIG];
           digits4<QDIG>(f, inv, w);
 #pragma unroll
           for (int k = 0; k < QDIG; ++k) qf[k * KF + j][e] = w[k];
         }
-    } else {
-      typedef u32x4 anywhere __attribute__((aligned(2)));
-#pragma unroll
-      for (int j = 0; j < KF; ++j) {
-        const int d = j * (64 / ES) + g * (16 / ES);
-        const u32x4 x = *reinterpret_cast<const anywhere *>(q + (d < D ? d : 0));
-        qf[j] = n < G && d < D ? x : u32x4{0, 0, 0, 0};
       }
+    } else {
+#pragma unroll
+      for (int j = 0; j < KF; ++j) qf[j] = qr[j];
     }
+  };
+
+  // A tile's keys are asked for when the one before has given its scores, its
+  // values when the one before is added up: one tile's bytes are always on the
+  // way while a wave computes, in the place that it has just read.  A head's
+  // query and first tile are asked for before the head in front of it is joined.
+  Rows at;
+  int t0, tend;
+  auto begin = [&](const Segment &sg, auto first) {
+    t0 = sg.sp.base + sg.i0 * UNIT + wave * TOK;
+    tend = min(sg.sp.n, sg.sp.base + sg.i1 * UNIT);
+    load_query(sg);
+    if (t0 < tend) {
+      at = locate(sg, t0);
+      load_keys(at);
+      load_values(at);
+      if constexpr (decltype(first)::value) turn_query();  // while they are on the way
+    }
+  };
+  begin(sg, Flag<true>{});
+  for (;;) {
 
     // ---- the tokens ------------------------------------------------------------
     float m = kNegInf, l = 0.0f;
@@ -341,106 +481,19 @@ __global__ void __launch_bounds__(256, DP > 128 ? 1 : 2) attend_kernel(AttendArg
 #pragma unroll
     for (int c = 0; c < HALVES * CPL; ++c) o[c] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
 
-    // rows of the cache: of each block's first token (B16), and of token `lane`
-    // (modulo TOK); seen: which tokens (B16: blocks) lie on a page
-    struct Rows {
-      uint32_t base[BLK], own;
-      unsigned long long seen;
-    };
-    auto locate = [&](int t0) {
-      Rows w;
-      // the row of token t, and whether its page exists (else a row that does)
-      auto row_of = [&](uint32_t t, auto load, bool &ok) {
-        const int pi = (int)((uint64_t)t * a.magic >> a.shift);
-        const int page = load(a.table + ((long long)b * a.ldt + min(pi, a.ldt - 1)));
-        ok = pi < a.ldt && page >= 0 && page < a.cache.pages;
-        return (uint32_t)((ok ? page : 0) * a.cache.heads + head) * ps + (t - pi * ps);
-      };
-      bool ok;
-      if constexpr (B16) {
-        w.seen = 0;
-#pragma unroll
-        for (int blk = 0; blk < BLK; ++blk) {
-          w.base[blk] = row_of(t0 + 16 * blk, load_uniform, ok);
-          w.seen |= ok ? 0xffffull << 16 * blk : 0ull;
-        }
-        if constexpr (S8)
-          w.own = (lane & 32 ? lane & 16 ? w.base[3] : w.base[2] : lane & 16 ? w.base[1] : w.base[0]) + n;
-      } else {
-        w.own = row_of(t0 + lane % TOK, [](const int *p) { return *p; }, ok);
-        w.seen = __ballot(ok) & (~0ull >> (64 - TOK));
-      }
-      return w;
-    };
-    char *const kt = shared + wave * KT;
-    typedef uint32_t piece __attribute__((ext_vector_type(VW)));
-    piece vf[BLK][4][HALVES];
-    float ks = 0.0f, vs = 0.0f;  // of token `lane`
-    // K's tile, straight into LDS: an instruction takes 64 pieces of 16 bytes,
-    // whole rows next to each other in the page (loaded as the products want
-    // them, 16 rows at a time, lines are asked for in halves: 5% slower).
-    // Piece c of row r is at place c ^ turn(r), so that the 16 rows that a
-    // ds_read_b128 takes in a cycle are in different banks.
-    auto load_keys = [&](const Rows &w) {
-#pragma unroll
-      for (int i = 0; i < BLK * KF; ++i) {
-        const int row = (i * 64 + lane) / CP, blk = i / KF;  // of the tile
-        const uint32_t c = (lane % CP) ^ key_turn<CP>(row % 16);
-        const uint32_t at = FULL || 16 * c < (uint32_t)(D * ES) ? 16 * c : 0u;
-        const char *keys = static_cast<const char *>(a.cache.K);
-        if constexpr (B16)
-          load_lds16(make_rsrc(keys + (uint64_t)w.base[blk] * (D * ES)), (row % 16) * (D * ES) + at, kt + i * 1024);
-        else
-          load_lds16(keys + (uint64_t)(uint32_t)__shfl((int)w.own, row, 64) * (D * ES) + at, kt + i * 1024);
-      }
-      if constexpr (S8) ks = a.cache.scaleK[w.own];
-    };
-    auto key = [&](int blk, int j) {
-      return *reinterpret_cast<const u32x4 *>(kt + (16 * blk + n) * (CP * 16) + 16 * ((4 * j + g) ^ key_turn<CP>(n)));
-    };
-    auto load_values = [&](const Rows &w) {
-#pragma unroll
-      for (int blk = 0; blk < BLK; ++blk) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const char *base = static_cast<const char *>(a.cache.V);
-          uint32_t off = 0;
-          if constexpr (B16) {
-            base += (uint64_t)w.base[blk] * (D * ES);
-            off = (4 * g + k) * (D * ES);
-          } else {
-            base += (uint64_t)(uint32_t)__shfl((int)w.own, 16 * blk + 4 * g + k, 64) * (D * ES);
-          }
-#pragma unroll
-          for (int hf = 0; hf < HALVES; ++hf) {
-            const uint32_t d = hf * 16 * CPL + n * CPL;
-            vf[blk][k][hf] = __builtin_nontemporal_load(
-                reinterpret_cast<const piece *>(base + (off + (FULL || d < (uint32_t)D ? d * ES : 0u))));
-          }
-        }
-      }
-      if constexpr (S8) vs = a.cache.scaleV[w.own];
-    };
-
-    // A tile's keys are asked for when the one before has given its scores, its
-    // values when the one before is added up: one tile's bytes are always on
-    // the way while a wave computes, in the registers that it has just read.
-    int t0 = sp.base + i0 * UNIT + wave * TOK;
-    const int tend = min(sp.n, sp.base + i1 * UNIT);
-    Rows at;
-    if (t0 < tend) {
-      at = locate(t0);
-      load_keys(at);
-      load_values(at);
-    }
     auto tile = [&](auto goes_on) {
       constexpr bool more = decltype(goes_on)::value;
       // which tokens are seen, by their place in the tile
       unsigned long long seen = at.seen;
-      if (t0 < sp.lo) seen &= ~0ull << (sp.lo - t0);  // fewer than 64 before the window: base is that near
-      if (t0 + 63 >= sp.n) seen &= ~0ull >> (63 - (sp.n - 1 - t0));
+      if (t0 < sg.sp.lo) seen &= ~0ull << (sg.sp.lo - t0);  // fewer than 64 before the window: base is that near
+      if (t0 + 63 >= sg.sp.n) seen &= ~0ull >> (63 - (sg.sp.n - 1 - t0));
       const bool whole = seen == ~0ull >> (64 - TOK);
-      if constexpr (more) at = locate(t0 + UNIT);
+      if constexpr (more) at = locate(sg, t0 + UNIT);
+
+      // K's tile has landed when no more than V's loads, which were asked for
+      // behind it, are on the way.  (The compiler does not see what the loads
+      // into LDS write, so it need not wait for them by itself.)
+      wait_loads<BLK * 4 * HALVES * ((VW + 3) / 4)>();
 
       // scores, in powers of two
       float s[BLK][4];
@@ -472,6 +525,7 @@ __global__ void __launch_bounds__(256, DP > 128 ? 1 : 2) attend_kernel(AttendArg
           for (int k = 0; k < 4; ++k) s[blk][k] = acc[k] * qscale;
         }
       }
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // K's tile has been read
       __builtin_amdgcn_sched_barrier(0);
       if constexpr (more) load_keys(at);
       __builtin_amdgcn_sched_barrier(0);
@@ -617,6 +671,14 @@ __global__ void __launch_bounds__(256, DP > 128 ? 1 : 2) attend_kernel(AttendArg
     }
 
     // ---- the four waves' results, joined ----------------------------------------
+    const Segment done = sg;
+    const int u = sg.start + sg.i1;
+    const bool more = u < u1;
+    if (more) {
+      sg = segment(u, sg.b, sg.prefix, sg.sp);
+      begin(sg, Flag<false>{});
+    }
+    const int G = done.G;
     l = sum_groups(l);
     __syncthreads();  // merge, wm and wl are free again
     if (g == 0) wm[wave][n] = m, wl[wave][n] = l;
@@ -634,11 +696,11 @@ __global__ void __launch_bounds__(256, DP > 128 ? 1 : 2) attend_kernel(AttendArg
           }
     }
     __syncthreads();
-    const bool alone = i0 == 0 && i1 == sp.units;
-    const int row_start = prefix + r * sp.units;
+    const bool alone = done.i0 == 0 && done.i1 == done.sp.units;
+    const int row_start = done.start;
     // the head's workgroups, and where their parts of it are: a workgroup's
     // first head is in its first place, its last one, if another, in its second
-    const int wa = row_start / per, ns = (row_start + sp.units - 1) / per - wa + 1;
+    const int wa = row_start / per, ns = (row_start + done.sp.units - 1) / per - wa + 1;
     const uint32_t record = (uint32_t)attend_record(min(16, a.G), D) * 4;
     const __amdgpu_buffer_rsrc_t parts = __builtin_amdgcn_make_buffer_rsrc(
         a.part, (short)0, (int)(2 * kAttendGroups * record), kRsrcWord3);
@@ -647,13 +709,13 @@ __global__ void __launch_bounds__(256, DP > 128 ? 1 : 2) attend_kernel(AttendArg
       const int row = 4 * e / D, d = 4 * e - row * D;
       typedef T four __attribute__((ext_vector_type(4), aligned(alignof(T))));
       typedef T plain __attribute__((ext_vector_type(4)));
-      *reinterpret_cast<four *>(static_cast<T *>(a.O) + (long long)b * a.ldo + (q0 + row) * D + d) =
+      *reinterpret_cast<four *>(static_cast<T *>(a.O) + (long long)done.b * a.ldo + (done.q0 + row) * D + d) =
           plain{(T)v[0], (T)v[1], (T)v[2], (T)v[3]};
     };
     constexpr float bias = __is_same(T, _Float16) && !S8 ? (float)kScoreBias16 : 0.0f;
     auto put_lse = [&](int row, float mm, float ll) {
       if (a.lse != nullptr)
-        a.lse[(long long)b * a.Hq + q0 + row] =
+        a.lse[(long long)done.b * a.Hq + done.q0 + row] =
             ll == 0.0f ? kNegInf : (mm - bias + __builtin_amdgcn_logf(ll)) * 0.69314718056f;
     };
     const uint32_t mine_at = (uint32_t)(2 * blockIdx.x + (row_start == first_row ? 0 : 1)) * record;
@@ -691,8 +753,9 @@ __global__ void __launch_bounds__(256, DP > 128 ? 1 : 2) attend_kernel(AttendArg
       if (last) {
         asm volatile("" ::: "memory");
         // 16 parts at a time: four outputs a thread of each, on the way while
-        // the parts' weights are found (thread: part tid / 16, head tid % 16).
-        // Parts behind the last read as zero, past the end of the buffer.
+        // the parts' weights are found (thread: part tid / 16, head tid % 16;
+        // a wave's four parts by lane exchange, the waves' in LDS).  Parts
+        // behind the last read as zero, past the end of the buffer.
         const uint32_t at0 = (uint32_t)(2 * wa) * record;
         const uint32_t extra = wa * per == row_start ? 0 : record;  // of part 0
         const int row = tid & 15, sub = tid >> 4;
@@ -714,42 +777,40 @@ __global__ void __launch_bounds__(256, DP > 128 ? 1 : 2) attend_kernel(AttendArg
               v[w] = load_through4(parts, e < vecs && w0 + w < ns ? from + 2 * w * record + (w0 + w == 0 ? extra : 0) + 16 * e
                                                                   : kOob);
             pm = in ? pm : kNegInf;
+            const float wave_m = fmax_groups(pm);
+            if (g == 0) wm[wave][row] = wave_m;
             __syncthreads();
-            part_m[sub][row] = pm;
-            part_l[sub][row] = pl;
+            float mm = top;
+#pragma unroll
+            for (int w = 0; w < 4; ++w) mm = __builtin_fmaxf(mm, wm[w][row]);
+            const float f = weight_of(pm, pl, mm), old = weight_of(top, all, mm);
+            const float wave_l = sum_groups(f * pl);
+            part_f[1 + sub][row] = f;
+            if (sub == 0) part_f[0][row] = old;
+            if (g == 0) wl[wave][row] = wave_l;
             __syncthreads();
-            float mm = top, sum = 0.0f;
-#pragma unroll
-            for (int w = 0; w < 16; ++w) mm = __builtin_fmaxf(mm, part_m[w][row]);
-#pragma unroll
-            for (int w = 0; w < 16; ++w)
-              sum = __builtin_fmaf(weight_of(part_m[w][row], part_l[w][row], mm), part_l[w][row], sum);
-            const float old = weight_of(top, all, mm);
-            all = __builtin_fmaf(all, old, sum);
+            all = __builtin_fmaf(all, old, (wl[0][row] + wl[1][row]) + (wl[2][row] + wl[3][row]));
             top = mm;
-            __syncthreads();
-            part_m[sub][row] = weight_of(pm, pl, mm);
-            if (sub == 0) part_l[0][row] = old;
-            __syncthreads();
-            acc *= part_l[0][rr];
+            acc *= part_f[0][rr];
 #pragma unroll
             for (int w = 0; w < 16; ++w)
 #pragma unroll
-              for (int k = 0; k < 4; ++k) acc[k] = __builtin_fmaf(part_m[w][rr], v[w][k], acc[k]);
+              for (int k = 0; k < 4; ++k) acc[k] = __builtin_fmaf(part_f[1 + w][rr], v[w][k], acc[k]);
           }
-          __syncthreads();
           if (sub == 0) {
-            part_l[0][row] = all;
+            total_of[row] = all;
             if (row < G && e0 == 0) put_lse(row, top, all);
           }
           __syncthreads();
-          const float sum = part_l[0][rr];
+          const float sum = total_of[rr];
           if (e < vecs) put(e, sum == 0.0f ? floatx4{0.0f, 0.0f, 0.0f, 0.0f} : acc / sum);
+          __syncthreads();
         }
         if (tid == 0) __hip_atomic_store(&a.cnt[wa], 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
       }
     }
-    u += i1 - i0;
+    if (!more) break;
+    turn_query();
   }
 }
 
