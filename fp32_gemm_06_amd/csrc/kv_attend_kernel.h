@@ -255,17 +255,28 @@ __global__ void __launch_bounds__(256, DP > 128 ? 1 : 2) attend_kernel(AttendArg
 
   // ---- this workgroup's run of units -----------------------------------------
   // (fewer than 2^31 units: checked by the caller)
-  int U, per, u0, u1, b, prefix, length;
+  // With long runs a head's beginning and end, which cost what a unit does, are
+  // counted as one more in front of its own (`over`): else the workgroup with
+  // the short sequences is the last to be done (64 ragged sequences up to 8192,
+  // codes: its run of 14 units took 85 us, the median 65).  With short runs the
+  // rounding of the runs would cost more.
+  int U, over, per, u0, u1, b, prefix, length;
+  auto runs = [&](int units) {
+    over = units >= 8 * a.groups ? 1 : 0;
+    U = units + over * rows * a.B;
+    per = (U + a.groups - 1) / a.groups;
+    u0 = (int)blockIdx.x * per;
+    u1 = min(U, u0 + per);
+  };
   if (a.B <= 64) {  // a sequence a lane, and no wave waits for another
     const int len = lane < a.B ? a.lengths[lane] : 0;
     const int mine = lane < a.B ? Span<UNIT>(a, len).units * rows : 0;
-    const int incl = sum_to_lane(mine);
-    U = __builtin_amdgcn_readlane(incl, 63);
-    per = (U + a.groups - 1) / a.groups;
-    u0 = (int)blockIdx.x * per;
+    int incl = sum_to_lane(mine);
+    runs(__builtin_amdgcn_readlane(incl, 63));
     if (u0 >= U) return;
+    incl += over * rows * (lane + 1);
     b = __builtin_popcountll(__ballot(incl <= u0));
-    prefix = __builtin_amdgcn_readlane(incl - mine, b);
+    prefix = __builtin_amdgcn_readlane(incl - mine, b) - over * rows;
     length = __builtin_amdgcn_readlane(len, b);
   } else {
     const int each = (a.B + 255) / 256;
@@ -283,14 +294,14 @@ __global__ void __launch_bounds__(256, DP > 128 ? 1 : 2) attend_kernel(AttendArg
       incl += w < wave ? scan[w] : 0;
       total += scan[w];
     }
-    U = __builtin_amdgcn_readfirstlane(total);
-    per = (U + a.groups - 1) / a.groups;
-    u0 = (int)blockIdx.x * per;
+    runs(__builtin_amdgcn_readfirstlane(total));
     if (u0 >= U) return;
+    incl += over * rows * min(a.B, (tid + 1) * each);
+    mine += over * rows * max(0, min(each, a.B - tid * each));
     if (incl - mine <= u0 && u0 < incl) {
       int p = incl - mine, x = tid * each;
       for (;; ++x) {
-        const int t = Span<UNIT>(a, a.lengths[x]).units * rows;
+        const int t = (Span<UNIT>(a, a.lengths[x]).units + over) * rows;
         if (u0 < p + t) break;
         p += t;
       }
@@ -302,22 +313,21 @@ __global__ void __launch_bounds__(256, DP > 128 ? 1 : 2) attend_kernel(AttendArg
     prefix = __builtin_amdgcn_readfirstlane(at_prefix);
     length = load_uniform(a.lengths + b);
   }
-  u1 = min(U, u0 + per);
 
-  // One head's part of the run: units [i0, i1) of the head's, which begin at
-  // unit `start` of all.
+  // One head's part of the run: units [i0, i1) of the head's, whose share of
+  // the runs begins at `start`.  The last of a run may have none.
   struct Segment {
     Span<UNIT> sp;
     int b, prefix, start, i0, i1, head, q0, G;
   };
   auto segment = [&](int u, int b, int prefix, Span<UNIT> sp) {
-    while (u >= prefix + sp.units * rows) {
-      prefix += sp.units * rows;
+    while (u >= prefix + (sp.units + over) * rows) {
+      prefix += (sp.units + over) * rows;
       sp = Span<UNIT>(a, load_uniform(a.lengths + ++b));
     }
-    const int r = (u - prefix) / sp.units, head = r / a.RG, h0 = (r - head * a.RG) * 16;
-    const int start = prefix + r * sp.units, i0 = u - start;
-    return Segment{sp, b, prefix, start, i0, min(sp.units, i0 + u1 - u), head, head * a.G + h0, min(16, a.G - h0)};
+    const int r = (u - prefix) / (sp.units + over), head = r / a.RG, h0 = (r - head * a.RG) * 16;
+    const int start = prefix + r * (sp.units + over), i0 = max(0, u - start - over);
+    return Segment{sp, b, prefix, start, i0, min(sp.units, u1 - start - over), head, head * a.G + h0, min(16, a.G - h0)};
   };
   Segment sg = segment(u0, b, prefix, Span<UNIT>(a, length));
   const int first_row = sg.start;
@@ -672,11 +682,12 @@ __global__ void __launch_bounds__(256, DP > 128 ? 1 : 2) attend_kernel(AttendArg
 
     // ---- the four waves' results, joined ----------------------------------------
     const Segment done = sg;
-    const int u = sg.start + sg.i1;
-    const bool more = u < u1;
+    const int u = sg.start + over + sg.i1;
+    bool more = u < u1;
     if (more) {
       sg = segment(u, sg.b, sg.prefix, sg.sp);
-      begin(sg, Flag<false>{});
+      more = sg.i0 < sg.i1;
+      if (more) begin(sg, Flag<false>{});
     }
     const int G = done.G;
     l = sum_groups(l);
@@ -697,10 +708,10 @@ __global__ void __launch_bounds__(256, DP > 128 ? 1 : 2) attend_kernel(AttendArg
     }
     __syncthreads();
     const bool alone = done.i0 == 0 && done.i1 == done.sp.units;
-    const int row_start = done.start;
+    const int row_start = done.start, token_start = row_start + over;
     // the head's workgroups, and where their parts of it are: a workgroup's
     // first head is in its first place, its last one, if another, in its second
-    const int wa = row_start / per, ns = (row_start + done.sp.units - 1) / per - wa + 1;
+    const int wa = token_start / per, ns = (token_start + done.sp.units - 1) / per - wa + 1;
     const uint32_t record = (uint32_t)attend_record(min(16, a.G), D) * 4;
     const __amdgpu_buffer_rsrc_t parts = __builtin_amdgcn_make_buffer_rsrc(
         a.part, (short)0, (int)(2 * kAttendGroups * record), kRsrcWord3);
@@ -757,7 +768,7 @@ __global__ void __launch_bounds__(256, DP > 128 ? 1 : 2) attend_kernel(AttendArg
         // a wave's four parts by lane exchange, the waves' in LDS).  Parts
         // behind the last read as zero, past the end of the buffer.
         const uint32_t at0 = (uint32_t)(2 * wa) * record;
-        const uint32_t extra = wa * per == row_start ? 0 : record;  // of part 0
+        const uint32_t extra = wa * per >= row_start ? 0 : record;  // of part 0
         const int row = tid & 15, sub = tid >> 4;
 #pragma unroll 1
         for (int e0 = 0; e0 < vecs; e0 += 256) {

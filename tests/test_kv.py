@@ -461,6 +461,32 @@ def test_one_long_sequence_among_short_ones(dtype, kind):
 
 
 @gpu
+@pytest.mark.parametrize("dtype,kind", [(torch.float32, torch.float32), (torch.float16, torch.float16),
+                                        (torch.bfloat16, torch.int8)], ids=str)
+@pytest.mark.parametrize("B", [40, 90])
+def test_long_runs(B, dtype, kind):
+    """Eight units and more a workgroup, where a head's own cost is counted: ragged sequences, many of them
+    short or empty, which share the same pages."""
+    require_gpu()
+    g = torch.Generator().manual_seed(B)
+    lengths = torch.randint(0, 200, (B,), generator=g)
+    lengths[::3] = torch.randint(1, 1500, (len(lengths[::3]),), generator=g)
+    lengths[B // 2] = 0
+    total = 8 * 512 * fg_step(kind) * 13 // 10 // 8     # tokens of that many units, at 8 heads, and some
+    lengths[1] = max(1, total - int(lengths.sum()))
+    top = int(lengths.max())
+    pages = -(-top // 64)
+    table = torch.randperm(pages, generator=g)[None, :].expand(B, -1)
+    kv = fill_cache(g, pages, 8, 64, 16, dtype, kind)
+    check(torch.randn(B, 16, 16, generator=g).to(dtype), kv, table.contiguous(), lengths)
+
+
+def fg_step(kind):
+    """Tokens of a workgroup's step."""
+    return {torch.int8: 256, torch.float32: 64}.get(kind, 128)
+
+
+@gpu
 @pytest.mark.parametrize("dtype,kind", [(torch.float32, torch.int8), (torch.bfloat16, torch.bfloat16)], ids=str)
 @pytest.mark.parametrize("B", [255, 256, 257, 1500])
 def test_many_sequences(B, dtype, kind):
