@@ -106,10 +106,11 @@ def attention(q, k, v, ks, vs, table, lengths, window, scale):
             err = err + 2.0 ** -28 * V.abs().sum(1, keepdim=True)
         if kind == torch.int8:
             row = V.abs().amax(-1)[:, None, :] / 127         # a code's step, or less
-            for x in tiles.unique():
-                m = tiles == x
-                step = ((w * row)[..., m].amax(-1, keepdim=True) * 1.02 + 2.0 ** -100) / TOP[digits]
-                err = err + step * (1.01 if digits == 3 else 0.52) * (V.abs()[:, m] / row[:, 0, m, None].clamp_min(1e-300)).sum(1)[:, None, :]
+            size = V.abs() / row[:, 0, :, None].clamp_min(1e-300)
+            for m in torch.split(torch.arange(len(t)), tiles.unique_consecutive(return_counts=True)[1].tolist()):
+                m = slice(int(m[0]), int(m[-1]) + 1)
+                step = ((w[..., m] * row[..., m]).amax(-1, keepdim=True) * 1.02 + 2.0 ** -100) / TOP[digits]
+                err = err + step * (1.01 if digits == 3 else 0.52) * size[:, m].sum(1)[:, None, :]
         o[b], lse[b] = out.reshape(Hq, D), l.reshape(Hq)
         bo[b] = (err + half_step(out.abs() + err, dtype)).reshape(Hq, D)
         bl[b] = (delta[..., 0] + (len(t) + 8) * U32 + 2.0 ** -21 + 8 * U32 * (l[..., 0].abs() + a[..., 0])).reshape(Hq)

@@ -481,6 +481,26 @@ def test_long_runs(B, dtype, kind):
     check(torch.randn(B, 16, 16, generator=g).to(dtype), kv, table.contiguous(), lengths)
 
 
+@gpu
+@pytest.mark.parametrize("dtype,kind", PAIRS, ids=str)
+@pytest.mark.parametrize("heads", ["begin runs of their own", "share workgroups"])
+def test_two_units_a_workgroup(heads, dtype, kind):
+    """Heads past 128 values have 256 workgroups: 222 units are too few for two each, 444 and 400 are not;
+    the latter in 200 heads of one unit and a long one, which leave no workgroup for a run of every head."""
+    require_gpu()
+    g = torch.Generator().manual_seed(7)
+    u = fg_step(kind)
+    if heads == "share workgroups":
+        lengths, Hk = torch.tensor([1] * 120 + [200 * u - 5] + [u] * 80), 1
+    else:
+        lengths, Hk = torch.tensor([141 * u, 78 * u + 1, 3 * u - 1]), 2
+    top = int(lengths.max())
+    pages = -(-top // 64)
+    table = torch.randperm(pages, generator=g)[None, :].expand(len(lengths), -1).contiguous()
+    kv = fill_cache(g, pages, Hk, 64, 144, dtype, kind)
+    check(torch.randn(len(lengths), Hk, 144, generator=g).to(dtype), kv, table, lengths)
+
+
 def fg_step(kind):
     """Tokens of a workgroup's step."""
     return {torch.int8: 256, torch.float32: 64}.get(kind, 128)
