@@ -34,6 +34,7 @@ struct KvRowArgs {
   const int *pos;
   const int *slots;       // with a cache
   KvCache cache;          // type < 0: none
+  bool past_caches;       // floats are stored past the caches
 };
 hipError_t launch_kv_rows(const KvRowArgs &a, int type, hipStream_t s);
 
@@ -44,6 +45,7 @@ struct KvReadArgs {
   KvCache cache;
   void *K, *V;
   int ldk, ldv;
+  bool past_caches;
 };
 hipError_t launch_kv_read(const KvReadArgs &a, int type, hipStream_t s);
 

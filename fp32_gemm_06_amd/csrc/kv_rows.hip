@@ -42,12 +42,19 @@ template <class T, bool WHOLE, class V> __device__ __forceinline__ void load4(co
     for (int e = 0; e < 4; ++e) v[e] = e < n ? (V)p[e] : (V)0.0f;
   }
 }
-template <class T, bool WHOLE> __device__ __forceinline__ void store4(T *p, int n, const float *v) {
+template <class T, bool WHOLE> __device__ __forceinline__ void store4(T *p, int n, const float *v, bool past_caches) {
   if (WHOLE || n == 4) {
     typename Four<T>::type c;
 #pragma unroll
     for (int e = 0; e < 4; ++e) c[e] = (T)v[e];
-    *reinterpret_cast<typename Four<T>::anywhere *>(p) = c;
+    typename Four<T>::anywhere *to = reinterpret_cast<typename Four<T>::anywhere *>(p);
+    if (past_caches) {
+      asm volatile("");  // (the compiler makes one plain store of the two, else)
+      __builtin_nontemporal_store(c, to);
+      asm volatile("");
+    } else {
+      *to = c;
+    }
   } else {
 #pragma unroll
     for (int e = 0; e < 4; ++e)
@@ -292,11 +299,17 @@ __global__ void __launch_bounds__(NT) kv_rows_kernel(KvRowArgs a, int steps) {
         y = static_cast<T *>(a.Yk) + (long long)t * a.ldyk + h * a.D;
       else
         y = static_cast<T *>(value ? a.cache.V : a.cache.K) + (row0 + (long long)h * a.cache.page_size) * a.D;
-      store4<T, WHOLE>(y + pa, n, f);
-      store4<T, WHOLE>(y + pb, n, f + 4);
+      store4<T, WHOLE>(y + pa, n, f, a.past_caches);
+      store4<T, WHOLE>(y + pb, n, f + 4, a.past_caches);
     }
   }
 }
+
+// Floats of this many bytes, as much as the XCDs' caches hold, are stored past
+// them: whatever reads them next finds them in memory anyway.  8192 tokens of
+// 32 + 8 heads of 128 bf16 39.7 -> 37.7 us, with codes for the cache 47.5 ->
+// 45.4.
+bool past_caches(long long values, int size) { return values * size >= 32 << 20; }
 
 // Lanes of a row: the power of two that holds its groups of four pairs.
 int lanes_of(const KvRowArgs &a) {
@@ -330,12 +343,14 @@ template <class T> hipError_t launch_type(const KvRowArgs &all, hipStream_t s) {
   const int RT = all.Hq + all.Hk + all.Hv;
   if (RT == 0) return hipSuccess;
   const int L = lanes_of(all);
+  const int floats = all.Hq + (all.cache.type == kTypeS8 ? 0 : all.Hk + all.Hv);
   const bool whole = all.style != 0 || all.R % 8 == 0;
   // a launch's threads stay below 2^31
   const int most = (1 << 24) / RT > 0 ? (1 << 24) / RT : 1;
   for (long long t0 = 0; t0 < all.T; t0 += most) {
     KvRowArgs a = all;
     a.T = (int)(all.T - t0 < most ? all.T - t0 : most);
+    a.past_caches = past_caches((long long)all.T * floats * all.D, sizeof(T));
     a.Q = static_cast<const T *>(all.Q) + t0 * all.ldq;
     a.K = static_cast<const T *>(all.K) + t0 * all.ldk;
     a.V = static_cast<const T *>(all.V) + t0 * all.ldv;
@@ -382,8 +397,18 @@ template <class T, int L, bool CODES> __global__ void __launch_bounds__(NT) kv_r
     load4<T, true>(static_cast<const T *>(src) + row * D + d, 4, f);
     load4<T, true>(static_cast<const T *>(src) + row * D + d + 4, 4, f + 4);
   }
-  store4<T, true>(y, 4, f);
-  store4<T, true>(y + 4, 4, f + 4);
+  typedef T eight __attribute__((ext_vector_type(8)));
+  typedef T anywhere __attribute__((ext_vector_type(8), aligned(alignof(T))));
+  eight v;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] = (T)f[e];
+  if (a.past_caches) {
+    asm volatile("");  // as in store4
+    __builtin_nontemporal_store(v, reinterpret_cast<anywhere *>(y));
+    asm volatile("");
+  } else {
+    *reinterpret_cast<anywhere *>(y) = v;
+  }
 }
 
 template <class T> hipError_t launch_read(const KvReadArgs &all, hipStream_t s) {
@@ -393,6 +418,7 @@ template <class T> hipError_t launch_read(const KvReadArgs &all, hipStream_t s) 
   for (long long t0 = 0; t0 < all.T; t0 += most) {
     KvReadArgs a = all;
     a.T = (int)(all.T - t0 < most ? all.T - t0 : most);
+    a.past_caches = past_caches((long long)all.T * rows * all.cache.dim, sizeof(T));
     a.slots = all.slots + t0;
     a.K = static_cast<T *>(all.K) + t0 * all.ldk;
     a.V = static_cast<T *>(all.V) + t0 * all.ldv;

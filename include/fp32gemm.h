@@ -483,7 +483,7 @@ int kv_read(int T, const int *slots, const fp32gemm_kv_cache *cache, int type,
  * O is B x Hq x dim of `type`.  Lengths below 0 count as 0, above ldt page_size
  * as that.  A table entry outside 0 .. pages - 1 is a page without tokens (one
  * that the window has left, or that was given up); entries of pages that no
- * seen token lies on are not looked at.  Where no token is left, or every score
+ * seen token lies on have no effect.  Where no token is left, or every score
  * is minus infinity, O is 0 and lse minus infinity.  Values of unseen tokens,
  * whatever they are, have no effect; a NaN or an infinity in the query, or in a
  * key's scale, or in a seen token's values shows in the outputs that depend on
