@@ -12,8 +12,9 @@
 // sequence among short ones is spread over all CUs.  The four waves take TOK
 // tokens each and keep their own maximum, sum and output until the run leaves
 // the head; then they are joined in LDS.  A head that several workgroups
-// share is joined by the last of them to arrive, in the order of its tokens
-// (partial results and arrival counter as in gemv_split.hip: agent-scope
+// share is joined in the order of its tokens by the last of them to arrive, or
+// in two or three steps, each by the last of its own parts' workgroups
+// (partial results and arrival counters as in gemv_split.hip: agent-scope
 // atomic stores and loads, a wait for the own stores before the counter, no
 // fences, no spinning).  The result depends on the lengths and the launch
 // alone.
@@ -41,6 +42,14 @@
 // Masked tokens get a score of minus infinity and weight 0 by selection; where
 // V is floats their values are selected away too, so whatever unwritten pages
 // hold does no harm.
+//
+// Long calls are bound by reading K and V once (counted: 1.01 times their bytes):
+// 64 ragged sequences up to 8192 tokens, 32 heads on 8 of 128, codes 82 us (5.5
+// TB/s; matrix cores and vector units each below a third), bf16 143 us (6.1 TB/s;
+// a kernel that only reads such pages 6.3-6.7).  Few rows are bound by latency:
+// one sequence of 4096 on codes 10.9 us, of which planning .8, the first bytes 2.2,
+// the tile 2.3, the waves' join and the stores 1.3, the counter .4, the join of
+// 16 parts 1.9 and the launch the rest.
 #pragma once
 
 #include "kv_common.h"
@@ -119,6 +128,7 @@ template <int DIG, int K> __device__ __forceinline__ floatx4 digit_product(const
 }
 
 template <bool V> struct Flag { static constexpr bool value = V; };
+template <int V> struct Number { static constexpr int value = V; };
 
 template <class T, bool S8> struct Kind;
 template <class T> struct Kind<T, true> {
@@ -245,7 +255,7 @@ __global__ void __launch_bounds__(256, DP > 128 ? 1 : 2) attend_kernel(AttendArg
   constexpr int KT = TOK * DP * ES;  // bytes of a tile
   __shared__ __attribute__((aligned(16))) char keys_of[4][KT];
   __shared__ __attribute__((aligned(16))) float merge[4][16 * PITCH];
-  __shared__ float wm[4][16], wl[4][16], part_f[17][16], total_of[16];
+  __shared__ float wm[4][16], wl[4][16], part_f[16][16];
   __shared__ int scan[4], at_prefix, at_seq, last;
 
   const int tid = threadIdx.x, lane = tid & 63;
@@ -263,7 +273,7 @@ __global__ void __launch_bounds__(256, DP > 128 ? 1 : 2) attend_kernel(AttendArg
   // A few units a workgroup: where there are workgroups enough for every head
   // to begin a run of its own (`whole`), its share is rounded up to whole runs,
   // and no workgroup has parts of two heads (16 windows of 4096, 16 heads of
-  // 256 fp16: 27.0 -> 24.8 us).
+  // 256 fp16: 27.0 -> 24.8 us, with all parts joined at once).
   int U, over, per, u0, u1, b, prefix, length;
   bool whole_runs = false;
   auto share = [&](int units) { return whole_runs ? (units + per - 1) / per * per : units + over; };
@@ -778,83 +788,112 @@ __global__ void __launch_bounds__(256, DP > 128 ? 1 : 2) attend_kernel(AttendArg
       }
     }
     if (!alone) {
-      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-      __syncthreads();
-      if (tid == 0)
-        last = __hip_atomic_fetch_add(&a.cnt[wa], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == (unsigned)(ns - 1);
-      __syncthreads();
-      if (last) {
-        asm volatile("" ::: "memory");
-        // 16 parts at a time: four outputs a thread of each, on the way while
-        // the parts' weights are found (thread: part tid / 16, head tid % 16;
-        // a wave's four parts by lane exchange, the waves' in LDS).  Parts
-        // behind the last read as zero, past the end of the buffer.
-        const uint32_t at0 = (uint32_t)(2 * wa) * record;
-        const uint32_t extra = wa * per >= row_start ? 0 : record;  // of part 0
+      // Joins `count` parts, `step` bytes apart from `from` (the first `extra`
+      // behind that), P of them at most: all outputs are on the way while the
+      // parts' weights are found (thread: part tid / 16, head tid % 16; a
+      // wave's four parts by lane exchange, the waves' in LDS).  Parts behind
+      // the last read as zero, past the end of the buffer.  The result goes out,
+      // or into the first part's place; where registers are short, in rounds of
+      // the outputs from e0, the maxima with the one that `ends`.
+      auto join = [&](auto most_parts, auto most_vecs, int e0, uint32_t from, uint32_t step, uint32_t extra,
+                      int count, bool out, bool ends) {
+        constexpr int P = decltype(most_parts)::value, OWN = decltype(most_vecs)::value;
         const int row = tid & 15, sub = tid >> 4;
-        // Where the registers allow, twice four outputs are on the way at once
-        // (16 windows of 4096, 16 heads of 256 fp16: 28.1 -> 26.6 us).
-        constexpr int OWN = DP > 128 ? 2 : 1;
-#pragma unroll 1
-        for (int e0 = tid; e0 - tid < vecs; e0 += 256 * OWN) {
-          floatx4 acc[OWN];
+        const bool in = row < G && sub < count;
+        const uint32_t p = from + sub * step + (sub == 0 ? extra : 0) + 16 * vecs + 4 * row;
+        float pm = load_through(parts, in ? p : kOob);
+        const float pl = load_through(parts, in ? p + 4 * G : kOob);
+        floatx4 v[OWN][P];
 #pragma unroll
-          for (int x = 0; x < OWN; ++x) acc[x] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
-          float top = kNegInf, all = 0.0f;  // of head `row`
-#pragma unroll 1
-          for (int w0 = 0; w0 < ns; w0 += 16) {
-            const uint32_t from = at0 + (uint32_t)(2 * w0) * record;
-            const bool in = row < G && w0 + sub < ns;
-            const uint32_t p = from + 2 * sub * record + (w0 + sub == 0 ? extra : 0) + 16 * vecs + 4 * row;
-            float pm = load_through(parts, in ? p : kOob);
-            const float pl = load_through(parts, in ? p + 4 * G : kOob);
-            floatx4 v[OWN][16];
+        for (int x = 0; x < OWN; ++x)
 #pragma unroll
-            for (int x = 0; x < OWN; ++x)
+          for (int w = 0; w < P; ++w)
+            v[x][w] = load_through4(parts, e0 + 256 * x < vecs && w < count
+                                               ? from + w * step + (w == 0 ? extra : 0) + 16 * (e0 + 256 * x)
+                                               : kOob);
+        pm = in ? pm : kNegInf;
+        const float wave_m = fmax_groups(pm);
+        if (g == 0) wm[wave][row] = wave_m;
+        __syncthreads();
+        float mm = wm[0][row];
 #pragma unroll
-              for (int w = 0; w < 16; ++w)
-                v[x][w] = load_through4(parts, e0 + 256 * x < vecs && w0 + w < ns
-                                                   ? from + 2 * w * record + (w0 + w == 0 ? extra : 0) + 16 * (e0 + 256 * x)
-                                                   : kOob);
-            pm = in ? pm : kNegInf;
-            const float wave_m = fmax_groups(pm);
-            if (g == 0) wm[wave][row] = wave_m;
-            __syncthreads();
-            float mm = top;
+        for (int w = 1; w < 4; ++w) mm = __builtin_fmaxf(mm, wm[w][row]);
+        const float f = weight_of(pm, pl, mm), wave_l = sum_groups(f * pl);
+        part_f[sub][row] = f;
+        if (g == 0) wl[wave][row] = wave_l;
+        __syncthreads();
+        auto total = [&](int row) { return (wl[0][row] + wl[1][row]) + (wl[2][row] + wl[3][row]); };
 #pragma unroll
-            for (int w = 0; w < 4; ++w) mm = __builtin_fmaxf(mm, wm[w][row]);
-            const float f = weight_of(pm, pl, mm), old = weight_of(top, all, mm);
-            const float wave_l = sum_groups(f * pl);
-            part_f[1 + sub][row] = f;
-            if (sub == 0) part_f[0][row] = old;
-            if (g == 0) wl[wave][row] = wave_l;
-            __syncthreads();
-            all = __builtin_fmaf(all, old, (wl[0][row] + wl[1][row]) + (wl[2][row] + wl[3][row]));
-            top = mm;
+        for (int x = 0; x < OWN; ++x) {
+          const int e = e0 + 256 * x, rr = min(4 * e / D, 15);
+          floatx4 acc = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-            for (int x = 0; x < OWN; ++x) {
-              const int rr = min(4 * (e0 + 256 * x) / D, 15);
-              acc[x] *= part_f[0][rr];
+          for (int w = 0; w < P; ++w)
 #pragma unroll
-              for (int w = 0; w < 16; ++w)
-#pragma unroll
-                for (int k = 0; k < 4; ++k) acc[x][k] = __builtin_fmaf(part_f[1 + w][rr], v[x][w][k], acc[x][k]);
-            }
-          }
-          if (sub == 0) {
-            total_of[row] = all;
-            if (row < G && e0 == tid) put_lse(row, top, all);
-          }
-          __syncthreads();
-#pragma unroll
-          for (int x = 0; x < OWN; ++x) {
-            const int e = e0 + 256 * x;
-            const float sum = total_of[min(4 * e / D, 15)];
-            if (e < vecs) put(e, sum == 0.0f ? floatx4{0.0f, 0.0f, 0.0f, 0.0f} : acc[x] / sum);
-          }
-          __syncthreads();
+            for (int k = 0; k < 4; ++k) acc[k] = __builtin_fmaf(part_f[w][rr], v[x][w][k], acc[k]);
+          if (e >= vecs) continue;
+          const float sum = total(rr);
+          if (!out)
+            store_through(acc, parts, from + extra + 16 * e);
+          else
+            put(e, sum == 0.0f ? floatx4{0.0f, 0.0f, 0.0f, 0.0f} : acc / sum);
         }
-        if (tid == 0) __hip_atomic_store(&a.cnt[wa], 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        if (sub == 0 && row < G && ends) {  // (nobody reads the maxima any more)
+          if (!out) {
+            store_through(mm, parts, p);
+            store_through(total(row), parts, p + 4 * G);
+          } else {
+            put_lse(row, mm, total(row));
+          }
+        }
+      };
+      // One CU reads parts at some 28 KB a us, 2 to 3 us at a time with the counter:
+      // as many at once as its registers take on the way, and for more parts two
+      // or three steps of as equal sizes as that allows.  Against the last to
+      // arrive reading all: 128 parts of 16 KB (32768 tokens, 16 heads x 256
+      // fp16) 76 -> 23 us, 128 of 8 KB 28.6 -> 16.9, 64 of 264 bytes 17.1 -> 11.8,
+      // 17 of 16 KB (16 windows of 4096) 24.7 -> 22.2; 16 parts of 2 KB as before.
+      const bool small = vecs <= 256;
+      const int most = small ? 16 : 8;
+      int F = ns;
+      if (ns > most) {
+        F = 2;
+        while (F * F < ns) ++F;
+        if (F > most) {
+          F = 2;
+          while (F * F * F < ns) ++F;
+        }
+      }
+      const uint32_t extra = wa * per >= row_start ? 0 : record;  // of part 0
+      // part `mine` of the head, of parts `apart` workgroups from each other
+      int mine = (int)blockIdx.x - wa, apart = 1, field = 0;
+      for (;;) {
+        const int first = mine / (F * apart) * (F * apart), all = (ns + apart - 1) / apart;
+        const int count = min(F, all - first / apart);
+        if (count > 1) {
+          asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+          __syncthreads();
+          if (tid == 0)
+            last = (__hip_atomic_fetch_add(&a.cnt[wa + first], 1u << field, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) >>
+                        field & 31) == (unsigned)(count - 1);
+          __syncthreads();
+          if (!__builtin_amdgcn_readfirstlane(last)) break;
+          asm volatile("" ::: "memory");
+          const uint32_t from = (uint32_t)(2 * (wa + first)) * record, step = (uint32_t)(2 * apart) * record;
+          const uint32_t late = first == 0 ? extra : 0;
+          if (small)
+            join(Number<16>(), Number<1>(), tid, from, step, late, count, all <= F, true);
+          else if constexpr (ES == 4 && DP > 128)  // (more are in the way of the next head's first tile)
+            for (int x = 0; x < vecs; x += 512)
+              join(Number<8>(), Number<2>(), tid + x, from, step, late, count, all <= F, x + 512 >= vecs);
+          else
+            join(Number<8>(), Number<DP / 64>(), tid, from, step, late, count, all <= F, true);
+          if (tid == 0)
+            __hip_atomic_fetch_sub(&a.cnt[wa + first], (unsigned)count << field, __ATOMIC_RELAXED,
+                                   __HIP_MEMORY_SCOPE_AGENT);
+        }
+        if (all <= F) break;
+        mine = first, apart *= F, field += 5;
       }
     }
     if (!more) break;

@@ -64,7 +64,7 @@ struct AttendArgs {
   void *O;
   int ldo;
   float *lse;             // NULL: not wanted
-  unsigned *cnt;          // an arrival counter for each workgroup, zero between calls
+  unsigned *cnt;          // for each workgroup three arrival counters of 5 bits, zero between calls
   float *part;            // two partial results for each workgroup
   int groups;             // workgroups of the launch
   uint32_t magic, shift;  // t / page_size = (t magic) >> shift for t < 2^31

