@@ -59,6 +59,7 @@ namespace {
 
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef u32x2 u32x2_words __attribute__((aligned(4)));
 
 constexpr float kNegInf = -__builtin_inff();
 constexpr int kScoreBias16 = 15;  // fp16 weights are kept times 2^15: their second numbers stay normal
@@ -238,17 +239,21 @@ template <int UNIT> struct Span {
 };
 
 // B16: a page holds whole blocks of 16 tokens, so a block's address is the
-// wave's; else every token has its own.  FULL: heads have DP values, not fewer.
-template <class T, bool S8, int DP, bool B16, bool FULL>
+// wave's; else every token has its own.  FULL: heads have DC values, not fewer.
+// DC is DP, a power of two, but for heads of 192, whose rows have the places of
+// 256 in LDS while queries, scores, V and outputs are done without the rest
+// (64 ragged to 8192, 20 heads on 4: codes 97 -> 79 us, fp32 268 -> 240).
+template <class T, bool S8, int DP, int DC, bool B16, bool FULL>
 __global__ void __launch_bounds__(256, DP > 128 ? 1 : 2) attend_kernel(AttendArgs a) {
   typedef Kind<T, S8> KD;
   constexpr int ES = KD::ES, TOK = KD::TOK, DIG = KD::DIG, QDIG = KD::QDIG, UNIT = 4 * TOK, BLK = TOK / 16;
-  constexpr int CPL = DP >= 128 ? 8 : 4;       // columns of V of a lane, next to each other
-  constexpr int HALVES = DP / (16 * CPL);      // of which there are 16 lanes
-  constexpr int KF = DP * ES / 64;             // 16-byte pieces of a token's K in a lane
+  // columns of V of a lane, next to each other
+  constexpr int CPL = DC != DP ? S8 ? 12 : 4 : DP >= 128 ? 8 : 4;
+  constexpr int HALVES = DC / (16 * CPL);      // of which there are 16 lanes
+  constexpr int KF = DC * ES / 64;             // 16-byte pieces of a token's K in a lane
   constexpr int VW = CPL * ES / 4;             // words of a token's V piece
-  constexpr int CP = 4 * KF;                   // 16-byte pieces of a row of K in LDS
-  constexpr int PITCH = DP + 4;                // of a head's outputs in LDS: 16 heads hit 64 banks
+  constexpr int CP = DP * ES / 16;             // 16-byte pieces of a row of K in LDS
+  constexpr int PITCH = DC + 4;                // of a head's outputs in LDS: 16 heads hit 64 banks
 
   // each wave's tile of K; the waves' outputs when they are joined, beside it,
   // since the next head's first tile is on its way by then
@@ -261,7 +266,7 @@ __global__ void __launch_bounds__(256, DP > 128 ? 1 : 2) attend_kernel(AttendArg
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int n = lane & 15, g = lane >> 4;
-  const int rows = a.Hk * a.RG, D = FULL ? DP : a.cache.dim, ps = a.cache.page_size;
+  const int rows = a.Hk * a.RG, D = FULL ? DC : a.cache.dim, ps = a.cache.page_size;
 
   // ---- this workgroup's run of units -----------------------------------------
   // (fewer than 2^31 units: checked by the caller)
@@ -406,10 +411,10 @@ __global__ void __launch_bounds__(256, DP > 128 ? 1 : 2) attend_kernel(AttendArg
   // ds_read_b128 takes in a cycle are in different banks.
   auto load_keys = [&](const Rows &w) {
 #pragma unroll
-    for (int i = 0; i < BLK * KF; ++i) {
-      const int row = (i * 64 + lane) / CP, blk = i / KF;  // of the tile
+    for (int i = 0; i < BLK * CP / 4; ++i) {
+      const int row = (i * 64 + lane) / CP, blk = i / (CP / 4);  // of the tile
       const uint32_t c = (lane % CP) ^ key_turn<CP>(row % 16);
-      const uint32_t at = FULL || 16 * c < (uint32_t)(D * ES) ? 16 * c : 0u;
+      const uint32_t at = (FULL && DC == DP) || 16 * c < (uint32_t)(D * ES) ? 16 * c : 0u;
       const char *keys = static_cast<const char *>(a.cache.K);
       if constexpr (B16)
         load_lds16(make_rsrc(keys + (uint64_t)w.base[blk] * (D * ES)), (row % 16) * (D * ES) + at, kt + i * 1024);
@@ -439,8 +444,15 @@ __global__ void __launch_bounds__(256, DP > 128 ? 1 : 2) attend_kernel(AttendArg
         else
           row = values + (uint64_t)(uint32_t)__shfl((int)w.own, 16 * blk + 4 * g + k, 64) * (D * ES);
 #pragma unroll
-        for (int hf = 0; hf < HALVES; ++hf)
-          vf[blk][k][hf] = __builtin_nontemporal_load(reinterpret_cast<const piece *>(row + col[hf]));
+        for (int hf = 0; hf < HALVES; ++hf) {
+          if constexpr (VW == 3) {  // (a vector of three is loaded as four, which would pass the cache's end)
+            const u32x2 two = __builtin_nontemporal_load(reinterpret_cast<const u32x2_words *>(row + col[hf]));
+            const uint32_t one = __builtin_nontemporal_load(reinterpret_cast<const uint32_t *>(row + col[hf]) + 2);
+            vf[blk][k][hf] = piece{two[0], two[1], one};
+          } else {
+            vf[blk][k][hf] = __builtin_nontemporal_load(reinterpret_cast<const piece *>(row + col[hf]));
+          }
+        }
       }
     }
     if constexpr (S8) vs = a.cache.scaleV[w.own];
@@ -853,7 +865,7 @@ __global__ void __launch_bounds__(256, DP > 128 ? 1 : 2) attend_kernel(AttendArg
       // arrive reading all: 128 parts of 16 KB (32768 tokens, 16 heads x 256
       // fp16) 76 -> 23 us, 128 of 8 KB 28.6 -> 16.9, 64 of 264 bytes 17.1 -> 11.8,
       // 17 of 16 KB (16 windows of 4096) 24.7 -> 22.2; 16 parts of 2 KB as before.
-      const bool small = vecs <= 256;
+      const bool small = DC <= 64 || vecs <= 256;
       const int most = small ? 16 : 8;
       int F = ns;
       if (ns > most) {
@@ -881,13 +893,15 @@ __global__ void __launch_bounds__(256, DP > 128 ? 1 : 2) attend_kernel(AttendArg
           asm volatile("" ::: "memory");
           const uint32_t from = (uint32_t)(2 * (wa + first)) * record, step = (uint32_t)(2 * apart) * record;
           const uint32_t late = first == 0 ? extra : 0;
+          // (fp32: more outputs at once are in the way of the next head's first tile)
+          constexpr int OWN = ES == 4 ? DP / 128 : DC / 64;
           if (small)
             join(Number<16>(), Number<1>(), tid, from, step, late, count, all <= F, true);
-          else if constexpr (ES == 4 && DP > 128)  // (more are in the way of the next head's first tile)
-            for (int x = 0; x < vecs; x += 512)
-              join(Number<8>(), Number<2>(), tid + x, from, step, late, count, all <= F, x + 512 >= vecs);
-          else
-            join(Number<8>(), Number<DP / 64>(), tid, from, step, late, count, all <= F, true);
+          else if constexpr (256 * OWN >= 4 * DC)
+            join(Number<8>(), Number<OWN>(), tid, from, step, late, count, all <= F, true);
+          else if constexpr (OWN > 0)
+            for (int x = 0; x < vecs; x += 256 * OWN)
+              join(Number<8>(), Number<OWN>(), tid + x, from, step, late, count, all <= F, x + 256 * OWN >= vecs);
           if (tid == 0)
             __hip_atomic_fetch_sub(&a.cnt[wa + first], (unsigned)count << field, __ATOMIC_RELAXED,
                                    __HIP_MEMORY_SCOPE_AGENT);
@@ -901,23 +915,24 @@ __global__ void __launch_bounds__(256, DP > 128 ? 1 : 2) attend_kernel(AttendArg
   }
 }
 
-template <class T, bool S8, int DP> hipError_t launch_attend_dim(const AttendArgs &all, hipStream_t s) {
+template <class T, bool S8, int DP, int DC = DP> hipError_t launch_attend_dim(const AttendArgs &all, hipStream_t s) {
   AttendArgs a = all;
   // two workgroups a CU, one where heads past 128 values take the registers of both
   if (DP > 128 && a.groups > 256) a.groups = 256;
   const bool blocks = a.cache.page_size % 16 == 0;
-  if (a.cache.dim == DP) {
-    if (blocks) attend_kernel<T, S8, DP, true, true><<<a.groups, 256, 0, s>>>(a);
-    else attend_kernel<T, S8, DP, false, true><<<a.groups, 256, 0, s>>>(a);
-  } else {
-    if (blocks) attend_kernel<T, S8, DP, true, false><<<a.groups, 256, 0, s>>>(a);
-    else attend_kernel<T, S8, DP, false, false><<<a.groups, 256, 0, s>>>(a);
+  if (a.cache.dim == DC) {
+    if (blocks) attend_kernel<T, S8, DP, DC, true, true><<<a.groups, 256, 0, s>>>(a);
+    else attend_kernel<T, S8, DP, DC, false, true><<<a.groups, 256, 0, s>>>(a);
+  } else if constexpr (DC == DP) {
+    if (blocks) attend_kernel<T, S8, DP, DP, true, false><<<a.groups, 256, 0, s>>>(a);
+    else attend_kernel<T, S8, DP, DP, false, false><<<a.groups, 256, 0, s>>>(a);
   }
   return hipGetLastError();
 }
 template <class T, bool S8> hipError_t launch_attend(const AttendArgs &a, hipStream_t s) {
   if (a.cache.dim <= 64) return launch_attend_dim<T, S8, 64>(a, s);
   if (a.cache.dim <= 128) return launch_attend_dim<T, S8, 128>(a, s);
+  if (a.cache.dim == 192) return launch_attend_dim<T, S8, 256, 192>(a, s);
   return launch_attend_dim<T, S8, 256>(a, s);
 }
 

@@ -390,7 +390,7 @@ PAIRS = [(d, k) for d in TYPES for k in (torch.int8, d)]
 @gpu
 @pytest.mark.parametrize("dtype,kind", PAIRS, ids=str)
 @pytest.mark.parametrize("Hk,G,D,ps", [(1, 1, 64, 16), (2, 4, 128, 64), (1, 3, 80, 24), (2, 17, 16, 1), (1, 16, 256, 16),
-                                       (3, 8, 96, 7), (1, 5, 192, 48)])
+                                       (3, 8, 96, 7), (1, 5, 192, 48), (2, 6, 192, 7), (1, 2, 176, 16)])
 def test_attention(Hk, G, D, ps, dtype, kind):
     """Ragged lengths around the tiles' edges, an empty sequence among them."""
     require_gpu()
