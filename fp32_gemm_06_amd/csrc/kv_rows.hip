@@ -25,6 +25,8 @@
 // 5.1 that a large copy reaches (61 us with a row a wave, which computed each
 // token's sines for every row); with the cache in codes 45-49 us.  Few rows are
 // bound by the launch and one trip to memory: one token 3.4 us.
+#include <initializer_list>
+
 #include "kv_common.h"
 
 namespace fp32gemm {
@@ -194,11 +196,15 @@ __global__ void __launch_bounds__(NT) kv_rows_kernel(KvRowArgs a, int steps) {
     pb = pa + hh;
     n = min(4, hh - 4 * cc);
   } else {
-    turns = 4 * c < half;
-    pa = 8 * c;
-    pb = pa + 4;
+    // two pairs of each half of the row, so that the lanes' stores lie next to
+    // each other (with four pairs in a run, 8192 tokens of 32 + 8 heads of 128
+    // fp32 took 77 us, past the caches 146; now 67, as halves do)
+    pa = 4 * c;
+    pb = a.D / 2 + 4 * c;
+    turns = 2 * c < half;  // pb's pairs are behind pa's
     n = 8 * c < a.D ? 4 : 0;
   }
+  auto pair = [&](int e) { return a.style == 0 ? 4 * c + e : (e < 2 ? pa : pb) / 2 + e % 2; };
   SinCos turn[4];
   if (half > 0 && s0 < sq + sk) {
     SinCos *mine = turns_of[wave];
@@ -207,8 +213,10 @@ __global__ void __launch_bounds__(NT) kv_rows_kernel(KvRowArgs a, int steps) {
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");  // the wave's own LDS is in order
     __builtin_amdgcn_wave_barrier();
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      turn[e] = turns && 4 * c + e < half ? mine[4 * c + e] : SinCos{0.0, 1.0};
+    for (int e = 0; e < 4; ++e) {
+      const int i = pair(e);
+      turn[e] = turns && i < half ? mine[i] : SinCos{0.0, 1.0};
+    }
   }
 
   // a step's row, asked for a step before it is used
@@ -268,7 +276,7 @@ __global__ void __launch_bounds__(NT) kv_rows_kernel(KvRowArgs a, int steps) {
         } else {
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            if (4 * c + e < half) rotate(v[2 * e], v[2 * e + 1], turn[e]);
+            if (pair(e) < half) rotate(v[2 * e], v[2 * e + 1], turn[e]);
         }
       }
 #pragma unroll
@@ -314,8 +322,22 @@ __global__ void __launch_bounds__(NT) kv_rows_kernel(KvRowArgs a, int steps) {
 // Floats of this many bytes, as much as the XCDs' caches hold, are stored past
 // them: whatever reads them next finds them in memory anyway.  8192 tokens of
 // 32 + 8 heads of 128 bf16 39.7 -> 37.7 us, with codes for the cache 47.5 ->
-// 45.4.
-bool past_caches(long long values, int size) { return values * size >= 32 << 20; }
+// 45.4; 4096 of fp32 40.4 -> 36.4.  But not where the two stores of a row, whose
+// runs end at `ends`, often share 64 bytes, which memory then gets in parts:
+// fp32, 64 values of which 16 turn 46.7 us with the caches and 61.6 past them (2
+// of a row's 4 pieces of 64 bytes), 128 of which 16 turn 42.2 and 46.5 (2 of 8),
+// 192 of which 16 turn 41.8 and 38.8 (2 of 12).  16-bit runs of other lengths do
+// no such harm, those of 64 bytes do (64 of 64 turn 40.9 and 43.6, 64 of 128
+// 40.3 and 44.7).
+bool past_caches(long long values, int size, int D, std::initializer_list<int> ends, bool aligned) {
+  if (values * size < 32 << 20) return false;
+  int first = 0, shared = 0;
+  for (int e : ends) {
+    if (first == 0) first = e;
+    if (!aligned || e * size % 64 != 0) ++shared;
+  }
+  return size == 2 ? first != 32 : 80 * (shared + !aligned) < D;
+}
 
 // Lanes of a row: the power of two that holds its groups of four pairs.
 int lanes_of(const KvRowArgs &a) {
@@ -351,12 +373,18 @@ template <class T> hipError_t launch_type(const KvRowArgs &all, hipStream_t s) {
   const int L = lanes_of(all);
   const int floats = all.Hq + (all.cache.type == kTypeS8 ? 0 : all.Hk + all.Hv);
   const bool whole = all.style != 0 || all.R % 8 == 0;
+  auto in64 = [](const void *p, int ld) { return ((uintptr_t)p | (uintptr_t)ld * sizeof(T)) % 64 == 0; };
+  const bool aligned = in64(all.Yq, all.ldyq) && in64(all.Yk, all.ldyk) &&
+                       (all.cache.type < 0 || (in64(all.cache.K, 0) && in64(all.cache.V, 0)));
+  const long long values = (long long)all.T * floats * all.D;
+  const bool past = all.style == 0 ? past_caches(values, sizeof(T), all.D, {all.R / 2, all.R, (all.D + all.R) / 2}, aligned)
+                                   : past_caches(values, sizeof(T), all.D, {all.D / 2}, aligned);
   // a launch's threads stay below 2^31
   const int most = (1 << 24) / RT > 0 ? (1 << 24) / RT : 1;
   for (long long t0 = 0; t0 < all.T; t0 += most) {
     KvRowArgs a = all;
     a.T = (int)(all.T - t0 < most ? all.T - t0 : most);
-    a.past_caches = past_caches((long long)all.T * floats * all.D, sizeof(T));
+    a.past_caches = past;
     a.Q = static_cast<const T *>(all.Q) + t0 * all.ldq;
     a.K = static_cast<const T *>(all.K) + t0 * all.ldk;
     a.V = static_cast<const T *>(all.V) + t0 * all.ldv;
@@ -383,39 +411,48 @@ template <class T> hipError_t launch_type(const KvRowArgs &all, hipStream_t s) {
 // heads of 128, codes to bf16, 11.2 us (4.6 TB/s).
 template <class T, int L, bool CODES> __global__ void __launch_bounds__(NT) kv_read_kernel(KvReadArgs a) {
   const int heads = a.cache.heads, D = a.cache.dim;
-  const int i = blockIdx.x * (NT / L) + (int)threadIdx.x / L, d = threadIdx.x % L * 8;
+  // eight values of 16 bits in a run, or twice four of 32, so that stores lie next to each other
+  constexpr bool kTwo = sizeof(T) == 4;
+  const int i = blockIdx.x * (NT / L) + (int)threadIdx.x / L, c = threadIdx.x % L;
+  const int d = c * (kTwo ? 4 : 8), d1 = kTwo ? D / 2 + d : d + 4;
   const int t = i / (2 * heads);
-  if (t >= a.T || d >= D) return;
+  if (t >= a.T || 8 * c >= D) return;
   const int h = i - t * 2 * heads;
   const bool value = h >= heads;
   const int head = value ? h - heads : h;
   const long long row = cache_row(a.cache, a.slots[t], head);
   if (row < 0) return;
   T *y = value ? static_cast<T *>(a.V) + (long long)t * a.ldv : static_cast<T *>(a.K) + (long long)t * a.ldk;
-  y += head * D + d;
+  y += head * D;
   const void *src = value ? a.cache.V : a.cache.K;
   float f[8];
   if constexpr (CODES) {
-    typedef int8_t codes __attribute__((ext_vector_type(8)));
-    const codes c = *reinterpret_cast<const codes *>(static_cast<const int8_t *>(src) + row * D + d);
+    typedef int8_t codes __attribute__((ext_vector_type(4)));
+    const int8_t *q = static_cast<const int8_t *>(src) + row * D;
+    const codes lo = *reinterpret_cast<const codes *>(q + d), hi = *reinterpret_cast<const codes *>(q + d1);
     const float scale = (value ? a.cache.scaleV : a.cache.scaleK)[row];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) f[e] = (float)c[e] * scale;
+    for (int e = 0; e < 4; ++e) f[e] = (float)lo[e] * scale, f[4 + e] = (float)hi[e] * scale;
   } else {
     load4<T, true>(static_cast<const T *>(src) + row * D + d, 4, f);
-    load4<T, true>(static_cast<const T *>(src) + row * D + d + 4, 4, f + 4);
+    load4<T, true>(static_cast<const T *>(src) + row * D + d1, 4, f + 4);
   }
-  typedef T eight __attribute__((ext_vector_type(8)));
-  typedef T anywhere __attribute__((ext_vector_type(8), aligned(alignof(T))));
-  eight v;
-#pragma unroll
-  for (int e = 0; e < 8; ++e) v[e] = (T)f[e];
-  if (a.past_caches) {
-    asm volatile("");  // as in store4
-    __builtin_nontemporal_store(v, reinterpret_cast<anywhere *>(y));
-    asm volatile("");
+  if constexpr (kTwo) {
+    store4<T, true>(y + d, 4, f, a.past_caches);
+    store4<T, true>(y + d1, 4, f + 4, a.past_caches);
   } else {
-    *reinterpret_cast<anywhere *>(y) = v;
+    typedef T eight __attribute__((ext_vector_type(8)));
+    typedef T anywhere __attribute__((ext_vector_type(8), aligned(alignof(T))));
+    eight v;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = (T)f[e];
+    if (a.past_caches) {
+      asm volatile("");  // as in store4
+      __builtin_nontemporal_store(v, reinterpret_cast<anywhere *>(y + d));
+      asm volatile("");
+    } else {
+      *reinterpret_cast<anywhere *>(y + d) = v;
+    }
   }
 }
 
@@ -423,10 +460,14 @@ template <class T> hipError_t launch_read(const KvReadArgs &all, hipStream_t s) 
   const int rows = 2 * all.cache.heads, lanes = all.cache.dim / 8;
   const int L = lanes <= 8 ? 8 : lanes <= 16 ? 16 : 32;
   const int most = (1 << 24) / rows > 0 ? (1 << 24) / rows : 1;
+  const int D = all.cache.dim;
+  const bool aligned =
+      ((uintptr_t)all.K | (uintptr_t)all.V | (uintptr_t)all.ldk * sizeof(T) | (uintptr_t)all.ldv * sizeof(T)) % 64 == 0;
+  const bool past = past_caches((long long)all.T * rows * D, sizeof(T), D, {sizeof(T) == 4 ? D / 2 : D}, aligned);
   for (long long t0 = 0; t0 < all.T; t0 += most) {
     KvReadArgs a = all;
     a.T = (int)(all.T - t0 < most ? all.T - t0 : most);
-    a.past_caches = past_caches((long long)all.T * rows * all.cache.dim, sizeof(T));
+    a.past_caches = past;
     a.slots = all.slots + t0;
     a.K = static_cast<T *>(all.K) + t0 * all.ldk;
     a.V = static_cast<T *>(all.V) + t0 * all.ldv;

@@ -318,6 +318,38 @@ def test_rows_that_are_not_finite_show():
 
 
 # ---- attention --------------------------------------------------------------------
+@gpu
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+@pytest.mark.parametrize("R,style", [(128, "halves"), (16, "halves"), (64, "halves"), (128, "pairs"), (40, "pairs")])
+def test_large_outputs_are_those_of_small_calls(R, style, dtype):
+    """From 32 MB on outputs take another way to memory; a token's result does not depend on it."""
+    require_gpu()
+    T = 2100 if dtype == torch.float32 else 4200
+    g = torch.Generator(device="cuda").manual_seed(R)
+    x = torch.randn(T, 42 * 128, generator=g, device="cuda").to(dtype)
+    q, k, v = (t.unflatten(1, (-1, 128)) for t in x.split([32 * 128, 5 * 128, 5 * 128], 1))
+    w = torch.randn(128, generator=g, device="cuda").to(dtype)
+    freq = torch.rand(R // 2, generator=g, device="cuda", dtype=torch.float64)
+    pos = torch.arange(T, device="cuda", dtype=torch.int32)
+    yq, yk = fg.norm_rope(q, k, pos, freq, w, None, style=style)
+    for t0 in range(0, T, 700):
+        s = slice(t0, t0 + 700)
+        a, b = fg.norm_rope(q[s], k[s], pos[s], freq, w, None, style=style)
+        assert torch.equal(yq[s], a) and torch.equal(yk[s], b)
+    heads = q[:, :30]
+    cache = fg.KVCache.empty(-(-T // 64), 64, 30, 128, dtype)
+    slots = torch.arange(T, device="cuda", dtype=torch.int32)
+    fg.cache_write(cache, heads, yq[:, :30], slots)
+    rk, rv = fg.cache_read(cache, slots)
+    assert torch.equal(rk, heads) and torch.equal(rv, yq[:, :30])
+    codes = fg.KVCache.empty(-(-T // 64), 64, 30, 128, torch.int8)
+    fg.cache_write(codes, heads, yq[:, :30], slots)
+    rk, rv = fg.cache_read(codes, slots, dtype)
+    for t0 in range(0, T, 700):
+        a, b = fg.cache_read(codes, slots[t0:t0 + 700], dtype)
+        assert torch.equal(rk[t0:t0 + 700], a) and torch.equal(rv[t0:t0 + 700], b)
+
+
 def fill_cache(g, pages, Hk, ps, D, dtype, kind, spread=1.0):
     """(k, v, k_scale, v_scale) on the CPU."""
     if kind != torch.int8:
