@@ -30,11 +30,11 @@
 //
 //  codes (s8): both products in integers.  The query's row, and each tile's
 //    weights times V's scales, become fixed-point numbers relative to their
-//    own largest, in signed 8-bit digits: three (23 bits) for the query, as
-//    the scores' sum is an fp32 result of its own; three for the weights of
-//    fp32 outputs, two (15 bits) for 16-bit ones, whose error of 2^-16 of a
-//    tile's largest weight is below a hundredth of the output's rounding.  No
-//    code of the cache is converted.
+//    own largest, in three signed 8-bit digits (23 bits).  Two digits, 15 bits,
+//    are too few for 16-bit outputs as well: a token whose scale is 512 times
+//    the others' leaves those 6 bits, an error of .5% in the columns where its
+//    own codes are small; with three it is 2^-15.  No code of the cache is
+//    converted.
 //  16-bit floats: products of the type, sums in fp32.  A weight goes in as two
 //    numbers of the type (its rounding and what that left), 16 bits or more.
 //  fp32: fp32 matrix instructions.
@@ -86,31 +86,28 @@ __device__ __forceinline__ float sum_groups(float v) {
   return over_groups(v, [](float a, float b) { return a + b; });
 }
 
-// Signed 8-bit digits of numbers in [-1, 1] times inv: the integer plus
-// 0x80 in every digit, whose bytes, 0x80 taken off again, are the digits.
-template <int DIG> struct Fixed {
-  static constexpr float top = DIG == 3 ? 8355000.0f : 32600.0f;
-  static constexpr float bias = DIG == 3 ? 8421504.0f : 32896.5f;  // above 2^23 the addition itself rounds
-};
-template <int DIG> __device__ __forceinline__ void digits4(const float (&v)[4], float inv, uint32_t (&w)[DIG]) {
+// Three signed 8-bit digits of v inv: the integer plus 0x80 in every digit,
+// whose bytes, 0x80 taken off again, are the digits.  A row's or tile's largest
+// becomes kTop.
+constexpr int kDigits = 3;
+constexpr float kTop = 8355000.0f;
+__device__ __forceinline__ void digits4(const float (&v)[4], float inv, uint32_t (&w)[kDigits]) {
   uint32_t u[4];
 #pragma unroll
-  for (int e = 0; e < 4; ++e) u[e] = (uint32_t)__builtin_fmaf(v[e], inv, Fixed<DIG>::bias);
+  for (int e = 0; e < 4; ++e) u[e] = (uint32_t)__builtin_fmaf(v[e], inv, 8421504.0f);  // above 2^23 the addition itself rounds
   const uint32_t t = __builtin_amdgcn_perm(u[1], u[0], 0x05010400u);
   const uint32_t s = __builtin_amdgcn_perm(u[3], u[2], 0x05010400u);
   w[0] = __builtin_amdgcn_perm(s, t, 0x05040100u) ^ 0x80808080u;
   w[1] = __builtin_amdgcn_perm(s, t, 0x07060302u) ^ 0x80808080u;
-  if constexpr (DIG == 3) {
-    const uint32_t t2 = __builtin_amdgcn_perm(u[1], u[0], 0x0c0c0602u);
-    const uint32_t s2 = __builtin_amdgcn_perm(u[3], u[2], 0x0c0c0602u);
-    w[2] = __builtin_amdgcn_perm(s2, t2, 0x05040100u) ^ 0x80808080u;
-  }
+  const uint32_t t2 = __builtin_amdgcn_perm(u[1], u[0], 0x0c0c0602u);
+  const uint32_t s2 = __builtin_amdgcn_perm(u[3], u[2], 0x0c0c0602u);
+  w[2] = __builtin_amdgcn_perm(s2, t2, 0x05040100u) ^ 0x80808080u;
 }
 
-// A product with fixed-point numbers: the digits' products one behind the other
-// in the same accumulator, moved up a digit in between (two digits stay below
+// A product with fixed-point numbers: two digits' products one behind the other
+// in the same accumulator, moved up a digit in between (they stay below
 // 2^31: 256 products of 127 and 128, or 64), the third beside it.
-template <int DIG, int K> __device__ __forceinline__ floatx4 digit_product(const u32x4 (&x)[K], const u32x4 *w) {
+template <int K> __device__ __forceinline__ floatx4 digit_product(const u32x4 (&x)[K], const u32x4 *w) {
   intx4 hi = {0, 0, 0, 0}, lo = {0, 0, 0, 0};
   auto add = [&](intx4 &acc, int digit) {
 #pragma unroll
@@ -118,13 +115,13 @@ template <int DIG, int K> __device__ __forceinline__ floatx4 digit_product(const
       acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(intx4, x[j]),
                                                   __builtin_bit_cast(intx4, w[digit * K + j]), acc, 0, 0, 0);
   };
-  add(hi, DIG - 1);
+  add(hi, 2);
   hi <<= 8;
-  add(hi, DIG - 2);
-  if constexpr (DIG == 3) add(lo, 0);
+  add(hi, 1);
+  add(lo, 0);
   floatx4 v;
 #pragma unroll
-  for (int r = 0; r < 4; ++r) v[r] = DIG == 3 ? __builtin_fmaf(256.0f, (float)hi[r], (float)lo[r]) : (float)hi[r];
+  for (int r = 0; r < 4; ++r) v[r] = __builtin_fmaf(256.0f, (float)hi[r], (float)lo[r]);
   return v;
 }
 
@@ -132,11 +129,9 @@ template <bool V> struct Flag { static constexpr bool value = V; };
 template <int V> struct Number { static constexpr int value = V; };
 
 template <class T, bool S8> struct Kind;
-template <class T> struct Kind<T, true> {
-  static constexpr int ES = 1, TOK = 64, DIG = sizeof(T) == 4 ? 3 : 2, QDIG = 3;
-};
-template <> struct Kind<float, false> { static constexpr int ES = 4, TOK = 16, DIG = 1, QDIG = 1; };
-template <class T> struct Kind<T, false> { static constexpr int ES = 2, TOK = 32, DIG = 2, QDIG = 1; };
+template <class T> struct Kind<T, true> { static constexpr int ES = 1, TOK = 64, QDIG = kDigits; };
+template <> struct Kind<float, false> { static constexpr int ES = 4, TOK = 16, QDIG = 1; };
+template <class T> struct Kind<T, false> { static constexpr int ES = 2, TOK = 32, QDIG = 1; };
 
 template <class T> __device__ __forceinline__ floatx4 mfma16(u32x4 a, u32x4 b, floatx4 c) {
   typedef T frag __attribute__((ext_vector_type(8)));
@@ -246,7 +241,7 @@ template <int UNIT> struct Span {
 template <class T, bool S8, int DP, int DC, bool B16, bool FULL>
 __global__ void __launch_bounds__(256, DP > 128 ? 1 : 2) attend_kernel(AttendArgs a) {
   typedef Kind<T, S8> KD;
-  constexpr int ES = KD::ES, TOK = KD::TOK, DIG = KD::DIG, QDIG = KD::QDIG, UNIT = 4 * TOK, BLK = TOK / 16;
+  constexpr int ES = KD::ES, TOK = KD::TOK, QDIG = KD::QDIG, UNIT = 4 * TOK, BLK = TOK / 16;
   // columns of V of a lane, next to each other
   constexpr int CPL = DC != DP ? S8 ? 12 : 4 : DP >= 128 ? 8 : 4;
   constexpr int HALVES = DC / (16 * CPL);      // of which there are 16 lanes
@@ -488,8 +483,8 @@ __global__ void __launch_bounds__(256, DP > 128 ? 1 : 2) attend_kernel(AttendArg
       top = nanmax_groups(top);
       // rows below 2^-64 are taken times 2^80, which keeps 1 / top finite
       const float lift = top < 0x1p-64f ? 0x1p80f : 1.0f;
-      const float inv = top > 0.0f ? Fixed<QDIG>::top / (top * lift) : 0.0f;
-      qscale *= top < __builtin_inff() ? top * (1.0f / Fixed<QDIG>::top) : __builtin_nanf("");  // shows in every score
+      const float inv = top > 0.0f ? kTop / (top * lift) : 0.0f;
+      qscale *= top < __builtin_inff() ? top * (1.0f / kTop) : __builtin_nanf("");  // shows in every score
 #pragma unroll
       for (int j = 0; j < KF; ++j) {
         const sixteen x = __builtin_bit_cast(sixteen, qr[j]);
@@ -498,7 +493,7 @@ __global__ void __launch_bounds__(256, DP > 128 ? 1 : 2) attend_kernel(AttendArg
           const float f[4] = {(float)x[4 * e] * lift, (float)x[4 * e + 1] * lift, (float)x[4 * e + 2] * lift,
                               (float)x[4 * e + 3] * lift};
           uint32_t w[QDIG];
-          digits4<QDIG>(f, inv, w);
+          digits4(f, inv, w);
 #pragma unroll
           for (int k = 0; k < QDIG; ++k) qf[k * KF + j][e] = w[k];
         }
@@ -557,7 +552,7 @@ __global__ void __launch_bounds__(256, DP > 128 ? 1 : 2) attend_kernel(AttendArg
           u32x4 kf[KF];
 #pragma unroll
           for (int j = 0; j < KF; ++j) kf[j] = key(blk, j);
-          const floatx4 v = digit_product<QDIG, KF>(kf, qf);
+          const floatx4 v = digit_product<KF>(kf, qf);
 #pragma unroll
           for (int k = 0; k < 4; ++k) s[blk][k] = v[k] * (__shfl(ks, 16 * blk + 4 * g + k, 64) * qscale);
         } else {
@@ -637,14 +632,14 @@ __global__ void __launch_bounds__(256, DP > 128 ? 1 : 2) attend_kernel(AttendArg
         big = nanmax_groups(big);
         // below 2^-100 the digits end at 2^-123; NaN and infinity go on into the outputs
         big = big < 0x1p-100f ? 0x1p-100f : big;
-        const float inv = Fixed<DIG>::top / big, factor = big * (1.0f / Fixed<DIG>::top);
-        u32x4 pd[DIG];
+        const float inv = kTop / big, factor = big * (1.0f / kTop);
+        u32x4 pd[kDigits];
 #pragma unroll
         for (int blk = 0; blk < BLK; ++blk) {
-          uint32_t w[DIG];
-          digits4<DIG>(p[blk], inv, w);
+          uint32_t w[kDigits];
+          digits4(p[blk], inv, w);
 #pragma unroll
-          for (int k = 0; k < DIG; ++k) pd[k][blk] = w[k];
+          for (int k = 0; k < kDigits; ++k) pd[k][blk] = w[k];
         }
 #pragma unroll
         for (int hf = 0; hf < HALVES; ++hf)
@@ -667,7 +662,7 @@ __global__ void __launch_bounds__(256, DP > 128 ? 1 : 2) attend_kernel(AttendArg
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
               const u32x4 one[1] = {col[c]};
-              const floatx4 v = digit_product<DIG, 1>(one, pd);
+              const floatx4 v = digit_product<1>(one, pd);
               floatx4 &out = o[hf * CPL + 4 * x + c];
 #pragma unroll
               for (int k = 0; k < 4; ++k) out[k] = __builtin_fmaf(factor, v[k], out[k]);

@@ -488,8 +488,8 @@ int kv_read(int T, const int *slots, const fp32gemm_kv_cache *cache, int type,
  * whatever they are, have no effect; a NaN or an infinity in the query, or in a
  * key's scale, or in a seen token's values shows in the outputs that depend on
  * it.  Sums are fp32; with codes the products are exact in integers of the
- * query's row, rounded to 23 bits of its largest, and of the weights, rounded
- * to 23 bits (fp32) or 15 (fp16, bf16) of theirs; weighted steps of V below
+ * query's row and of the weights times V's scales, each rounded to 23 bits of
+ * its largest (of the row, of up to 64 tokens); weighted steps of V below
  * 2^-100 lose digits there, and queries whose largest value times scale is.
  * The sum over the tokens is divided last: where values of V near fp32's largest
  * add up past it, O is infinite.
