@@ -86,15 +86,16 @@ __device__ __forceinline__ float sum_groups(float v) {
   return over_groups(v, [](float a, float b) { return a + b; });
 }
 
-// Three signed 8-bit digits of v inv: the integer plus 0x80 in every digit,
-// whose bytes, 0x80 taken off again, are the digits.  A row's or tile's largest
-// becomes kTop.
+// Three signed 8-bit digits of v inv, to the nearest integer: that plus 0x80 in
+// every digit, whose bytes, 0x80 taken off again, are the digits.  A row's or
+// tile's largest becomes kTop.  The integer is rounded by itself: below 2^23, so
+// for most negative numbers, the sum would have a half of its own to cut off.
 constexpr int kDigits = 3;
 constexpr float kTop = 8355000.0f;
 __device__ __forceinline__ void digits4(const float (&v)[4], float inv, uint32_t (&w)[kDigits]) {
   uint32_t u[4];
 #pragma unroll
-  for (int e = 0; e < 4; ++e) u[e] = (uint32_t)__builtin_fmaf(v[e], inv, 8421504.0f);  // above 2^23 the addition itself rounds
+  for (int e = 0; e < 4; ++e) u[e] = (uint32_t)(__builtin_rintf(v[e] * inv) + 8421504.0f);
   const uint32_t t = __builtin_amdgcn_perm(u[1], u[0], 0x05010400u);
   const uint32_t s = __builtin_amdgcn_perm(u[3], u[2], 0x05010400u);
   w[0] = __builtin_amdgcn_perm(s, t, 0x05040100u) ^ 0x80808080u;

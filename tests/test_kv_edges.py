@@ -38,3 +38,23 @@ def test_a_token_with_large_values_leaves_the_others_their_digits(D, ps, dtype):
     bound = bound + ref.half_step(want + bound, dtype)
     assert bool(((o[0].double() - want).abs() <= bound)[:, ::2].all()), float(((o[0].double() - want).abs() / bound)[:, ::2].max())
     assert bool(((o[0].double() - want).abs() <= bound).all())
+
+
+@gpu
+@pytest.mark.parametrize("at", [40000.3125, 39999.6875, 40000.4375, 300000.3125, 3000000.25])
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_query_values_are_rounded_to_the_nearest_step(at, sign):
+    """A query whose largest value is 8355000 steps of 2^-22, by which the others come out as fractions of a step.
+
+    The largest meets codes 0, so the score is the others' sum: off by half a step each, and 16 roundings of the
+    fp32 operations behind it.  One token's log-sum-exp is its score."""
+    require_gpu()
+    D, step = 64, 2.0 ** -22
+    q = torch.full((1, 1, D), sign * at * step)
+    q[0, 0, 0] = ref.TOP[3] * step
+    k = torch.full((1, 1, 16, D), 127, dtype=torch.int8)
+    k[..., 0] = 0
+    v, s = torch.zeros_like(k), torch.ones(1, 1, 16)
+    _, lse = attend(q, (k, v, s, s), torch.zeros(1, 1), torch.tensor([1]), scale=1.0)
+    want = sign * at * step * 127 * (D - 1)
+    assert abs(float(lse) - want) <= 127 * (D - 1) * step / 2 + 16 * ref.U32 * abs(want)
