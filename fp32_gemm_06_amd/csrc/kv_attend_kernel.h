@@ -164,6 +164,15 @@ __device__ __forceinline__ float load_through(__amdgpu_buffer_rsrc_t r, uint32_t
   return __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(r, at, 0, kThrough));
 }
 
+// Loads are issued on their side of this: a wait for all but the last N counts
+// on the order in which they were asked for, and the compiler, which sees no
+// dependence between loads into LDS and into registers, moves them past each
+// other (heads below 64 on odd pages had 3 of K's 4 loads behind half of V's).
+__device__ __forceinline__ void keep_order() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+}
+
 // Waits until all but the last N of the wave's memory accesses are done.
 template <int N> __device__ __forceinline__ void wait_loads() {
   static_assert(N <= 63, "six bits");
@@ -517,8 +526,11 @@ __global__ void __launch_bounds__(256, DP > 128 ? 1 : 2) attend_kernel(AttendArg
     load_query(sg);
     if (t0 < tend) {
       at = locate(sg, t0);
+      keep_order();
       load_keys(at);
+      keep_order();
       load_values(at);
+      keep_order();
       if constexpr (decltype(first)::value) turn_query();  // while they are on the way
     }
   };
@@ -541,7 +553,7 @@ __global__ void __launch_bounds__(256, DP > 128 ? 1 : 2) attend_kernel(AttendArg
       if constexpr (more) at = locate(sg, t0 + UNIT);
 
       // K's tile has landed when no more than V's loads, which were asked for
-      // behind it, are on the way.  (The compiler does not see what the loads
+      // behind it (keep_order), are on the way.  (The compiler does not see what the loads
       // into LDS write, so it need not wait for them by itself.)
       wait_loads<BLK * 4 * HALVES * ((VW + 3) / 4)>();
 
@@ -576,9 +588,9 @@ __global__ void __launch_bounds__(256, DP > 128 ? 1 : 2) attend_kernel(AttendArg
         }
       }
       asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // K's tile has been read
-      __builtin_amdgcn_sched_barrier(0);
+      keep_order();
       if constexpr (more) load_keys(at);
-      __builtin_amdgcn_sched_barrier(0);
+      keep_order();
       if (!whole) {
 #pragma unroll
         for (int blk = 0; blk < BLK; ++blk)
@@ -708,9 +720,9 @@ __global__ void __launch_bounds__(256, DP > 128 ? 1 : 2) attend_kernel(AttendArg
                     __builtin_bit_cast(float, (uint32_t)vf[0][k][hf][c]), p[0][k], o[hf * CPL + c], 0, 0, 0);
         }
       }
-      __builtin_amdgcn_sched_barrier(0);
+      keep_order();
       if constexpr (more) load_values(at);
-      __builtin_amdgcn_sched_barrier(0);
+      keep_order();
     };
     // The last tile asks for no other one.  It has code of its own: with a
     // branch around each of the two loads the compiler would wait for all of

@@ -1,8 +1,15 @@
 """Corners of the cache's operators: digits of the fixed-point products, bounds of a call's size, the order of
 loads that a kernel's waits count on, and values at the ends."""
+import os
+import re
+import shutil
+import struct
+import subprocess
+
 import pytest
 import torch
 
+import fp32_gemm_06_amd as fg
 import kv_reference as ref
 from gpu_util import require_gpu
 from test_kv import attend
@@ -58,3 +65,54 @@ def test_query_values_are_rounded_to_the_nearest_step(at, sign):
     _, lse = attend(q, (k, v, s, s), torch.zeros(1, 1), torch.tensor([1]), scale=1.0)
     want = sign * at * step * 127 * (D - 1)
     assert abs(float(lse) - want) <= 127 * (D - 1) * step / 2 + 16 * ref.U32 * abs(want)
+
+
+def attention_loads(tmp):
+    """{kernel: [order of the tile's loads between two branches]} of the built library's attention kernels: K for a
+    load of keys into LDS, V for one of values, which are those past the caches."""
+    objdump = shutil.which("llvm-objdump", path=os.pathsep.join(["/opt/rocm/llvm/bin", os.environ.get("PATH", "")]))
+    path = os.path.join(os.path.dirname(fg.__file__), "libfp32gemm.so")
+    if objdump is None or not os.path.exists(path):
+        pytest.skip("no llvm-objdump, or the library is not built")
+    with open(path, "rb") as f:
+        data = f.read()
+    found = {}
+    for m in re.finditer(b"__CLANG_OFFLOAD_BUNDLE__", data):
+        at = m.start() + 24
+        count, = struct.unpack_from("<Q", data, at)
+        at += 8
+        for _ in range(count):
+            offset, size, name = struct.unpack_from("<QQQ", data, at)
+            image = data[m.start() + offset:m.start() + offset + size]
+            at += 24 + name
+            if b"attend_kernel" not in image:
+                continue
+            (tmp / "image").write_bytes(image)
+            text = subprocess.run([objdump, "-d", "--no-show-raw-insn", str(tmp / "image")], capture_output=True, text=True,
+                                  check=True).stdout
+            for kernel, body in re.findall(r"<(\w*attend_kernel\w*)>:\n(.*?)(?=\n\n|\Z)", text, re.S):
+                runs = [""]
+                for line in body.splitlines():
+                    op = line.split("//")[0].split()
+                    if not op:
+                        continue
+                    if re.match(r"s_(cbranch|branch|endpgm|setpc)", op[0]):
+                        runs.append("")
+                    elif "_load_lds_" in op[0] or "_load_" in op[0] and "lds" in op:
+                        runs[-1] += "K"
+                    elif op[0].startswith("global_load") and "nt" in op:
+                        runs[-1] += "V"
+                found[kernel] = [r for r in runs if r]
+    return found
+
+
+def test_a_tile_s_keys_are_asked_for_before_its_values(tmp_path):
+    """The wait for a tile's keys lets as many loads be on the way as its values have, so all of those have to be
+    asked for behind all of these, in every kernel and wherever a tile is asked for."""
+    found = attention_loads(tmp_path)
+    assert len(found) == 84
+    for kernel, runs in found.items():
+        assert any("K" in r for r in runs) and any("V" in r for r in runs), kernel
+        assert all(re.fullmatch("K*V*", r) for r in runs), (kernel, runs)
+        values = {r.count("V") for r in runs if "V" in r}
+        assert len(values) == 1, (kernel, runs)
