@@ -666,9 +666,10 @@ int kv_attention(int B, int type, int Hq, const void *Q, int ldq, const fp32gemm
   const int G = Hq / c.heads, RG = (G + 15) / 16;
   const int tokens = c.pages > 0 ? ldt * c.page_size : 0;
   // more than any sequence can need: its tokens start up to 63 into a step, and
-  // a head may count for one more
+  // a head may count for one more; rounded up to whole runs of all workgroups
+  // the count stays below 2^31 too
   const double units = (double)B * c.heads * RG * (tokens / attend_step(c.type) + 3);
-  if (units >= 2147483647.0) return -8;
+  if (units >= 2147483648.0 - 2 * kAttendGroups) return -8;
   if (B > 0 && (lengths == nullptr || misaligned(lengths, 4))) return -9;
   if (window < 0) return -10;
   if (!(scale >= -0x1p127f && scale <= 0x1p127f)) return -11;

@@ -274,7 +274,7 @@ __global__ void __launch_bounds__(256, DP > 128 ? 1 : 2) attend_kernel(AttendArg
   const int rows = a.Hk * a.RG, D = FULL ? DC : a.cache.dim, ps = a.cache.page_size;
 
   // ---- this workgroup's run of units -----------------------------------------
-  // (fewer than 2^31 units: checked by the caller)
+  // (fewer than 2^31 units, rounded up to whole runs: checked by the caller)
   // With long runs a head's beginning and end, which cost what a unit does, are
   // counted as one more in front of its own (`over`): else the workgroup with
   // the short sequences is the last to be done (64 ragged sequences up to 8192,

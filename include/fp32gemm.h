@@ -504,11 +504,12 @@ int kv_read(int T, const int *slots, const fp32gemm_kv_cache *cache, int type,
  * It must not be used by another call, nor by two graphs' replays at once,
  * until this one has completed.
  *
- * ldt page_size <= 2^30, and B times the key heads times the table's length in
- * steps of 64 to 256 tokens < 2^31 (ldt is at fault otherwise).  Argument
- * positions for error codes: B 1, type 2, Hq 3, Q 4, ldq 5, cache 6, table 7,
- * ldt 8, lengths 9, window 10, scale 11 (NaN, or past 2^127), O 12, ldo 13, lse 14,
- * workspace 15, workspace_bytes 16, stream 17.
+ * ldt page_size <= 2^30, and B times the key heads (each counted once for
+ * every 16 of its query heads) times the table's length in steps (of 256 tokens
+ * for codes, 128 for 16 bits, 64 for fp32) plus 3 < 2^31 - 1024 (ldt is at fault
+ * otherwise).  Argument positions for error codes: B 1, type 2, Hq 3, Q 4,
+ * ldq 5, cache 6, table 7, ldt 8, lengths 9, window 10, scale 11 (NaN, or past
+ * 2^127), O 12, ldo 13, lse 14, workspace 15, workspace_bytes 16, stream 17.
  */
 int kv_attention(int B, int type, int Hq, const void *Q, int ldq,
                  const fp32gemm_kv_cache *cache, const int *table, int ldt,

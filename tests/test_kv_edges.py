@@ -12,7 +12,7 @@ import torch
 import fp32_gemm_06_amd as fg
 import kv_reference as ref
 from gpu_util import require_gpu
-from test_kv import attend
+from test_kv import ATTEND, attend, cache_struct, refused
 
 gpu = pytest.mark.gpu
 TYPES = list(ref.TYPES.values())
@@ -116,3 +116,19 @@ def test_a_tile_s_keys_are_asked_for_before_its_values(tmp_path):
         assert all(re.fullmatch("K*V*", r) for r in runs), (kernel, runs)
         values = {r.count("V") for r in runs if "V" in r}
         assert len(values) == 1, (kernel, runs)
+
+
+@pytest.mark.parametrize("type,step,heads,Hq,B", [(fg.TYPE_F32, 64, 4, 4, 32), (fg.TYPE_F32, 64, 1, 2, 128),
+                                                  (fg.TYPE_BF16, 128, 1, 17, 200), (fg.TYPE_S8, 256, 8, 8, 90)])
+def test_a_call_whose_runs_pass_32_bits_is_refused(type, step, heads, Hq, B):
+    """The count of all units is rounded up to whole runs in 32 bits, which leaves it 2^31 - 1024.  The longest
+    table below that is taken, which the next argument's refusal shows; one more page is not."""
+    groups = -(-Hq // heads // 16)
+    steps = (2 ** 31 - 1024 - 1) // (B * heads * groups) - 3        # of a table, the most
+    pages = steps * step // 64                                      # of 64 tokens
+    assert (pages + step // 64) * 64 <= 2 ** 30
+    c = cache_struct(type=type, heads=heads, page_size=64)
+    floats = type if type != fg.TYPE_S8 else fg.TYPE_F32
+    kw = dict(type=floats, Hq=Hq, ldq=4096, ldo=4096, B=B, cache=c, lengths=0)
+    for ldt, code in ((pages, -9), (pages + step // 64, -8)):
+        refused(fg.kv_attention, ATTEND, dict(kw, ldt=ldt), code)
