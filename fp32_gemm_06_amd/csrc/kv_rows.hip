@@ -144,15 +144,17 @@ template <int L, class V> __device__ __forceinline__ V over_row(V v) {
   return v;
 }
 
-// 1 / sqrt(x): the hardware's estimate (23 bits) and two Newton steps.
+// 1 / sqrt(x): the hardware's estimate (23 bits) and two Newton steps; of
+// infinity the estimate itself, 0, where a step would make a NaN.
 __device__ __forceinline__ double rsqrt64(double x) {
-  double y = __builtin_amdgcn_rsq(x);
+  const double estimate = __builtin_amdgcn_rsq(x);
+  double y = estimate;
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const double h = 0.5 * y;
     y = __builtin_fma(h, __builtin_fma(-x * y, y, 1.0), y);
   }
-  return y;
+  return x < __builtin_inf() ? y : estimate;
 }
 
 // Where a slot's row starts, in rows; -1 for slots outside the cache.

@@ -132,3 +132,27 @@ def test_a_call_whose_runs_pass_32_bits_is_refused(type, step, heads, Hq, B):
     kw = dict(type=floats, Hq=Hq, ldq=4096, ldo=4096, B=B, cache=c, lengths=0)
     for ldt, code in ((pages, -9), (pages + step // 64, -8)):
         refused(fg.kv_attention, ATTEND, dict(kw, ldt=ldt), code)
+
+
+@gpu
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+@pytest.mark.parametrize("style", ["halves", "pairs"])
+def test_an_infinity_under_the_norm_leaves_zeros_beside_it(style, dtype):
+    """x / sqrt(mean x^2 + eps) of a row with an infinity is NaN there and 0 elsewhere; a rotation spreads the NaN to
+    the other value of its pair.  A row with a NaN is NaN throughout."""
+    require_gpu()
+    D, R = 80, 32
+    x = torch.randn(3, 4, D, generator=torch.Generator().manual_seed(2)).to(dtype)
+    x[0, 1, 6], x[1, 2, 70], x[2, 0, 50] = float("inf"), float("-inf"), float("nan")
+    pos, freq = torch.arange(3).int(), 10000.0 ** (-torch.arange(R // 2, dtype=torch.float64) / 16)
+    w = torch.full((D,), 1.5, dtype=dtype)
+    y, _ = fg.norm_rope(x.cuda(), None, pos.cuda(), freq.cuda(), w.cuda(), style=style)
+    want = torch.zeros(3, 4, D, dtype=torch.bool)
+    want[0, 1, [6, 7 if style == "pairs" else 22]] = True
+    want[1, 2, 70] = want[2, 0] = True
+    y = y.cpu()
+    assert torch.equal(torch.isnan(y), want)
+    assert bool((y[0, 1] == 0)[~want[0, 1]].all()) and bool((y[1, 2] == 0)[~want[1, 2]].all())
+    clean, bound, _ = ref.norm_rope(x, w, 1e-6, pos, freq, style == "pairs")
+    rows = torch.isfinite(x).all(-1)
+    assert bool(((y.double() - clean).abs() <= bound)[rows].all())
