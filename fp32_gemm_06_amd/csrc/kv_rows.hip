@@ -321,24 +321,50 @@ __global__ void __launch_bounds__(NT) kv_rows_kernel(KvRowArgs a, int steps) {
   }
 }
 
+// Whether the halves of 128-byte lines come from different stores in half of a
+// row's lines or more.  A row of 16-bit values is written by two stores, whose
+// runs, which end at `ends`, take turns.
+bool halved_lines(int D, std::initializer_list<int> ends) {
+  if (2 * D % 128 != 0) return false;
+  int halved = 0;
+  for (int line = 0; line < 2 * D; line += 128) {
+    int turn[2] = {0, 0};
+    bool whole = true;
+    for (int half = 0; half < 2; ++half)
+      for (int e : ends) {
+        const int past = 2 * e - (line + 64 * half);
+        if (past <= 0) turn[half] ^= 1;
+        if (past > 0 && past < 64) whole = false;
+      }
+    halved += whole && turn[0] != turn[1];
+  }
+  return 4 * 64 * halved >= 2 * D;
+}
+
 // Floats of this many bytes, as much as the XCDs' caches hold, are stored past
 // them: whatever reads them next finds them in memory anyway.  8192 tokens of
 // 32 + 8 heads of 128 bf16 39.7 -> 37.7 us, with codes for the cache 47.5 ->
-// 45.4; 4096 of fp32 40.4 -> 36.4.  But not where the two stores of a row, whose
-// runs end at `ends`, often share 64 bytes, which memory then gets in parts:
-// fp32, 64 values of which 16 turn 46.7 us with the caches and 61.6 past them (2
-// of a row's 4 pieces of 64 bytes), 128 of which 16 turn 42.2 and 46.5 (2 of 8),
-// 192 of which 16 turn 41.8 and 38.8 (2 of 12).  16-bit runs of other lengths do
-// no such harm, those of 64 bytes do (64 of 64 turn 40.9 and 43.6, 64 of 128
-// 40.3 and 44.7).
-bool past_caches(long long values, int size, int D, std::initializer_list<int> ends, bool aligned) {
+// 45.4; 4096 of fp32 40.4 -> 36.4.  But not where that writes to memory in parts:
+//
+//  fp32, where the two stores of a row, whose runs end at `ends`, often share 64
+//    bytes: 64 values of which 16 turn 46.7 us with the caches and 61.6 past them
+//    (2 of a row's 4 pieces of 64 bytes), 128 of which 16 turn 42.2 and 46.5 (2
+//    of 8), 192 of which 16 turn 41.8 and 38.8 (2 of 12).
+//  16 bits, where lines are halved, from 75 MB on, with rows next to each other
+//    (bf16, 32 + 8 heads, with the caches and past them, us): 64 of 128 turn, 36
+//    MB 18.0 and 16.8, 72 MB 33.8 and 31.0, 84 MB 39.1 and 42.5, 120 MB 52.2 and
+//    53.1, 250 MB equal; 64 of 64 in pairs at 84 MB 39.9 and 42.9, 64 of 256 (2 of
+//    4 lines) 39.0 and 40.3, 64 of 192 (1 of 3) 46.8 and 46.0.  46 other layouts of
+//    16 to 256 values, and rows from any address, are 3% slower to 15% faster past
+//    the caches, all of them 7% and more at 60 MB; the rows of a cache 5% slower to
+//    14% faster, what is read from one 11 to 39% faster.
+bool past_caches(long long values, int size, int D, std::initializer_list<int> ends, bool aligned, bool next_to_each_other) {
   if (values * size < 32 << 20) return false;
-  int first = 0, shared = 0;
-  for (int e : ends) {
-    if (first == 0) first = e;
+  if (size == 2) return !(next_to_each_other && aligned && values * size >= 75 << 20 && halved_lines(D, ends));
+  int shared = 0;
+  for (int e : ends)
     if (!aligned || e * size % 64 != 0) ++shared;
-  }
-  return size == 2 ? first != 32 : 80 * (shared + !aligned) < D;
+  return 80 * (shared + !aligned) < D;
 }
 
 // Lanes of a row: the power of two that holds its groups of four pairs.
@@ -379,8 +405,10 @@ template <class T> hipError_t launch_type(const KvRowArgs &all, hipStream_t s) {
   const bool aligned = in64(all.Yq, all.ldyq) && in64(all.Yk, all.ldyk) &&
                        (all.cache.type < 0 || (in64(all.cache.K, 0) && in64(all.cache.V, 0)));
   const long long values = (long long)all.T * floats * all.D;
-  const bool past = all.style == 0 ? past_caches(values, sizeof(T), all.D, {all.R / 2, all.R, (all.D + all.R) / 2}, aligned)
-                                   : past_caches(values, sizeof(T), all.D, {all.D / 2}, aligned);
+  const bool rows = all.Hq > 0 || all.cache.type < 0;  // next to each other, not only those of a cache
+  const bool past = all.style == 0
+                        ? past_caches(values, sizeof(T), all.D, {all.R / 2, all.R, (all.D + all.R) / 2}, aligned, rows)
+                        : past_caches(values, sizeof(T), all.D, {all.D / 2}, aligned, rows);
   // a launch's threads stay below 2^31
   const int most = (1 << 24) / RT > 0 ? (1 << 24) / RT : 1;
   for (long long t0 = 0; t0 < all.T; t0 += most) {
@@ -465,7 +493,7 @@ template <class T> hipError_t launch_read(const KvReadArgs &all, hipStream_t s) 
   const int D = all.cache.dim;
   const bool aligned =
       ((uintptr_t)all.K | (uintptr_t)all.V | (uintptr_t)all.ldk * sizeof(T) | (uintptr_t)all.ldv * sizeof(T)) % 64 == 0;
-  const bool past = past_caches((long long)all.T * rows * D, sizeof(T), D, {sizeof(T) == 4 ? D / 2 : D}, aligned);
+  const bool past = past_caches((long long)all.T * rows * D, sizeof(T), D, {sizeof(T) == 4 ? D / 2 : D}, aligned, true);
   for (long long t0 = 0; t0 < all.T; t0 += most) {
     KvReadArgs a = all;
     a.T = (int)(all.T - t0 < most ? all.T - t0 : most);

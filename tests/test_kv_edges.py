@@ -156,3 +156,30 @@ def test_an_infinity_under_the_norm_leaves_zeros_beside_it(style, dtype):
     clean, bound, _ = ref.norm_rope(x, w, 1e-6, pos, freq, style == "pairs")
     rows = torch.isfinite(x).all(-1)
     assert bool(((y.double() - clean).abs() <= bound)[rows].all())
+
+
+@gpu
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+@pytest.mark.parametrize("D,R,style", [(128, 128, "halves"), (128, 64, "halves"), (64, 64, "pairs"), (256, 64, "halves"),
+                                       (80, 20, "halves")])
+def test_a_large_prompt_into_a_float_cache_is_that_of_small_calls(D, R, style, dtype):
+    """From 32 and from 75 MB of outputs on, rows take one or another way to memory, by their layout; a token's
+    queries, and its rows of the cache, do not depend on it."""
+    require_gpu()
+    for mb in (40, 88):
+        Hq, Hk = 2048 // D, 512 // D or 1
+        T = int(mb * 2 ** 20 / ((Hq + 2 * Hk) * D * dtype.itemsize))
+        g = torch.Generator(device="cuda").manual_seed(R)
+        x = torch.randn(T, Hq + 2 * Hk, D, generator=g, device="cuda").to(dtype)
+        q, k, v = x.split([Hq, Hk, Hk], 1)
+        w = torch.randn(D, generator=g, device="cuda").to(dtype)
+        freq = torch.rand(R // 2, generator=g, device="cuda", dtype=torch.float64)
+        pos = torch.arange(T, device="cuda", dtype=torch.int32)
+        slots = torch.randperm(T + 100, generator=g, device="cuda")[:T].int()
+        a, b = (fg.KVCache.empty(-(-(T + 100) // 16), 16, Hk, D, dtype) for _ in range(2))
+        y = fg.rope_write(a, q, k, v, slots, pos, freq, w, w, style=style)
+        for t0 in range(0, T, 2500):
+            s = slice(t0, t0 + 2500)
+            z = fg.rope_write(b, q[s], k[s], v[s], slots[s], pos[s], freq, w, w, style=style)
+            assert torch.equal(y[s], z)
+        assert torch.equal(a.k, b.k) and torch.equal(a.v, b.v)
