@@ -956,8 +956,8 @@ def attention(q, cache, table, lengths, scale=None, window=0, out=None, lse=None
 
     ``table`` (int32, sequences x pages) holds the pages that a sequence's
     tokens lie on, ``lengths`` (int32) how many tokens it has, the new one
-    among them.  ``scale`` is 1 / sqrt(head size) by default; with ``window``
-    the last so many tokens are seen.  ``lse`` (float32, sequences x heads)
+    among them.  ``scale`` is 1 / sqrt(head size) by default; with ``window``, a
+    whole number, the last so many tokens are seen (0: all).  ``lse`` (float32, sequences x heads)
     receives the scores' log-sum-exp.  ``workspace`` comes from
     attention_workspace; without one the call makes its own and clears it.
     """
@@ -984,6 +984,9 @@ def attention(q, cache, table, lengths, scale=None, window=0, out=None, lse=None
         raise ValueError("workspace must come from attention_workspace")
     device = _one_device(("q", q), ("the cache", cache.k), ("table", table), ("lengths", lengths), ("out", out),
                          ("lse", lse), ("workspace", workspace))
+    if int(window) != window:
+        raise ValueError("window must be a whole number")
+    window = max(-1, min(int(window), 0x7fffffff))  # the entry takes 32 bits, more than any table has tokens
     given = (out, lse)
     with _On(device, stream) as s:
         if out is None:
@@ -991,7 +994,7 @@ def attention(q, cache, table, lengths, scale=None, window=0, out=None, lse=None
         ldo = _heads(out, "out", q.dtype, q.shape)
         if workspace is None:
             workspace = attention_workspace(cache, Hq)
-        rc = kv_attention(B, type, Hq, q, ldq, cache, table, ldt, lengths, int(window),
+        rc = kv_attention(B, type, Hq, q, ldq, cache, table, ldt, lengths, window,
                           float(cache.dim ** -0.5 if scale is None else scale), out, ldo, lse, workspace,
                           workspace.numel(), s)
     if rc != 0:

@@ -183,3 +183,22 @@ def test_a_large_prompt_into_a_float_cache_is_that_of_small_calls(D, R, style, d
             z = fg.rope_write(b, q[s], k[s], v[s], slots[s], pos[s], freq, w, w, style=style)
             assert torch.equal(y[s], z)
         assert torch.equal(a.k, b.k) and torch.equal(a.v, b.v)
+
+
+@gpu
+def test_a_window_of_any_size():
+    """A window longer than the sequence, also one past 32 bits, is no window; others that are none are refused."""
+    require_gpu()
+    g = torch.Generator(device="cuda").manual_seed(3)
+    cache = fg.KVCache(*(torch.randn(4, 2, 16, 32, generator=g, device="cuda") for _ in range(2)))
+    q = torch.randn(1, 4, 32, generator=g, device="cuda")
+    table, n = torch.arange(4, device="cuda").int()[None].contiguous(), torch.tensor([50], device="cuda").int()
+    want = fg.attention(q, cache, table, n)
+    for window in (50, 64, 50.0, 2 ** 31 - 1, 2 ** 31, 2 ** 32 + 5, 2 ** 63, 10 ** 30):
+        assert torch.equal(fg.attention(q, cache, table, n, window=window), want)
+    assert not torch.equal(fg.attention(q, cache, table, n, window=5), want)
+    for window in (-1, -2 ** 31, -2 ** 32 + 5, -10 ** 30):
+        with pytest.raises(fg.Fp32GemmError):
+            fg.attention(q, cache, table, n, window=window)
+    with pytest.raises(ValueError):
+        fg.attention(q, cache, table, n, window=4.5)
