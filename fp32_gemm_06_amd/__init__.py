@@ -772,6 +772,8 @@ def _heads(t, name, dtype, shape=None):
     if t.device.type != "cuda":
         raise ValueError(f"{name} must be a GPU tensor")
     T, H, D = t.shape
+    if T >= 1 << 31:
+        raise ValueError(f"{name} has 2^31 tokens or more")
     if not t.numel():
         return max(1, H * D)
     if (D > 1 and t.stride(2) != 1) or (H > 1 and t.stride(1) != D):
@@ -779,7 +781,7 @@ def _heads(t, name, dtype, shape=None):
     ld = t.stride(0) if T > 1 else H * D
     if ld < H * D:
         raise ValueError(f"{name}'s tokens must not overlap")
-    return ld
+    return min(ld, 0x7fffffff)  # what passes 32 bits is refused, not cut to them
 
 
 def _style(style):
@@ -971,7 +973,7 @@ def attention(q, cache, table, lengths, scale=None, window=0, out=None, lse=None
     ldq = _heads(q, "q", q.dtype, (B, Hq, cache.dim))
     if table.dtype != torch.int32 or table.dim() != 2 or table.shape[0] != B:
         raise ValueError("table must be an int32 matrix with a row for each sequence")
-    ldt = table.shape[1]
+    ldt = min(table.shape[1], 0x7fffffff)  # as in _heads
     if not table.is_contiguous():
         raise ValueError("table must be contiguous")
     if table.device.type != "cuda":

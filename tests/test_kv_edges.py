@@ -202,3 +202,33 @@ def test_a_window_of_any_size():
             fg.attention(q, cache, table, n, window=window)
     with pytest.raises(ValueError):
         fg.attention(q, cache, table, n, window=4.5)
+
+
+@gpu
+def test_strides_and_tables_past_32_bits_are_refused():
+    """Not taken for what their low 32 bits say."""
+    require_gpu()
+    dev = "cuda"
+    far = torch.empty(2 ** 32 + 256, dtype=torch.float16, device=dev).as_strided((2, 1, 64), (2 ** 32 + 64, 64, 1))
+    far.zero_()
+    near = torch.zeros(2, 1, 64, dtype=torch.float16, device=dev)
+    slots = torch.arange(2, dtype=torch.int32, device=dev)
+    cache = fg.KVCache.empty(2, 16, 1, 64, torch.float16)
+    table, n = torch.zeros(2, 2, dtype=torch.int32, device=dev), torch.ones(2, dtype=torch.int32, device=dev)
+    calls = [lambda x: fg.norm_rope(x, None), lambda x: fg.norm_rope(near, x), lambda x: fg.norm_rope(near, None, out_q=x),
+             lambda x: fg.cache_write(cache, x, near, slots), lambda x: fg.cache_write(cache, near, x, slots),
+             lambda x: fg.rope_write(cache, x, near, near, slots), lambda x: fg.cache_read(cache, slots, out_k=x),
+             lambda x: fg.attention(x, cache, table, n), lambda x: fg.attention(near, cache, table, n, out=x)]
+    for call in calls:
+        call(near)
+        with pytest.raises(fg.Fp32GemmError):
+            call(far)
+    for call in (calls[0], calls[3], calls[7]):    # whose number of tokens is this operand's
+        with pytest.raises(ValueError, match="2\\^31 tokens"):
+            call(near[:1].expand(2 ** 32 + 2, 1, 64))
+    del far
+    wide = torch.empty(1, 2 ** 32 + 2, dtype=torch.int32, device=dev)
+    wide[:, :2] = 0
+    fg.attention(near[:1], cache, wide[:, :2].contiguous(), n[:1])
+    with pytest.raises(fg.Fp32GemmError):
+        fg.attention(near[:1], cache, wide, n[:1])
