@@ -44,12 +44,12 @@
 // hold does no harm.
 //
 // Long calls are bound by reading K and V once (counted: 1.01 times their bytes):
-// 64 ragged sequences up to 8192 tokens, 32 heads on 8 of 128, codes 82 us (5.5
-// TB/s; matrix cores and vector units each below a third), bf16 143 us (6.1 TB/s;
-// a kernel that only reads such pages 6.3-6.7).  Few rows are bound by latency:
-// one sequence of 4096 on codes 10.9 us, of which planning .8, the first bytes 2.2,
-// the tile 2.3, the waves' join and the stores 1.3, the counter .4, the join of
-// 16 parts 1.9 and the launch the rest.
+// 64 ragged sequences up to 8192 tokens, 32 heads on 8 of 128, codes 82.4 us (5.5
+// TB/s; vector units half of the cycles busy, matrix cores an eighth), bf16 142 us
+// (6.2 TB/s; a kernel that only reads such pages 6.3-6.7).  Few rows are bound by
+// latency: one sequence of 4096 on codes 11.3 us; when it was 10.9, with a digit
+// less, planning took .8, the first bytes 2.2, the tile 2.3, the waves' join and
+// the stores 1.3, the counter .4, the join of 16 parts 1.9 and the launch the rest.
 #pragma once
 
 #include "kv_common.h"
@@ -516,8 +516,14 @@ __global__ void __launch_bounds__(256, DP > 128 ? 1 : 2) attend_kernel(AttendArg
 
   // A tile's keys are asked for when the one before has given its scores, its
   // values when the one before is added up: one tile's bytes are always on the
-  // way while a wave computes, in the place that it has just read.  A head's
-  // query and first tile are asked for before the head in front of it is joined.
+  // way while a wave computes, in the place that it has just read.  (Without
+  // B16 the next tile's table entries are asked for behind V and needed for its
+  // keys, so V has landed by then: 64 ragged to 8192 on codes, pages of 24 instead
+  // of 64, 83.4 -> 92.9 us.)  A head's
+  // query and first tile are asked for before the head in front of it is joined;
+  // so far the compiler also waits for them there (the query is masked behind
+  // the branch around the tile's loads, and the join's first barrier waits for
+  // what goes into LDS), so a change of head costs a trip to memory.
   Rows at;
   int t0, tend;
   auto begin = [&](const Segment &sg, auto first) {

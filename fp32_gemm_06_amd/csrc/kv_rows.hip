@@ -20,11 +20,11 @@
 // needs no other lane, and sines, cosines and weights stay in registers from
 // row to row.  No wave waits for another.
 //
-// Bound by memory, with the 64-bit arithmetic close behind it (vector units 67%
-// busy): 8192 tokens of 32 + 8 heads of 128 bf16 take 37.7 us, 4.4 TB/s of the
+// Bound by memory, with the 64-bit arithmetic close behind it (vector units 82%
+// busy): 8192 tokens of 32 + 8 heads of 128 bf16 take 38.6 us, 4.4 TB/s of the
 // 5.1 that a large copy reaches (61 us with a row a wave, which computed each
-// token's sines for every row); with the cache in codes 45-49 us.  Few rows are
-// bound by the launch and one trip to memory: one token 3.4 us.
+// token's sines for every row); with the cache in codes 48-53 us, in bf16 46.
+// Few rows are bound by the launch and one trip to memory: one token 3.5 us.
 #include <initializer_list>
 
 #include "kv_common.h"
@@ -438,7 +438,7 @@ template <class T> hipError_t launch_type(const KvRowArgs &all, hipStream_t s) {
 
 // Rows of the cache as floats: L lanes a row, eight values a lane, which is 16
 // bytes of 16-bit outputs and 8 of codes.  Bound by memory: 8192 tokens of 2 x 8
-// heads of 128, codes to bf16, 11.2 us (4.6 TB/s).
+// heads of 128, codes to bf16, 11.0 us (4.6 TB/s).
 template <class T, int L, bool CODES> __global__ void __launch_bounds__(NT) kv_read_kernel(KvReadArgs a) {
   const int heads = a.cache.heads, D = a.cache.dim;
   // eight values of 16 bits in a run, or twice four of 32, so that stores lie next to each other
